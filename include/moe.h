@@ -105,7 +105,7 @@ typedef enum {
     MOE_ERR_UNSUPPORTED = 2, /* valid but unsupported shape or dtype */
     MOE_ERR_CUDA = 3,        /* a CUDA call or kernel launch failed */
     MOE_ERR_TIMEOUT = 4,     /* device: a bounded wait ran out */
-    MOE_ERR_NONFINITE = 5    /* device: a router logit was NaN or infinite */
+    MOE_ERR_NONFINITE = 5    /* device: a router logit or a gradient norm was NaN or infinite */
 } moe_status;
 
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
@@ -360,6 +360,86 @@ MOE_API moe_status moe_route_noalloc(const moe_shape* s, const void* x, const vo
                                      int compute_logits, int32_t* idx, float* w,
                                      int32_t* counts, int32_t* offsets, int32_t* pos,
                                      int32_t* perm, int32_t* dev_status, moe_stream_t stream);
+
+/* ---- the whole layer for a few tokens ------------------------------------------
+ *
+ * A decode step calls the layer with one token per sequence: A1, A2, the
+ * dispatch, A5 and A6 on at most MOE_FEW_MAX_TOKENS tokens, in two launches.
+ * Then the weights of the chosen experts are nearly all there is to move, and
+ * every one of them is read once per call.  Source: a trained layer's forward
+ * ("ES-MoE", review, section 3); no backward, no dropped token, no dispatch
+ * mask, as everywhere in this library. */
+#define MOE_FEW_MAX_TOKENS 64
+
+/* The layer's parameters (device pointers, as in moe_route and
+ * moe_expert_ffn_fwd): Wg [E,d], W1 [E,f,d], W2 [E,d,f] in the shape's dtype;
+ * logit_bias [E] fp32, b1 [E,f], b2 [E,d] dtype, each of the three or NULL. */
+typedef struct {
+    const void* Wg;
+    const float* logit_bias;
+    const void* W1;
+    const void* b1;
+    const void* W2;
+    const void* b2;
+} moe_layer_params;
+
+/* Bytes of device workspace of moe_layer_few for this shape (0 when the shape
+ * is invalid or has more than MOE_FEW_MAX_TOKENS tokens).  A call with fewer
+ * tokens and otherwise the same shape needs no more. */
+MOE_API size_t moe_layer_few_workspace_size(const moe_shape* s);
+
+/* y[t] = residual[t] + sum_j w[t,j] (W2[e] GELU(W1[e] x[t] + b1[e]) + b2[e]),
+ * e = idx[t,j], with idx and w of moe_route's gate over the same logits
+ * formula (the logits are summed in another order, so that two of them closer
+ * than fp32 rounding may change places between the two entry points).
+ *   s         0 <= T <= MOE_FEW_MAX_TOKENS (more: MOE_ERR_UNSUPPORTED);
+ *             d % 8 == 0, f % 8 == 0 in both dtypes
+ *   x         [T,d] dtype
+ *   residual  [T,d] dtype or NULL (none); may be x
+ *   y         [T,d] dtype, out; may be residual, must not overlap x
+ *   ws        workspace (contents need no initialisation, garbage after)
+ *   dev_status  MOE_ERR_NONFINITE on a NaN or infinite logit (the experts then
+ *             chosen are in range, y is unspecified), MOE_ERR_TIMEOUT
+ * Hidden activations and the sums over slots are held to more than bf16's
+ * precision in both dtypes; y is rounded once.  Deterministic: the same inputs
+ * give the same bits.  Can be captured in a CUDA graph. */
+MOE_API moe_status moe_layer_few(const moe_shape* s, const moe_layer_params* p, const void* x,
+                                 const void* residual, void* y, void* ws, int32_t* dev_status,
+                                 moe_stream_t stream);
+
+/* ---- gradient norm and clipping ----------------------------------------------------
+ *
+ * The end of a training step ("ES-MoE", review, section 3: each expert's
+ * gradients feed one optimizer step): the gradients of every parameter read as
+ * one vector.  These two calls take tensors of any length and any element
+ * alignment (views of one flat buffer included). */
+typedef struct {
+    const void* grad;  /* device, n elements, contiguous, aligned to its elements */
+    void* out;         /* moe_grad_clip: the scaled gradient, same dtype; may be
+                          grad or NULL (in place), must otherwise not overlap any
+                          tensor of the list */
+    int64_t n;         /* elements, >= 0 (0: pointers are not looked at) */
+    int32_t dtype;     /* moe_dtype */
+} moe_grad;
+
+/* Bytes of device workspace of the two calls below for a list of n tensors (0
+ * for n < 0). */
+MOE_API size_t moe_grad_workspace_size(int n);
+
+/* norm[0] = sqrt(sum over the list of the squares of all elements), fp32.
+ *   n, g  HOST array of n >= 0 tensors (copied before the call returns)
+ *   norm  [1] fp32, out
+ * Sums are held in 64 bits, and squares beyond fp32's range are scaled: the
+ * norm is as good for gradients of 1e-30 or 1e30.  An infinite or NaN norm
+ * sets *dev_status to MOE_ERR_NONFINITE.  Deterministic for a given list. */
+MOE_API moe_status moe_grad_norm(int n, const moe_grad* g, float* norm, void* ws,
+                                 int32_t* dev_status, moe_stream_t stream);
+
+/* The norm as above, and out = grad * (max_norm / norm) if norm > max_norm, else
+ * out = grad (with an infinite or NaN norm too).  max_norm >= 0 (infinity never
+ * clips).  A tensor must not be in the list twice. */
+MOE_API moe_status moe_grad_clip(int n, const moe_grad* g, float max_norm, float* norm, void* ws,
+                                 int32_t* dev_status, moe_stream_t stream);
 
 /* Diagnostics: launch one kernel that waits on a device flag that nothing
  * sets, with the library's bounded wait (limit_ns nanoseconds), then writes

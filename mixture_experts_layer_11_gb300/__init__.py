@@ -6,4 +6,4 @@ point names and ``layer`` composes them into one forward + backward pass.
 Importing this package loads nothing native; the first call into ``ops``
 loads the library and raises if it has not been built.
 """
-__all__ = ["synth", "ops", "layer"]
+__all__ = ["synth", "ops", "layer", "decode", "grads"]

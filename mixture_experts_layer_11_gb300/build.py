@@ -19,7 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
-SOURCES = ["moe_api.cu", "route.cu", "dispatch.cu", "gemm_simt.cu", "gemm_tc.cu"]
+SOURCES = ["moe_api.cu", "route.cu", "dispatch.cu", "gemm_simt.cu", "gemm_tc.cu",
+           "few.cu", "grads.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"),
            os.path.join(ROOT, "include", "moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -151,6 +151,17 @@ cudaError_t launch_gemm_vark_tc(const GemmVarK& g, int32_t* status, cudaStream_t
 cudaError_t launch_gemm_varm_simt(const GemmVarM& g, cudaStream_t st);
 cudaError_t launch_gemm_vark_simt(const GemmVarK& g, cudaStream_t st);
 
+// The whole layer for a few tokens; workspace bytes
+cudaError_t launch_layer_few(const moe_shape& s, const moe_layer_params& p, const void* x,
+                             const void* residual, void* y, void* ws, int32_t* status,
+                             cudaStream_t st);
+size_t few_workspace(const moe_shape& s);
+
+// Norm of the n gradients g (and, with clip, their scaled copies)
+cudaError_t launch_grad_norm(int n, const moe_grad* g, bool clip, float max_norm, float* norm,
+                             void* ws, int32_t* status, cudaStream_t st);
+size_t grad_workspace(int n);
+
 // Diagnostics
 cudaError_t launch_bounded_wait(uint64_t limit_ns, int32_t* status, cudaStream_t st);
 cudaError_t launch_debug_gelu(int64_t n, const float* x, float* g, float* gd, int fast,

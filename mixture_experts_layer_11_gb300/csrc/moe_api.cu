@@ -116,7 +116,7 @@ const char* moe_status_string(moe_status s) {
         case MOE_ERR_UNSUPPORTED: return "MOE_ERR_UNSUPPORTED: unsupported shape or dtype";
         case MOE_ERR_CUDA: return "MOE_ERR_CUDA: CUDA call or launch failed";
         case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT: a bounded device wait ran out";
-        case MOE_ERR_NONFINITE: return "MOE_ERR_NONFINITE: non-finite router logit";
+        case MOE_ERR_NONFINITE: return "MOE_ERR_NONFINITE: non-finite router logit or gradient norm";
     }
     return "unknown moe_status";
 }
@@ -626,6 +626,68 @@ moe_status moe_route_noalloc(const moe_shape* s, const void* x, const void* Wg,
     if (e == cudaSuccess) e = launch_dispatch_scan(*s, block_counts, counts, offsets, st);
     if (e == cudaSuccess && s->T > 0) e = launch_dispatch_rank(*s, idx, block_counts, pos, perm, st);
     return cuda_status(e);
+}
+
+size_t moe_layer_few_workspace_size(const moe_shape* s) {
+    if (check_shape(s) != MOE_OK || s->T > MOE_FEW_MAX_TOKENS) return 0;
+    return few_workspace(*s);
+}
+
+moe_status moe_layer_few(const moe_shape* s, const moe_layer_params* p, const void* x,
+                         const void* residual, void* y, void* ws, int32_t* dev_status,
+                         moe_stream_t stream) {
+    moe_status r = check_shape(s);
+    if (r != MOE_OK) return r;
+    if (s->T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    if (s->T == 0) return MOE_OK;
+    if (p == nullptr || !ok_ptr(p->Wg) || !ok_opt(p->logit_bias) || !ok_ptr(p->W1) ||
+        !ok_opt(p->b1) || !ok_ptr(p->W2) || !ok_opt(p->b2) || !ok_ptr(x) || !ok_opt(residual) ||
+        !ok_ptr(y) || !ok_ptr(ws) || !ok_status(dev_status))
+        return MOE_ERR_INVALID;
+    return cuda_status(launch_layer_few(*s, *p, x, residual, y, ws, dev_status,
+                                        (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+moe_status check_grads(int n, const moe_grad* g, const float* norm, const void* ws,
+                       const int32_t* dev_status) {
+    if (n < 0 || (n > 0 && g == nullptr) || norm == nullptr ||
+        (reinterpret_cast<uintptr_t>(norm) & 3u) || !ok_ptr(ws) || !ok_status(dev_status))
+        return MOE_ERR_INVALID;
+    for (int i = 0; i < n; ++i) {
+        if (g[i].n < 0 || (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16)) return MOE_ERR_INVALID;
+        if (g[i].n == 0) continue;
+        const uintptr_t mask = g[i].dtype == MOE_BF16 ? 1u : 3u;
+        if (g[i].grad == nullptr || ((uintptr_t)g[i].grad & mask) || ((uintptr_t)g[i].out & mask))
+            return MOE_ERR_INVALID;
+    }
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_grad_workspace_size(int n) { return n < 0 ? 0 : align_up(grad_workspace(n)); }
+
+moe_status moe_grad_norm(int n, const moe_grad* g, float* norm, void* ws, int32_t* dev_status,
+                         moe_stream_t stream) {
+    moe_status r = check_grads(n, g, norm, ws, dev_status);
+    if (r != MOE_OK) return r;
+    return cuda_status(launch_grad_norm(n, g, false, 0.f, norm, ws, dev_status,
+                                        (cudaStream_t)stream));
+}
+
+moe_status moe_grad_clip(int n, const moe_grad* g, float max_norm, float* norm, void* ws,
+                         int32_t* dev_status, moe_stream_t stream) {
+    moe_status r = check_grads(n, g, norm, ws, dev_status);
+    if (r != MOE_OK) return r;
+    if (!(max_norm >= 0.f)) return MOE_ERR_INVALID;
+    return cuda_status(launch_grad_norm(n, g, true, max_norm, norm, ws, dev_status,
+                                        (cudaStream_t)stream));
 }
 
 moe_status moe_debug_bounded_wait(uint64_t limit_ns, int32_t* dev_status, moe_stream_t stream) {

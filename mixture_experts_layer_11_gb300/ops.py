@@ -27,7 +27,9 @@ ENTRY_POINTS = ("moe_status_string", "moe_workspace_size", "moe_route", "moe_per
                 "moe_debug_gelu", "moe_route_noalloc", "moe_expert_ffn_bwd_data",
                 "moe_expert_ffn_bwd_weights", "moe_expert_ffn_fwd_gather",
                 "moe_expert_ffn_bwd_weights_gather", "moe_set_gemm_max_units",
-                "moe_expert_ffn_bwd_weights_workspace_size")
+                "moe_expert_ffn_bwd_weights_workspace_size", "moe_layer_few",
+                "moe_layer_few_workspace_size", "moe_grad_norm", "moe_grad_clip",
+                "moe_grad_workspace_size")
 
 
 class MoEError(RuntimeError):
@@ -40,6 +42,15 @@ class moe_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("f", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("renorm", ctypes.c_int32)]
+
+
+class moe_layer_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("Wg", "logit_bias", "W1", "b1", "W2", "b2")]
+
+
+class moe_grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 def make_shape(T: int, d: int, f: int, E: int, k: int, dtype, renorm: int) -> moe_shape:
@@ -102,6 +113,14 @@ def lib() -> ctypes.CDLL:
             L.moe_expert_ffn_bwd_weights_workspace_size.restype = ctypes.c_size_t
             L.moe_expert_ffn_bwd_weights_workspace_size.argtypes = [
                 _SP, ctypes.c_int, ctypes.POINTER(ctypes.c_int64)]
+            L.moe_layer_few.argtypes = [_SP, ctypes.POINTER(moe_layer_params)] + [_P] * 6
+            L.moe_layer_few_workspace_size.restype = ctypes.c_size_t
+            L.moe_layer_few_workspace_size.argtypes = [_SP]
+            L.moe_grad_workspace_size.restype = ctypes.c_size_t
+            L.moe_grad_workspace_size.argtypes = [ctypes.c_int]
+            L.moe_grad_norm.argtypes = [ctypes.c_int, ctypes.POINTER(moe_grad)] + [_P] * 4
+            L.moe_grad_clip.argtypes = [ctypes.c_int, ctypes.POINTER(moe_grad),
+                                        ctypes.c_float] + [_P] * 4
             for fn in ENTRY_POINTS[2:]:
                 if not fn.endswith("_workspace_size"):
                     getattr(L, fn).restype = ctypes.c_int
@@ -306,3 +325,62 @@ def moe_route_noalloc(s, x, Wg, logit_bias, logits, compute_logits, idx, w, coun
         _ptr(logits, _F32), int(compute_logits), _ptr(idx, _I32), _ptr(w, _F32),
         _ptr(counts, _I32), _ptr(offsets, _I32), _ptr(pos, _I32), _ptr(perm, _I32),
         _ptr(dev_status, _I32), _stream(stream)))
+
+
+FEW_MAX_TOKENS = 64  # MOE_FEW_MAX_TOKENS in include/moe.h
+
+
+def make_layer_params(s, Wg, logit_bias, W1, b1, W2, b2) -> moe_layer_params:
+    """The parameter struct of moe_layer_few.  It holds addresses only: keep the
+    tensors alive while it is used."""
+    act = _act(s)
+    return moe_layer_params(_ptr(Wg, act), _ptr(logit_bias, _F32), _ptr(W1, act), _ptr(b1, act),
+                            _ptr(W2, act), _ptr(b2, act))
+
+
+def moe_layer_few_workspace_size(s: moe_shape) -> int:
+    return int(lib().moe_layer_few_workspace_size(ctypes.byref(s)))
+
+
+def moe_layer_few(s, params: moe_layer_params, x, residual, y, ws, dev_status, stream=None):
+    _check("moe_layer_few", lib().moe_layer_few(
+        ctypes.byref(s), ctypes.byref(params), _ptr(x, _act(s)), _ptr(residual, _act(s)),
+        _ptr(y, _act(s)), _ptr(ws), _ptr(dev_status, _I32), _stream(stream)))
+
+
+def make_grads(tensors, outs=None):
+    """A list of gradients as moe_grad_norm / moe_grad_clip take it: a ctypes
+    array of moe_grad (a fresh one for other tensors; it holds addresses only:
+    keep the tensors alive while it is used).  tensors: CUDA tensors, contiguous,
+    fp32 or bf16, any sizes; outs: a tensor or None (in place) for each."""
+    fn = "make_grads"
+    tensors = list(tensors)
+    outs = [None] * len(tensors) if outs is None else list(outs)
+    if len(outs) != len(tensors):
+        raise MoEError(fn, MOE_ERR_INVALID, f"{len(outs)} outs for {len(tensors)} gradients")
+    arr = (moe_grad * len(tensors))()
+    for a, t, o in zip(arr, tensors, outs):
+        if t.dtype not in (torch.float32, torch.bfloat16):
+            raise MoEError(fn, MOE_ERR_INVALID, f"gradient dtype {t.dtype}")
+        if o is not None and o.numel() != t.numel():
+            raise MoEError(fn, MOE_ERR_INVALID, "an out of another size than its gradient")
+        a.grad, a.out, a.n = _ptr(t), _ptr(o, t.dtype), t.numel()
+        a.dtype = MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
+    return arr
+
+
+def moe_grad_workspace_size(n: int) -> int:
+    return int(lib().moe_grad_workspace_size(int(n)))
+
+
+def moe_grad_norm(grads, norm, ws, dev_status, stream=None):
+    """grads: from make_grads."""
+    _check("moe_grad_norm", lib().moe_grad_norm(
+        len(grads), grads, _ptr(norm, _F32), _ptr(ws), _ptr(dev_status, _I32), _stream(stream)))
+
+
+def moe_grad_clip(grads, max_norm: float, norm, ws, dev_status, stream=None):
+    """grads: from make_grads."""
+    _check("moe_grad_clip", lib().moe_grad_clip(
+        len(grads), grads, float(max_norm), _ptr(norm, _F32), _ptr(ws), _ptr(dev_status, _I32),
+        _stream(stream)))
