@@ -155,6 +155,7 @@ cudaError_t launch_gemm_vark_simt(const GemmVarK& g, cudaStream_t st);
 cudaError_t launch_layer_few(const moe_shape& s, const moe_layer_params& p, const void* x,
                              const void* residual, void* y, void* ws, int32_t* status,
                              cudaStream_t st);
+bool few_supported(const moe_shape& s);   // sizes its 32-bit counts of K blocks can hold
 size_t few_workspace(const moe_shape& s);
 
 // Norm of the n gradients g (and, with clip, their scaled copies)

@@ -629,7 +629,7 @@ moe_status moe_route_noalloc(const moe_shape* s, const void* x, const void* Wg,
 }
 
 size_t moe_layer_few_workspace_size(const moe_shape* s) {
-    if (check_shape(s) != MOE_OK || s->T > MOE_FEW_MAX_TOKENS) return 0;
+    if (check_shape(s) != MOE_OK || s->T > MOE_FEW_MAX_TOKENS || !few_supported(*s)) return 0;
     return few_workspace(*s);
 }
 
@@ -638,7 +638,7 @@ moe_status moe_layer_few(const moe_shape* s, const moe_layer_params* p, const vo
                          moe_stream_t stream) {
     moe_status r = check_shape(s);
     if (r != MOE_OK) return r;
-    if (s->T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    if (s->T > MOE_FEW_MAX_TOKENS || !few_supported(*s)) return MOE_ERR_UNSUPPORTED;
     if (s->T == 0) return MOE_OK;
     if (p == nullptr || !ok_ptr(p->Wg) || !ok_opt(p->logit_bias) || !ok_ptr(p->W1) ||
         !ok_opt(p->b1) || !ok_ptr(p->W2) || !ok_opt(p->b2) || !ok_ptr(x) || !ok_opt(residual) ||

@@ -35,7 +35,8 @@ def test_few_refuses_invalid_shapes(lib, bad):
     assert ops.moe_layer_few_workspace_size(_shape(**bad)) == 0
 
 
-@pytest.mark.parametrize("bad", [dict(T=65), dict(d=12), dict(f=12), dict(d=260, dtype="f32")])
+@pytest.mark.parametrize("bad", [dict(T=65), dict(d=12), dict(f=12), dict(d=260, dtype="f32"),
+                                 dict(T=64, E=256, k=16, d=1 << 17, f=1 << 17, dtype="f32")])
 def test_few_refuses_unsupported_shapes(lib, bad):
     assert _few(lib, _shape(**bad)) == ops.MOE_ERR_UNSUPPORTED
 
