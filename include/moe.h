@@ -427,7 +427,8 @@ typedef struct {
 MOE_API size_t moe_grad_workspace_size(int n);
 
 /* norm[0] = sqrt(sum over the list of the squares of all elements), fp32.
- *   n, g  HOST array of n >= 0 tensors (copied before the call returns)
+ *   n, g  HOST array of n >= 0 tensors (copied before the call returns); more
+ *         than 2^45 bytes in all are MOE_ERR_UNSUPPORTED
  *   norm  [1] fp32, out
  * Sums are held in 64 bits, and squares beyond fp32's range are scaled: the
  * norm is as good for gradients of 1e-30 or 1e30.  An infinite or NaN norm

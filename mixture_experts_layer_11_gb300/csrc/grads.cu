@@ -5,6 +5,7 @@
 // Two passes over the list, one launch each (per kGradTable tensors): sums of
 // squares, one partial per block; then every block adds the partials (in index
 // order, so the norm does not depend on timing) and scales its chunks.
+#include <limits.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -14,21 +15,22 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kGradThreads = 512;
-constexpr int kGradChunk = 16384;      // elements of one unit of work
-constexpr int kGradTable = 128;        // tensors one launch takes
-constexpr int kGradBlocksPerSm = 4;    // 2048 threads
+constexpr int kGradThreads = 256;
+constexpr int kGradBlocksPerSm = 4;    // at 64 registers: 128 KB of loads in flight an SM
+constexpr int kGradVecs = 8;           // 16-byte vectors a thread has in flight
+constexpr int kChunkBytes = kGradThreads * kGradVecs * 16;   // one unit of work
 
 // The tensors of one launch, in its parameters.  Tensor i's chunks are
-// [first[i], first[i+1]).  Its chunk boundaries lie kGradChunk elements apart
-// counted from the 16-byte boundary at or before the source, so that every
-// chunk but the first starts aligned wherever the tensor starts.
-struct GradTable {
-    const void* src[kGradTable];
-    void* dst[kGradTable];
-    int64_t n[kGradTable];
-    int64_t first[kGradTable + 1];
-    uint8_t bf16[kGradTable];
+// [first[i], first[i+1]); a list has at most kGradMostBytes, far fewer than 2^31
+// chunks.  Its chunk boundaries lie kChunkBytes apart counted
+// from the 16-byte boundary at or before the source, so that every chunk but
+// the first starts aligned wherever the tensor starts.
+template <int CAP> struct GradTable {
+    const void* src[CAP];
+    void* dst[CAP];
+    int64_t n[CAP];
+    int32_t first[CAP + 1];
+    uint8_t bf16[CAP];
     int count;
 };
 
@@ -39,50 +41,65 @@ struct Chunk {
     bool bf16;
 };
 
-__device__ __forceinline__ Chunk find_chunk(const GradTable& t, int64_t c) {
+// Chunk c, which tensor i holds.
+template <int CAP> __device__ __forceinline__ Chunk chunk_of(const GradTable<CAP>& t, int i, int c) {
+    const int shift = t.bf16[i] ? 1 : 2;
+    const int skew = (int)(reinterpret_cast<uintptr_t>(t.src[i]) & 15) >> shift;
+    int64_t a = ((int64_t)(c - t.first[i]) * kChunkBytes >> shift) - skew;
+    int64_t b = a + (kChunkBytes >> shift);
+    if (a < 0) a = 0;
+    if (b > t.n[i]) b = t.n[i];
+    return {(const uint8_t*)t.src[i] + (a << shift), (uint8_t*)t.dst[i] + (a << shift), (int)(b - a),
+            t.bf16[i] != 0};
+}
+
+template <int CAP> __device__ __forceinline__ int find_tensor(const GradTable<CAP>& t, int c) {
     int lo = 0, hi = t.count;
     while (hi - lo > 1) {
         const int m = (lo + hi) >> 1;
         if (t.first[m] <= c) lo = m; else hi = m;
     }
-    const int es = t.bf16[lo] ? 2 : 4;
-    const int skew = (int)((reinterpret_cast<uintptr_t>(t.src[lo]) & 15) / es);
-    int64_t a = (c - t.first[lo]) * kGradChunk - skew, b = a + kGradChunk;
-    if (a < 0) a = 0;
-    if (b > t.n[lo]) b = t.n[lo];
-    return {(const uint8_t*)t.src[lo] + a * es, (uint8_t*)t.dst[lo] + a * es, (int)(b - a),
-            t.bf16[lo] != 0};
+    return lo;
+}
+
+// A block's consecutive chunks [begin, end).
+template <int CAP>
+__device__ __forceinline__ void my_chunks(const GradTable<CAP>& t, int& begin, int& end) {
+    const int chunks = t.first[t.count];
+    begin = (int)((int64_t)chunks * blockIdx.x / gridDim.x);
+    end = (int)((int64_t)chunks * (blockIdx.x + 1) / gridDim.x);
 }
 
 // Sum of squares over the whole range of fp32 inputs: values whose squares
-// leave fp32's range are scaled by a power of two first and kept in sums of
-// their own.  A group of values goes by its largest magnitude: what the others
-// lose then is below 2^-40 of that value's square.
+// leave fp32's range are scaled by a power of two first and go to 64 bits.  Four
+// values go by their largest magnitude: what the others lose then is below 2^-40
+// of that value's square.  The common sum is kept as an unevaluated
+// pair of fp32 (each chunk's sum added exactly, by the error of an addition being
+// an fp32 number itself), since 64-bit additions run at a small fraction of the
+// rate here.
+__device__ __noinline__ double rare_squares(float a, float b, float c, float d, float scale) {
+    a *= scale; b *= scale; c *= scale; d *= scale;
+    const double s = fmaf(a, a, fmaf(b, b, fmaf(c, c, d * d)));
+    return s * (scale < 1.f ? 0x1p160 : 0x1p-160);
+}
+
 struct SquareSum {
-    float mid = 0.f, low = 0.f, high = 0.f;
-    double total = 0.0;
-    template <int N> __device__ __forceinline__ void add(const float (&v)[N]) {
-        float m = 0.f;
-        #pragma unroll
-        for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));   // NaN: not seen here
-        if (m > 0x1p56f) {
-            #pragma unroll
-            for (int i = 0; i < N; ++i) { const float s = v[i] * 0x1p-80f; high = fmaf(s, s, high); }
-        } else if (m < 0x1p-40f && m > 0.f) {
-            #pragma unroll
-            for (int i = 0; i < N; ++i) { const float s = v[i] * 0x1p80f; low = fmaf(s, s, low); }
-        } else {
-            #pragma unroll
-            for (int i = 0; i < N; ++i) mid = fmaf(v[i], v[i], mid);
-        }
+    float high = 0.f, low = 0.f;
+    double rare = 0.0;
+    __device__ __forceinline__ void add(float a, float b, float c, float d, float& sum) {
+        const float m = fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d)));   // no NaN
+        if (m <= 0x1p40f && (m >= 0x1p-40f || m == 0.f))
+            sum = fmaf(a, a, fmaf(b, b, fmaf(c, c, fmaf(d, d, sum))));
+        else
+            rare += rare_squares(a, b, c, d, m > 1.f ? 0x1p-80f : 0x1p80f);
     }
-    // into 64 bits, after each chunk (at most 48 values a thread)
-    __device__ __forceinline__ void flush() {
-        total += (double)mid;
-        if (low != 0.f) total += (double)low * 0x1p-160;
-        if (high != 0.f) total += (double)high * 0x1p160;
-        mid = low = high = 0.f;
+    // the sum of one chunk's squares (at most 72 a thread)
+    __device__ __forceinline__ void flush(float sum) {
+        const float s = __fadd_rn(high, sum), b = __fsub_rn(s, high);
+        low = __fadd_rn(low, __fadd_rn(__fsub_rn(high, __fsub_rn(s, b)), __fsub_rn(sum, b)));
+        high = s;
     }
+    __device__ __forceinline__ double total() const { return (double)high + (double)low + rare; }
 };
 
 template <typename T> struct Vec;   // 16 bytes of T as floats
@@ -131,31 +148,26 @@ __device__ __forceinline__ void square_chunk(const Chunk& c, SquareSum& sum) {
     const int head = head_of<T>(p, c.n);
     const int nv = (c.n - head) / N;
     const uint4* q = (const uint4*)(p + head);
-    constexpr int U = kGradChunk / N / kGradThreads;   // vectors a thread of a full chunk
-    if (nv == U * kGradThreads) {
-        uint4 u[U];
-        #pragma unroll
-        for (int i = 0; i < U; ++i) u[i] = __ldg(q + threadIdx.x + i * kGradThreads);
-        #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            float v[N];
-            Vec<T>::unpack(u[i], v);
-            sum.add(v);
-        }
-    } else {
-        for (int i = threadIdx.x; i < nv; i += kGradThreads) {
-            float v[N];
-            Vec<T>::unpack(__ldg(q + i), v);
-            sum.add(v);
-        }
+    float s = 0.f;
+    uint4 u[kGradVecs];
+    #pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int j = threadIdx.x + i * kGradThreads;
+        u[i] = j < nv ? __ldg(q + j) : make_uint4(0u, 0u, 0u, 0u);
     }
     const int rest = c.n - nv * N;   // head and tail, fewer than 2 N
     if ((int)threadIdx.x < rest) {
         const int i = (int)threadIdx.x < head ? (int)threadIdx.x : nv * N + (int)threadIdx.x;
-        const float v[1] = {to_f32<T>(p[i])};
-        sum.add(v);
+        sum.add(to_f32<T>(p[i]), 0.f, 0.f, 0.f, s);
     }
-    sum.flush();
+    #pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        float v[N];
+        Vec<T>::unpack(u[i], v);
+        #pragma unroll
+        for (int j = 0; j < N; j += 4) sum.add(v[j], v[j + 1], v[j + 2], v[j + 3], s);
+    }
+    sum.flush(s);
 }
 
 // sum over the block, the same on every thread
@@ -170,17 +182,21 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
     return s;
 }
 
+template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
-    grad_square_kernel(const __grid_constant__ GradTable t, double* __restrict__ partial) {
+    grad_square_kernel(const __grid_constant__ GradTable<CAP> t, double* __restrict__ partial) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ double buf[kGradThreads / 32];
     SquareSum sum;
-    const int64_t chunks = t.first[t.count];
-    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const Chunk k = find_chunk(t, c);
+    int c, end;
+    my_chunks(t, c, end);
+    for (int i = c < end ? find_tensor(t, c) : 0; c < end; ++c) {
+        while (c >= t.first[i + 1]) ++i;
+        const Chunk k = chunk_of(t, i, c);
         if (k.bf16) square_chunk<__nv_bfloat16>(k, sum);
         else square_chunk<float>(k, sum);
     }
-    const double s = block_sum(sum.total, buf);
+    const double s = block_sum(sum.total(), buf);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -188,7 +204,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
 __device__ __forceinline__ float finish_norm(const double* partial, int np, double* buf,
                                              float* norm, int32_t* status, bool writer) {
     double s = 0.0;
-    for (int i = threadIdx.x; i < np; i += kGradThreads) s += partial[i];
+    for (int i = threadIdx.x; i < np; i += kGradThreads) s += __ldcg(partial + i);
     const float n = (float)sqrt(block_sum(s, buf));
     if (writer && threadIdx.x == 0) {
         *norm = n;
@@ -200,6 +216,7 @@ __device__ __forceinline__ float finish_norm(const double* partial, int np, doub
 __global__ void __launch_bounds__(kGradThreads)
     grad_norm_kernel(const double* __restrict__ partial, int np, float* norm, int32_t* status) {
     __shared__ double buf[kGradThreads / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     finish_norm(partial, np, buf, norm, status, true);
 }
 
@@ -216,22 +233,20 @@ template <typename T> __device__ __forceinline__ void scale_chunk(const Chunk& c
     const int nv = (c.n - head) / N;
     const uint4* q = (const uint4*)(p + head);
     uint4* r = (uint4*)(o + head);
-    constexpr int U = kGradChunk / N / kGradThreads;
-    auto scaled = [&](uint4 u) {
+    uint4 u[kGradVecs];
+    #pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int j = threadIdx.x + i * kGradThreads;
+        if (j < nv) u[i] = q[j];
+    }
+    #pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int j = threadIdx.x + i * kGradThreads;
         float v[N];
-        Vec<T>::unpack(u, v);
+        Vec<T>::unpack(u[i], v);
         #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] *= f;
-        return Vec<T>::pack(v);
-    };
-    if (nv == U * kGradThreads) {
-        uint4 u[U];
-        #pragma unroll
-        for (int i = 0; i < U; ++i) u[i] = q[threadIdx.x + i * kGradThreads];
-        #pragma unroll
-        for (int i = 0; i < U; ++i) r[threadIdx.x + i * kGradThreads] = scaled(u[i]);
-    } else {
-        for (int i = threadIdx.x; i < nv; i += kGradThreads) r[i] = scaled(q[i]);
+        for (int n = 0; n < N; ++n) v[n] *= f;
+        if (j < nv) __stcs(r + j, Vec<T>::pack(v));
     }
     const int rest = c.n - nv * N;
     if ((int)threadIdx.x < rest) {
@@ -240,16 +255,23 @@ template <typename T> __device__ __forceinline__ void scale_chunk(const Chunk& c
     }
 }
 
-__global__ void __launch_bounds__(kGradThreads)
-    grad_scale_kernel(const __grid_constant__ GradTable t, const double* __restrict__ partial,
+// A block goes over the chunks that it has the same number of as in
+// grad_square_kernel, last one first: what that read last is still in the L2.
+template <int CAP>
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
+    grad_scale_kernel(const __grid_constant__ GradTable<CAP> t, const double* __restrict__ partial,
                       int np, float max_norm, float* norm, int first_launch, int32_t* status) {
     __shared__ double buf[kGradThreads / 32];
+    int begin, c;
+    my_chunks(t, begin, c);
+    int i = begin < c ? find_tensor(t, c - 1) : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float n = finish_norm(partial, np, buf, norm, status, first_launch && blockIdx.x == 0);
     // a norm within the bound, or none (infinite, NaN): the gradients as they are
     const float f = isfinite(n) && n > max_norm ? max_norm / n : 1.f;
-    const int64_t chunks = t.first[t.count];
-    for (int64_t c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-        const Chunk k = find_chunk(t, c);
+    while (--c >= begin) {
+        while (c < t.first[i]) --i;
+        const Chunk k = chunk_of(t, i, c);
         if (f == 1.f && k.src == k.dst) continue;
         if (k.bf16) scale_chunk<__nv_bfloat16>(k, f);
         else scale_chunk<float>(k, f);
@@ -261,53 +283,78 @@ int grad_blocks(int64_t chunks) {
     return (int)(chunks < most ? (chunks > 0 ? chunks : 1) : most);
 }
 
-// tensors [from, from + kGradTable) of the list
-GradTable make_table(const moe_grad* g, int from, int n) {
-    GradTable t;
-    t.count = n - from < kGradTable ? n - from : kGradTable;
-    int64_t c = 0;
+// Tensors [from, from + CAP) of the list.
+template <int CAP> void make_table(GradTable<CAP>& t, const moe_grad* g, int from, int n) {
+    int32_t c = 0;
+    t.count = n - from < CAP ? n - from : CAP;
     for (int i = 0; i < t.count; ++i) {
         const moe_grad& x = g[from + i];
         const bool half = x.dtype == MOE_BF16;
-        const int64_t skew = (int64_t)((reinterpret_cast<uintptr_t>(x.grad) & 15) / (half ? 2 : 4));
+        const int64_t bytes = x.n * (half ? 2 : 4) + (int64_t)(reinterpret_cast<uintptr_t>(x.grad) & 15);
         t.src[i] = x.grad;
         t.dst[i] = x.out ? x.out : const_cast<void*>(x.grad);
         t.n[i] = x.n;
         t.bf16[i] = half;
         t.first[i] = c;
-        c += x.n ? (x.n + skew + kGradChunk - 1) / kGradChunk : 0;
+        c += x.n ? (int32_t)((bytes + kChunkBytes - 1) / kChunkBytes) : 0;
     }
     t.first[t.count] = c;
-    return t;
+}
+
+// A launch that may begin while the one before it ends.
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*kern)(A...), int blocks, cudaStream_t st, const B&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int CAP>
+cudaError_t launch(int n, const moe_grad* g, bool clip, float max_norm, float* norm, double* partial,
+                   int32_t* status, cudaStream_t st) {
+    GradTable<CAP> t;
+    int np = 0;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n; i += t.count) {
+        make_table(t, g, i, n);
+        const int blocks = grad_blocks(t.first[t.count]);
+        grad_square_kernel<CAP><<<blocks, kGradThreads, 0, st>>>(t, partial + np);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        np += blocks;
+    }
+    if (!clip || n == 0)
+        return launch_after(grad_norm_kernel, 1, st, (const double*)partial, np, norm, status);
+    const bool single = t.count == n;   // the table is still that of the only launch
+    for (int i = 0; i < n && e == cudaSuccess; i += t.count) {
+        if (!single) make_table(t, g, i, n);
+        e = launch_after(grad_scale_kernel<CAP>, grad_blocks(t.first[t.count]), st, t,
+                         (const double*)partial, np, max_norm, norm, (int)(i == 0), status);
+    }
+    return e;
 }
 
 }  // namespace
 
+// Tables of two sizes: launches copy their parameters, 29 KB for the larger.
+constexpr int kSmallTable = 64, kLargeTable = 1000;
+
 size_t grad_workspace(int n) {
-    const int launches = n > 0 ? (n + kGradTable - 1) / kGradTable : 1;
+    const int launches = n > 0 ? (n + kLargeTable - 1) / kLargeTable : 1;
     return (size_t)launches * device_sm_count() * kGradBlocksPerSm * sizeof(double);
 }
 
 cudaError_t launch_grad_norm(int n, const moe_grad* g, bool clip, float max_norm, float* norm,
                              void* ws, int32_t* status, cudaStream_t st) {
     double* partial = (double*)ws;
-    int np = 0;
-    for (int i = 0; i < n; i += kGradTable) {
-        const GradTable t = make_table(g, i, n);
-        const int blocks = grad_blocks(t.first[t.count]);
-        grad_square_kernel<<<blocks, kGradThreads, 0, st>>>(t, partial + np);
-        np += blocks;
-    }
-    if (!clip || n == 0) {
-        grad_norm_kernel<<<1, kGradThreads, 0, st>>>(partial, np, norm, status);
-        return cudaGetLastError();
-    }
-    for (int i = 0; i < n; i += kGradTable) {
-        const GradTable t = make_table(g, i, n);
-        grad_scale_kernel<<<grad_blocks(t.first[t.count]), kGradThreads, 0, st>>>(
-            t, partial, np, max_norm, norm, i == 0, status);
-    }
-    return cudaGetLastError();
+    return n <= kSmallTable ? launch<kSmallTable>(n, g, clip, max_norm, norm, partial, status, st)
+                            : launch<kLargeTable>(n, g, clip, max_norm, norm, partial, status, st);
 }
 
 }  // namespace moe

@@ -162,6 +162,7 @@ size_t few_workspace(const moe_shape& s);
 cudaError_t launch_grad_norm(int n, const moe_grad* g, bool clip, float max_norm, float* norm,
                              void* ws, int32_t* status, cudaStream_t st);
 size_t grad_workspace(int n);
+constexpr int64_t kGradMostBytes = int64_t(1) << 45;   // of a list
 
 // Diagnostics
 cudaError_t launch_bounded_wait(uint64_t limit_ns, int32_t* status, cudaStream_t st);

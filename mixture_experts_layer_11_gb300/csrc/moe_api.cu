@@ -657,12 +657,16 @@ moe_status check_grads(int n, const moe_grad* g, const float* norm, const void* 
     if (n < 0 || (n > 0 && g == nullptr) || norm == nullptr ||
         (reinterpret_cast<uintptr_t>(norm) & 3u) || !ok_ptr(ws) || !ok_status(dev_status))
         return MOE_ERR_INVALID;
+    int64_t bytes = 0;
     for (int i = 0; i < n; ++i) {
         if (g[i].n < 0 || (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16)) return MOE_ERR_INVALID;
         if (g[i].n == 0) continue;
         const uintptr_t mask = g[i].dtype == MOE_BF16 ? 1u : 3u;
         if (g[i].grad == nullptr || ((uintptr_t)g[i].grad & mask) || ((uintptr_t)g[i].out & mask))
             return MOE_ERR_INVALID;
+        if (g[i].n > kGradMostBytes) return MOE_ERR_UNSUPPORTED;
+        bytes += g[i].n * (g[i].dtype == MOE_BF16 ? 2 : 4);
+        if (bytes > kGradMostBytes) return MOE_ERR_UNSUPPORTED;
     }
     return MOE_OK;
 }

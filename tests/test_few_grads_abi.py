@@ -90,6 +90,13 @@ def test_grads_refuse_bad_arguments(lib, fn, bad):
     assert code == ops.MOE_ERR_INVALID
 
 
+def test_grads_refuse_more_than_any_memory(lib):
+    g = _grads((16, None, 1 << 44, 0))
+    assert lib.moe_grad_norm(1, g, 16, 16, 16, None) == ops.MOE_ERR_UNSUPPORTED
+    g = _grads(*[(16, None, 1 << 42, 0)] * 3)
+    assert lib.moe_grad_norm(3, g, 16, 16, 16, None) == ops.MOE_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("bound", [-1.0, float("nan"), -float("inf")])
 def test_clip_refuses_bad_bounds(lib, bound):
     assert lib.moe_grad_clip(1, _grads((16, None, 3, 0)), bound, 16, 16, 16, None) == ops.MOE_ERR_INVALID
