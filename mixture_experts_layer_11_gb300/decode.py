@@ -47,19 +47,26 @@ class FewTokenPass:
         self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
         self.y = torch.empty(T, d, dtype=W1.dtype, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._device = self.y.device.index
+        self._owned = (self.ws.data_ptr(), self.status.data_ptr())
 
     def forward(self, x, residual: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None):
         """x [t,d], t <= T; residual [t,d] or None; returns y [t,d] in ``out``
         (which may be residual) or in a buffer owned by this object."""
-        t = x.shape[0]
-        if t > self.T:
-            raise ValueError(f"{t} tokens, room for {self.T}")
-        shape = x.shape
-        if shape != (t, self.d) or (residual is not None and residual.shape != shape) or (
-                out is not None and out.shape != shape):
-            raise ValueError("x, residual and out must be [t, d]")
-        y = out if out is not None else self.y if t == self.T else self.y[:t]
-        self.shape.T = t
-        ops.moe_layer_few(self.shape, self.params, x, residual, y, self.ws, self.status)
+        size = x.shape
+        y = self.y if out is None else out
+        if size != y.shape:
+            if len(size) != 2 or size[1] != self.d or size[0] > self.T:
+                raise ValueError(f"x is {tuple(size)}, expected [t, {self.d}] with t <= {self.T}")
+            if out is not None:
+                raise ValueError(f"out is {tuple(out.shape)}, expected {tuple(size)}")
+            y = self.y[:size[0]]
+        elif out is not None and (len(size) != 2 or size[1] != self.d or size[0] > self.T):
+            raise ValueError(f"x is {tuple(size)}, expected [t, {self.d}] with t <= {self.T}")
+        if residual is not None and residual.shape != size:
+            raise ValueError(f"residual is {tuple(residual.shape)}, expected {tuple(size)}")
+        self.shape.T = size[0]
+        ops.moe_layer_few(self.shape, self.params, x, residual, y, *self._owned,
+                          stream=ops.raw_stream(self._device))
         return y

@@ -31,16 +31,18 @@ class GradClip:
                               device=dev)
         self.total = torch.zeros((), dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._device = self.total.device.index
+        self._owned = (self.total.data_ptr(), self.ws.data_ptr(), self.status.data_ptr())
 
     def norm(self) -> torch.Tensor:
         """The norm of all gradients (a fp32 scalar owned by this object); sets
         ``status`` to MOE_ERR_NONFINITE when it is infinite or NaN."""
-        ops.moe_grad_norm(self.grads, self.total, self.ws, self.status)
+        ops.moe_grad_norm(self.grads, *self._owned, stream=ops.raw_stream(self._device))
         return self.total
 
     def clip(self, max_norm: float) -> torch.Tensor:
         """Scale the gradients by max_norm / norm if norm > max_norm (else, and
         with a norm that is not finite, they stay or are copied to outs as they
         are).  Returns the norm before."""
-        ops.moe_grad_clip(self.grads, max_norm, self.total, self.ws, self.status)
+        ops.moe_grad_clip(self.grads, max_norm, *self._owned, stream=ops.raw_stream(self._device))
         return self.total

@@ -327,6 +327,12 @@ def moe_route_noalloc(s, x, Wg, logit_bias, logits, compute_logits, idx, w, coun
         _ptr(dev_status, _I32), _stream(stream)))
 
 
+def raw_stream(device_index: int) -> int:
+    """The current stream's handle, for calls a few microseconds long: without
+    the torch.cuda.Stream object that torch.cuda.current_stream() makes."""
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
 FEW_MAX_TOKENS = 64  # MOE_FEW_MAX_TOKENS in include/moe.h
 
 

@@ -117,6 +117,14 @@ def test_all_zero_and_empty():
         assert int(c.status.item()) == 0
 
 
+def test_a_first_launch_without_elements():
+    ts = [torch.zeros(0, device=DEV)] * 1000 + make([5, 3])
+    c = GradClip(ts)
+    want = exact(ts)
+    assert abs(float(c.clip(0.5 * want)) - want) <= NORM * want
+    assert abs(exact(ts) - 0.5 * want) <= 2 * NORM * want
+
+
 def test_bounds():
     ts = make([5000, 77], (F32, BF16))
     norm = float(GradClip(ts).norm())
