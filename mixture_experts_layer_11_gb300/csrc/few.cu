@@ -98,110 +98,74 @@ __global__ void __launch_bounds__(kLogitThreads)
 }
 
 // ---- gate ---------------------------------------------------------------------------
-// One warp, for NT tokens t0, t0 + step, ... in lockstep (their chains of reductions
-// overlap): the k experts with the largest logits (equal ones by their index) and
+// One warp: the k experts with the largest logits (equal ones by their index) and
 // their softmax weights.  Lane l holds experts l, l + 32, ...
-template <int EPL, int NT>
-__device__ __forceinline__ void gate(const float* logits, int t0, int step, int tokens, int E, int k,
-                                     int renorm, uint8_t* e_of, float* w, int32_t* status) {
+template <int EPL>
+__device__ __forceinline__ void gate(const float* L, int E, int k, int renorm, uint8_t* e_of,
+                                     float* w, int32_t* status) {
     const int lane = threadIdx.x & 31;
     auto value = [](uint32_t x) { return __uint_as_float(x & 0x80000000u ? x & 0x7fffffffu : ~x); };
-    uint32_t key[NT][EPL];   // ordered as the logits; 0: not an expert, or taken
+    uint32_t key[EPL], high = 0u;   // ordered as the logits; 0: not an expert, or taken
     bool bad = false;
     #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int t = t0 + i * step < tokens ? t0 + i * step : t0;   // past the end: the first again
-        #pragma unroll
-        for (int q = 0; q < EPL; ++q) {
-            const int e = lane + 32 * q;
-            key[i][q] = 0u;
-            if (e < E) {
-                float l = __ldcg(logits + t * E + e);
-                if (!isfinite(l)) bad = true;
-                if (isnan(l)) l = -INFINITY;                   // ranks below every number
-                const uint32_t u = __float_as_uint(l + 0.f);   // one zero
-                key[i][q] = u & 0x80000000u ? ~u : u | 0x80000000u;
-            }
+    for (int q = 0; q < EPL; ++q) {
+        const int e = lane + 32 * q;
+        key[q] = 0u;
+        if (e < E) {
+            float l = __ldcg(L + e);
+            if (!isfinite(l)) bad = true;
+            if (isnan(l)) l = -INFINITY;                   // ranks below every number
+            const uint32_t u = __float_as_uint(l + 0.f);   // one zero
+            key[q] = u & 0x80000000u ? ~u : u | 0x80000000u;
         }
+        high = key[q] > high ? key[q] : high;
     }
     if (__any_sync(kFull, bad) && lane == 0) report(status, MOE_ERR_NONFINITE);
-    float m[NT], z[NT];
+    const float m = value(__reduce_max_sync(kFull, high));
+    float z = 0.f;
     #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        uint32_t high = key[i][0];
+    for (int q = 0; q < EPL; ++q)
+        if (lane + 32 * q < E) z += expf(value(key[q]) - m);
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+    int my_e = 0;
+    uint32_t my_key = 0u;
+    #pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = key[0];
+        int at = lane;
         #pragma unroll
-        for (int q = 1; q < EPL; ++q) high = key[i][q] > high ? key[i][q] : high;
-        m[i] = value(__reduce_max_sync(kFull, high));
-    }
-    #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        z[i] = 0.f;
+        for (int q = 1; q < EPL; ++q)
+            if (key[q] > best) { best = key[q]; at = lane + 32 * q; }
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        at = (int)__reduce_min_sync(kFull, best == top ? (unsigned)at : 256u);
         #pragma unroll
         for (int q = 0; q < EPL; ++q)
-            if (lane + 32 * q < E) z[i] += expf(value(key[i][q]) - m[i]);
+            if (at == lane + 32 * q) key[q] = 0u;
+        if (lane == j) { my_e = at; my_key = top; }
     }
-    #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        #pragma unroll
-        for (int i = 0; i < NT; ++i) z[i] += __shfl_xor_sync(kFull, z[i], o);
-    int my_e[NT] = {};
-    uint32_t my_key[NT] = {};
-    for (int j = 0; j < k; ++j) {
-        uint32_t best[NT], top[NT];
-        int at[NT];
-        #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            best[i] = key[i][0];
-            at[i] = lane;
-            #pragma unroll
-            for (int q = 1; q < EPL; ++q)
-                if (key[i][q] > best[i]) { best[i] = key[i][q]; at[i] = lane + 32 * q; }
-        }
-        #pragma unroll
-        for (int i = 0; i < NT; ++i) top[i] = __reduce_max_sync(kFull, best[i]);
-        #pragma unroll
-        for (int i = 0; i < NT; ++i)
-            at[i] = (int)__reduce_min_sync(kFull, best[i] == top[i] ? (unsigned)at[i] : 256u);
-        #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            #pragma unroll
-            for (int q = 0; q < EPL; ++q)
-                if (at[i] == lane + 32 * q) key[i][q] = 0u;
-            if (lane == j) { my_e[i] = at[i]; my_key[i] = top[i]; }
-        }
-    }
-    float pr[NT], sum[NT];
-    #pragma unroll
-    for (int i = 0; i < NT; ++i) sum[i] = pr[i] = lane < k ? expf(value(my_key[i]) - m[i]) / z[i] : 0.f;
+    float pr = lane < k ? expf(value(my_key) - m) / z : 0.f;
     if (renorm) {
+        float sum = pr;
         #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            #pragma unroll
-            for (int i = 0; i < NT; ++i) sum[i] += __shfl_xor_sync(kFull, sum[i], o);
-        #pragma unroll
-        for (int i = 0; i < NT; ++i) pr[i] /= sum[i];
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        pr /= sum;
     }
-    #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int t = t0 + i * step;
-        if (lane < k && t < tokens) {
-            e_of[t * k + lane] = (uint8_t)my_e[i];
-            w[t * k + lane] = pr[i];
-        }
+    if (lane < k) {
+        e_of[lane] = (uint8_t)my_e;
+        w[lane] = pr;
     }
 }
 
-template <int EPL>
-__device__ __forceinline__ void gate_all(const float* logits, int tokens, int E, int k, int renorm,
-                                         uint8_t* e_of, float* w, int32_t* status) {
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int t = warp;
-    if (tokens <= warps) {
-        if (t < tokens) gate<EPL, 1>(logits, t, warps, tokens, E, k, renorm, e_of, w, status);
-        return;
+// The block's warps, a token each in turn.
+__device__ __forceinline__ void gate_tokens(const float* logits, int tokens, int E, int k, int renorm,
+                                            uint8_t* e_of, float* w, int32_t* status) {
+    #pragma unroll 1
+    for (int t = threadIdx.x >> 5; t < tokens; t += blockDim.x >> 5) {
+        if (E <= 32) gate<1>(logits + t * E, E, k, renorm, e_of + t * k, w + t * k, status);
+        else if (E <= 128) gate<4>(logits + t * E, E, k, renorm, e_of + t * k, w + t * k, status);
+        else gate<8>(logits + t * E, E, k, renorm, e_of + t * k, w + t * k, status);
     }
-    for (; t < tokens; t += 3 * warps)
-        gate<EPL, 3>(logits, t, warps, tokens, E, k, renorm, e_of, w, status);
 }
 
 // ---- a handful of tokens on the CUDA cores -------------------------------------------
@@ -263,12 +227,7 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int claimed = 0;
     if (threadIdx.x == 0) claimed = atomicAdd(g.ticket, 1);
-    if (warp < g.tokens) {
-        int32_t* status = blockIdx.x == 0 ? g.status : nullptr;
-        if (g.E <= 32) gate<1, 1>(g.logits, warp, W, g.tokens, g.E, g.k, g.renorm, e_of, w, status);
-        else if (g.E <= 128) gate<4, 1>(g.logits, warp, W, g.tokens, g.E, g.k, g.renorm, e_of, w, status);
-        else gate<8, 1>(g.logits, warp, W, g.tokens, g.E, g.k, g.renorm, e_of, w, status);
-    }
+    gate_tokens(g.logits, g.tokens, g.E, g.k, g.renorm, e_of, w, blockIdx.x == 0 ? g.status : nullptr);
     __syncthreads();
     // the distinct experts in the order of their first slots, and each one's slot
     // (255: none) of every token
@@ -435,6 +394,7 @@ constexpr int kWarpsBeforeEpilogue = 4;
 // Times that decide whether the first product's units are cut: a K block of
 // weights when all blocks stream, when few do, and adding the parts of cut units.
 constexpr float kBlockNs = 366.f, kLoneBlockNs = 250.f, kJoinNs = 3000.f;
+constexpr uint64_t kTakeOverNs = 20000;   // a share without a block for so long is taken over
 
 template <typename T> struct Kind;
 template <> struct Kind<__nv_bfloat16> {
@@ -456,54 +416,50 @@ template <typename T> constexpr int few_threads() {
     return Kind<T>::kTensor ? 384 : kWarpsBeforeEpilogue * 32 + Kind<T>::kEpilogue;
 }
 
-// counters in the workspace, zeroed by the logits kernel
+constexpr int kMaxBlocks = 512;
+
+// In the workspace, zeroed by the logits kernel.
 struct Counters {
-    int done;           // finished units (tasks) of the first product
-    int ticket;         // tasks handed out
-    int joined[512];    // per block: parts of the unit that starts in it and ends in another
+    int done;                    // finished units (few_direct_kernel: tasks) of the first product
+    int ticket;                  // few_direct_kernel: tasks handed out
+    int claimed[2];              // shares of each product that a block has taken
+    int sums;                    // summing tasks handed out
+    int claim[2][kMaxBlocks];    // 1: the share is taken
+    int joined[kMaxBlocks];      // per share: parts of the unit that starts in it and ends in another
     // then per output tile: parts written
 };
-constexpr int kMaxBlocks = 512;
 
 struct FewArgs {
     int tokens, d, f, E, k, renorm;
     int tiles1, tiles2, KB1, KB2;         // of the two products: output tiles, K blocks
-    int a_stages, b_stages, b_bytes;      // shared-memory rings
+    int slices;                           // summing tasks an output tile
+    int a_stages, b_ring;                 // shared-memory rings: weights (stages), activations (bytes)
     const float* logits;
     const void *b1, *b2, *residual;
     void* y;
     void* hidden;          // [T k kRowsPerSlot][f]
-    float *part1, *part2;  // [blocks][2][T][128] partial sums of the two products
+    float *part1, *part2;  // [shares][2][T][128] partial sums of the two products
     Counters* cnt;
     int* tiles_done;       // per output tile
     int32_t* status;
     uint64_t limit_ns;
 };
 
-struct FewCtrl {
-    uint64_t a_full[kMaxAStages], a_empty[kMaxAStages];
-    uint64_t b_full[kMaxBStages], b_empty[kMaxBStages];
-    uint64_t t_full[2], t_empty[2], drain;
-    uint32_t tmem;
-    int abort_flag;
-    int last;
-};
-
 // ---- dispatch -----------------------------------------------------------------------
-// Every block of the expert kernel works out the gate for itself, a warp a token,
-// and sorts the (token, slot) pairs (1024 of them at most): rows by expert, then by
-// token.  That takes it less time than to wait for another block's result.
+// Every block of the expert kernel works out the gate for itself and sorts the
+// (token, slot) pairs (1024 of them at most): rows by expert, then by token.  That
+// takes it less time than to wait for another block's result.
 struct Sorted {
     unsigned long long tokens[256];   // bit t: token t goes to this expert
     int off[257];                     // first row of each expert
     int act[256];                     // experts with tokens, ascending
     int cost[257];                    // prefix sums over act of block_cost()
     int most;                         // largest block_cost()
+    int most_rows;                    // largest number of rows of an expert
     int nact;
-    int warp_sum[8], warp_cost[8];
     float w[kMaxSlots];               // gate weight of slot (t, j)
-    uint8_t e_of[kMaxSlots];          // its expert
     float row_w[kMaxSlots];           // gate weight of each row
+    uint8_t e_of[kMaxSlots];          // expert of slot (t, j)
     uint8_t row_token[kMaxSlots];     // token of each row
 };
 
@@ -516,190 +472,198 @@ template <typename T> __device__ __forceinline__ int block_cost(int rows) {
 
 // One block's consecutive K blocks of one (expert, tile).
 struct Seg {
-    int phase;        // 0: first product, 1: second
     int a, m;         // active expert, tile
     int kb0, kb1;     // K blocks
     int c0, c1;       // blocks that hold the unit's first and last K block
 };
 
-// Walks a block's share of the first product, then of the second.  The K blocks
-// of a product lie one after another on a line, each as long as its cost: in the
-// first product an expert's tiles follow one another, in the second an output
-// tile's experts.  The line is cut into equal shares, and a K block is the
-// share's in which it begins; so every block works for the same time, and a
-// share may begin and end inside a unit (an expert's tile).
+// A share of a product.  The K blocks of a product lie one after another on a line,
+// each as long as its cost: in the first product an expert's tiles follow one
+// another, in the second an output tile's experts.  The line is cut into equal
+// shares, one a block, and a K block is the share's in which it begins; so every
+// block works for the same time, and a share may begin and end inside a unit (an
+// expert's tile).
+enum : int { kFirst = 0, kSecond = 1, kSum = 2, kEnd = 3 };
 struct Walk {
-    const Sorted* p;
-    const Walk* then;      // the share of the second product
     int phase;
+    int me;                // the share's (kSum: the task's) number
     int tiles, KB;         // of the product
-    int blocks, share, longer;   // the first `longer` shares are share + 1 long
+    int shares, size, longer;    // the first `longer` shares are size + 1 long
     bool whole;            // first product: shares of whole units, counted in units
     int end;
     int a, m, kb;          // next K block
 
-    __device__ int start(int block) const { return block * share + (block < longer ? block : longer); }
-    __device__ int line(int a_, int m_, int kb_) const {   // where a K block begins
-        const int c = p->cost[a_ + 1] - p->cost[a_];
-        return phase == 0 ? p->cost[a_] * tiles * KB + (m_ * KB + kb_) * c
-                          : (m_ * p->cost[p->nact] + p->cost[a_]) * KB + kb_ * c;
+    __device__ int start(int share) const { return share * size + (share < longer ? share : longer); }
+    __device__ int line(const Sorted& p, int a_, int m_, int kb_) const {   // where a K block begins
+        const int c = p.cost[a_ + 1] - p.cost[a_];
+        return phase == kFirst ? p.cost[a_] * tiles * KB + (m_ * KB + kb_) * c
+                               : (m_ * p.cost[p.nact] + p.cost[a_]) * KB + kb_ * c;
     }
-    __device__ int holder(int a_, int m_, int kb_) const {   // the block whose share it is in
-        const int x = line(a_, m_, kb_), cut = longer * (share + 1);
-        return x < cut ? x / (share + 1) : longer + (x - cut) / share;
+    __device__ int holder(const Sorted& p, int a_, int m_, int kb_) const {   // the share it is in
+        const int x = line(p, a_, m_, kb_), cut = longer * (size + 1);
+        return x < cut ? x / (size + 1) : longer + (x - cut) / size;
     }
-    // needs the plan's act and cost
-    __device__ void begin(const FewArgs& g, const Sorted* plan, int product, const Walk* then_) {
-        p = plan;
-        then = then_;
+    __device__ void cut(const FewArgs& g, const Sorted& p, int product) {
         phase = product;
-        tiles = product == 0 ? g.tiles1 : g.tiles2;
-        KB = product == 0 ? g.KB1 : g.KB2;
-        const int grid = (int)gridDim.x, nact = p->nact, me = (int)blockIdx.x;
+        tiles = product == kFirst ? g.tiles1 : g.tiles2;
+        KB = product == kFirst ? g.KB1 : g.KB2;
+        const int grid = (int)gridDim.x, nact = p.nact;
         const int units = nact * tiles;
         whole = false;
-        if (product == 0) {
+        if (product == kFirst) {
             const int rounds = (units + grid - 1) / grid;
             const float all = (float)units / (float)grid * kBlockNs;     // a K block of every unit
             const float each = units < grid ? fmaxf(all, kLoneBlockNs) : kBlockNs;
             whole = rounds * each * KB <= all * KB + kJoinNs;
         }
-        const int total = whole ? units : p->cost[nact] * tiles * KB;
+        const int total = whole ? units : p.cost[nact] * tiles * KB;
         // no share is shorter than a K block: each holds the beginning of one
-        blocks = whole || p->most == 1 ? total : total / p->most;
-        blocks = blocks < grid ? blocks : grid;
-        share = total / blocks;
-        longer = total - share * blocks;
+        shares = whole || p.most == 1 ? total : total / p.most;
+        shares = shares < grid ? shares : grid;
+        size = total / shares;
+        longer = total - size * shares;
+    }
+    __device__ void begin(const Sorted& p, int share) {
+        me = share;
         a = m = kb = 0;
-        end = 0;
-        if (me >= blocks) return;
-        int x = start(me);
-        end = start(me + 1);
+        int x = start(share);
+        end = start(share + 1);
         if (whole) {
             a = x / tiles;
             m = x - a * tiles;
             return;
         }
         // the first K block that begins at or after x
-        const int per = product == 0 ? tiles * KB : KB;   // K blocks an expert
-        if (product == 1) {
-            m = x / (per * p->cost[nact]);
-            x -= m * per * p->cost[nact];
+        const int nact = p.nact, per = phase == kFirst ? tiles * KB : KB;   // K blocks an expert
+        if (phase == kSecond) {
+            m = x / (per * p.cost[nact]);
+            x -= m * per * p.cost[nact];
         }
         int lo = 0, hi = nact;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (p->cost[mid] * per <= x) lo = mid; else hi = mid;
+            if (p.cost[mid] * per <= x) lo = mid; else hi = mid;
         }
         a = lo;
-        const int c = p->cost[a + 1] - p->cost[a];
-        kb = x - p->cost[a] * per;
+        const int c = p.cost[a + 1] - p.cost[a];
+        kb = x - p.cost[a] * per;
         if (c > 1) kb = (kb + c - 1) / c;
-        if (product == 0) {
+        if (phase == kFirst) {
             m = kb / KB;
             kb -= m * KB;
         }
-        wrap();
+        wrap(p);
     }
-    __device__ void wrap() {   // past the end of a unit, an expert, a tile
+    __device__ void wrap(const Sorted& p) {   // past the end of a unit, an expert, a tile
         if (kb >= KB) {
             kb = 0;
-            if (phase == 0) ++m; else ++a;
+            if (phase == kFirst) ++m; else ++a;
         }
-        if (phase == 0 && m >= tiles) { m = 0; ++a; }
-        if (phase == 1 && a >= p->nact) { a = 0; ++m; }
+        if (phase == kFirst && m >= tiles) { m = 0; ++a; }
+        if (phase == kSecond && a >= p.nact) { a = 0; ++m; }
     }
-    __device__ bool left() const {
-        if (whole) return a * tiles + m < end;
-        return (phase == 0 ? a < p->nact : m < tiles) && line(a, m, kb) < end;
-    }
-    __device__ bool next(Seg& s) {
-        if (!left()) {
-            if (phase == 1) return false;
-            *this = *then;
-            if (!left()) return false;
+    __device__ bool next(const Sorted& p, Seg& s) {
+        if (whole) {
+            if (a * tiles + m >= end) return false;
+        } else if ((phase == kFirst ? a >= p.nact : m >= tiles) || line(p, a, m, kb) >= end) {
+            return false;
         }
-        s.phase = phase;
         s.a = a;
         s.m = m;
         s.kb0 = kb;
         s.kb1 = KB;
-        s.c0 = s.c1 = (int)blockIdx.x;
+        s.c0 = s.c1 = me;
         if (!whole) {
-            const int c = p->cost[a + 1] - p->cost[a];
-            int n = end - line(a, m, kb);
+            const int c = p.cost[a + 1] - p.cost[a];
+            int n = end - line(p, a, m, kb);
             if (c > 1) n = (n + c - 1) / c;
             if (kb + n < KB) s.kb1 = kb + n;
-            if (kb > 0) s.c0 = holder(a, m, 0);
-            if (s.kb1 < KB) s.c1 = holder(a, m, KB - 1);
+            if (kb > 0) s.c0 = holder(p, a, m, 0);
+            if (s.kb1 < KB) s.c1 = holder(p, a, m, KB - 1);
         }
         kb = s.kb1;
-        wrap();
+        wrap(p);
         return true;
     }
 };
 
-// The sorted rows, and where this block's two shares begin.
+// The sorted rows, and how the two products are cut.
 struct Plan : Sorted {
     Walk first, second;
 };
 
 // Called by all threads of a block of at least 256.
 template <typename T>
-__device__ void make_plan(Plan& p, const FewArgs& g) {
-    const int tokens = g.tokens, k = g.k;
+__device__ __forceinline__ void make_plan(Plan& p, const FewArgs& g) {
+    const int tokens = g.tokens, k = g.k, E = g.E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e < 256; e += blockDim.x) p.tokens[e] = 0ull;
-    if (threadIdx.x == 0) p.most = 1;
-    int32_t* status = blockIdx.x == 0 ? g.status : nullptr;
-    if (g.E <= 32) gate_all<1>(g.logits, tokens, g.E, k, g.renorm, p.e_of, p.w, status);
-    else if (g.E <= 128) gate_all<4>(g.logits, tokens, g.E, k, g.renorm, p.e_of, p.w, status);
-    else gate_all<8>(g.logits, tokens, g.E, k, g.renorm, p.e_of, p.w, status);
+    for (int e = threadIdx.x; e < E; e += blockDim.x) p.tokens[e] = 0ull;
+    gate_tokens(g.logits, tokens, E, k, g.renorm, p.e_of, p.w, blockIdx.x == 0 ? g.status : nullptr);
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * k; i += blockDim.x)
         atomicOr(&p.tokens[p.e_of[i]], 1ull << (i / k));
     __syncthreads();
-    // exclusive prefix sums over the experts: (rows, has rows) in one word, cost
-    const int e = threadIdx.x;
-    int n = 0, v = 0, c = 0;
-    if (e < 256) {
-        n = __popcll(p.tokens[e]);
-        v = n | (n > 0 ? 1 << 16 : 0);
-        c = n > 0 ? block_cost<T>(n) : 0;
-        if (sizeof(T) == 4 && c > 1) atomicMax(&p.most, c);
-        const int own = v, own_c = c;
-        #pragma unroll
+    if (warp == 0) {
+        // Prefix sums over the experts, `per` of them a lane: (rows, has rows) in one
+        // word, and cost.  (Loops, not unrolled: short code is fast code here.)
+        const int per = (E + 31) >> 5, e0 = lane * per;
+        int v = 0, c = 0, rows = 0;
+        #pragma unroll 1
+        for (int e = e0; e < e0 + per; ++e) {
+            const int n = e < E ? __popcll(p.tokens[e]) : 0;
+            if (n == 0) continue;
+            v += n | 1 << 16;
+            c += block_cost<T>(n);
+            rows = n > rows ? n : rows;
+        }
+        const int own_v = v, own_c = c;
+        #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(kFull, v, o), uc = __shfl_up_sync(kFull, c, o);
             if (lane >= o) { v += u; c += uc; }
         }
-        if (lane == 31) { p.warp_sum[warp] = v; p.warp_cost[warp] = c; }
-        v -= own;
+        v -= own_v;
         c -= own_c;
-    }
-    __syncthreads();
-    if (e < 256) {
-        for (int q = 0; q < warp; ++q) { v += p.warp_sum[q]; c += p.warp_cost[q]; }
-        p.off[e] = v & 0xffff;
-        if (n > 0) { p.act[v >> 16] = e; p.cost[v >> 16] = c; }
-        if (e == 255) {
-            const int na = (v >> 16) + (n > 0);
-            p.off[256] = (v & 0xffff) + n;
-            p.nact = na;
-            p.cost[na] = c + (n > 0 ? block_cost<T>(n) : 0);
+        #pragma unroll 1
+        for (int e = e0; e < e0 + per && e < E; ++e) {
+            const int n = __popcll(p.tokens[e]);
+            p.off[e] = v & 0xffff;
+            if (n == 0) continue;
+            p.act[v >> 16] = e;
+            p.cost[v >> 16] = c;
+            v += n | 1 << 16;
+            c += block_cost<T>(n);
+        }
+        rows = (int)__reduce_max_sync(kFull, (unsigned)rows);
+        if (lane == 31) {
+            p.off[E] = v & 0xffff;
+            p.nact = v >> 16;
+            p.cost[v >> 16] = c;
+            p.most_rows = rows;
+            p.most = block_cost<T>(rows);
         }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * k; i += blockDim.x) {
-        const int ee = p.e_of[i], t = i / k;
-        const int r = p.off[ee] + __popcll(p.tokens[ee] & ((1ull << t) - 1ull));
+        const int e = p.e_of[i], t = i / k;
+        const int r = p.off[e] + __popcll(p.tokens[e] & ((1ull << t) - 1ull));
         p.row_token[r] = (uint8_t)t;
         p.row_w[r] = p.w[i];
     }
-    if (lane == 0 && warp == 6) p.first.begin(g, &p, 0, &p.second);
-    if (lane == 0 && warp == 7) p.second.begin(g, &p, 1, nullptr);
+    if (lane == 0 && warp >= 6 && warp < 8) (warp == 6 ? p.first : p.second).cut(g, p, warp - 6);
     __syncthreads();
 }
+
+struct FewCtrl {
+    uint64_t a_full[kMaxAStages], a_empty[kMaxAStages];
+    uint64_t b_full[2][kMaxBStages], b_empty[2][kMaxBStages];   // of each product
+    uint64_t t_full[2], t_empty[2], drain;
+    uint64_t q_full[2], q_empty[2];
+    Walk queue[2];         // what the block's roles work on next
+    uint32_t tmem;
+    int abort_flag;
+    int last;
+};
 
 constexpr int kAccCols = 128;   // columns of one of the two accumulators
 
@@ -730,22 +694,55 @@ template <int N> __device__ __forceinline__ bool epilogue_all(bool ok) {
     return r != 0;
 }
 
+// The activations' ring.  A K block's slot is as large as the product needs, so
+// each product has its own number of stages in the same memory, and its own
+// barriers.
+struct Ring {
+    uint8_t* base;
+    uint64_t *full, *empty;
+    int stages, bytes;     // slots, bytes of one
+    int stage;
+    uint32_t parity;
+    __device__ void set(FewCtrl& c, uint8_t* memory, int size, int product, int rows, int box) {
+        base = memory;
+        full = c.b_full[product];
+        empty = c.b_empty[product];
+        bytes = (rows + box - 1) / box * box * kBlockBytes;
+        stages = size / bytes < kMaxBStages ? size / bytes : kMaxBStages;
+        stage = 0;
+        parity = 0;
+    }
+    __device__ uint8_t* at() const { return base + stage * bytes; }
+    __device__ void step() {
+        if (++stage == stages) { stage = 0; parity ^= 1; }
+    }
+};
+
+// A role's view of the queue of shares.
+struct Reader {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ void step() {
+        if (++slot == 2) { slot = 0; parity ^= 1; }
+    }
+};
+
 // fp32 products on the CUDA cores: 8 warps, a lane holding 4 weight rows and NC
 // activation rows.  With more than NC rows the warps split them into `groups`
 // (1, 2, 4 or 8) and K into 8 / groups; sums run over even and odd k apart, as
 // packed pairs.  The result goes to red[K slice][row][128].
 template <int NC>
-__device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const Seg& s, int rows,
-                                             const uint8_t* row_token, uint8_t* a_ring,
-                                             uint8_t* b_ring, int& as, uint32_t& ap, int& bs,
-                                             uint32_t& bp, int ew, int lane, int groups, float* red) {
+__device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const Seg& s, bool first,
+                                             int rows, const uint8_t* row_token, uint8_t* a_ring,
+                                             int& as, uint32_t& ap, Ring& b, int ew, int lane,
+                                             int groups, float* red) {
     const int grp = ew % groups, slice = ew / groups;
     uint32_t brow[NC];
     #pragma unroll
     for (int j = 0; j < NC; ++j) {
         int r = grp * NC + j;
         r = r < rows ? r : rows - 1;
-        brow[j] = s.phase == 0 ? row_token[r] : r;
+        brow[j] = first ? row_token[r] : r;
     }
     uint64_t acc[4][NC];
     #pragma unroll
@@ -754,10 +751,10 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
         for (int j = 0; j < NC; ++j) acc[q][j] = 0ull;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
         if (!mbar_wait_warp(smem_u32(&c.a_full[as]), ap, g.limit_ns, &c.abort_flag) ||
-            !mbar_wait_warp(smem_u32(&c.b_full[bs]), bp, g.limit_ns, &c.abort_flag))
+            !mbar_wait_warp(smem_u32(&b.full[b.stage]), b.parity, g.limit_ns, &c.abort_flag))
             return false;
         const uint8_t* A = a_ring + as * kABytes;
-        const uint8_t* B = b_ring + bs * g.b_bytes;
+        const uint8_t* B = b.at();
         for (int i = 0; i < groups; ++i) {
             const int ch = slice * groups + i;   // 16-byte chunk of the K block
             ulonglong2 a[4];
@@ -767,20 +764,20 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
                                                             ((ch ^ (lane & 7)) << 4));
             #pragma unroll
             for (int j = 0; j < NC; ++j) {
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(
                     B + brow[j] * 128 + ((ch ^ (brow[j] & 7)) << 4));
                 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    acc[q][j] = f2_fma(a[q].y, b.y, f2_fma(a[q].x, b.x, acc[q][j]));
+                    acc[q][j] = f2_fma(a[q].y, x.y, f2_fma(a[q].x, x.x, acc[q][j]));
             }
         }
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(smem_u32(&c.a_empty[as]));
-            mbar_arrive(smem_u32(&c.b_empty[bs]));
+            mbar_arrive(smem_u32(&b.empty[b.stage]));
         }
         if (++as == g.a_stages) { as = 0; ap ^= 1; }
-        if (++bs == g.b_stages) { bs = 0; bp ^= 1; }
+        b.step();
     }
     #pragma unroll
     for (int j = 0; j < NC; ++j)
@@ -804,7 +801,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
     uint8_t* a_ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(few_smem) + 1023) & ~(uintptr_t)1023);
     uint8_t* b_ring = a_ring + (size_t)g.a_stages * kABytes;
-    float* yacc = reinterpret_cast<float*>(b_ring + (size_t)g.b_stages * g.b_bytes);  // [T][128]
+    float* yacc = reinterpret_cast<float*>(b_ring + g.b_ring);  // [T][128]
     float* red = yacc + g.tokens * kTileM;      // fp32 only
     __shared__ Plan plan;
     __shared__ FewCtrl c;
@@ -812,17 +809,22 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
 
     if (threadIdx.x == 0) {
         const int consumers = K::kTensor ? 1 : K::kEpilogue / 32;
+        #pragma unroll 1
         for (int i = 0; i < g.a_stages; ++i) {
             mbar_init(smem_u32(&c.a_full[i]), 1);
             mbar_init(smem_u32(&c.a_empty[i]), consumers);
         }
-        for (int i = 0; i < g.b_stages; ++i) {
-            mbar_init(smem_u32(&c.b_full[i]), 1);
-            mbar_init(smem_u32(&c.b_empty[i]), consumers);
+        #pragma unroll 1
+        for (int i = 0; i < 2 * kMaxBStages; ++i) {
+            mbar_init(smem_u32(&c.b_full[i / kMaxBStages][i % kMaxBStages]), 1);
+            mbar_init(smem_u32(&c.b_empty[i / kMaxBStages][i % kMaxBStages]), consumers);
         }
+        #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&c.t_full[i]), 1);
             mbar_init(smem_u32(&c.t_empty[i]), K::kEpilogue / 32);
+            mbar_init(smem_u32(&c.q_full[i]), 1);
+            mbar_init(smem_u32(&c.q_empty[i]), K::kEpilogue / 32 + (K::kTensor ? 2 : 1));
         }
         mbar_init(smem_u32(&c.drain), 1);
         c.abort_flag = 0;
@@ -837,36 +839,108 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
         tmem_relinquish();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (on its way while the plan is made)
+    int taken = threadIdx.x == 0 ? atomicCAS(&g.cnt->claim[kFirst][blockIdx.x], 0, 1) : 0;
     make_plan<T>(plan, g);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = K::kTensor ? c.tmem : 0u;
-    Walk walk = plan.first;
+    Walk walk;
     Seg s;
+    Reader q;
+    // B, MMA: the next entry of the queue, by one thread
+    auto take = [&]() {
+        if (!mbar_wait_bounded(smem_u32(&c.q_full[q.slot]), q.parity, g.limit_ns, &c.abort_flag)) {
+            few_abort(c, g.status);
+            return false;
+        }
+        walk = c.queue[q.slot];
+        mbar_arrive(smem_u32(&c.q_empty[q.slot]));
+        q.step();
+        return walk.phase != kEnd;
+    };
 
     if (warp == 0) {
-        // ---- weights: one box of 128 rows a K block, both products in one stream -----
+        // ---- shares, and weights: one box of 128 rows a K block ------------------------
+        // Block b takes share b of each product.  It goes on to the second product (whose
+        // products wait for the whole of the first) and to the summing (which waits for
+        // all parts) only when every share before has a block that works on it, and
+        // takes over one that has none for long: the block it is meant for may wait
+        // for an SM that this kernel, or another, holds.  So nothing waits for a block
+        // that does not run, and blocks need not be resident together.
         if (lane == 0) {
             int st = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            while (ok && walk.next(s)) {
-                const int e = plan.act[s.a];
-                const CUtensorMap* map = s.phase == 0 ? &mapW1 : &mapW2;
-                for (int kb = s.kb0; kb < s.kb1; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&c.a_empty[st]), ph ^ 1, g.limit_ns, &c.abort_flag)) {
-                        few_abort(c, g.status);
-                        ok = false;
-                        break;
+            auto post = [&](const Walk& w) {
+                if (!mbar_wait_bounded(smem_u32(&c.q_empty[q.slot]), q.parity ^ 1, g.limit_ns,
+                                       &c.abort_flag)) {
+                    few_abort(c, g.status);
+                    return false;
+                }
+                c.queue[q.slot] = w;
+                mbar_arrive(smem_u32(&c.q_full[q.slot]));
+                q.step();
+                return true;
+            };
+            #pragma unroll 1
+            for (int product = kFirst; product <= kSecond && ok; ++product) {
+                walk = product == kFirst ? plan.first : plan.second;
+                const CUtensorMap* map = product == kFirst ? &mapW1 : &mapW2;
+                int* claim = g.cnt->claim[product];
+                if (product == kSecond) taken = atomicCAS(&claim[blockIdx.x], 0, 1);
+                int share = (int)blockIdx.x < walk.shares && taken == 0 ? (int)blockIdx.x : -1;
+                while (ok) {
+                    if (share >= 0) {
+                        atomicAdd(&g.cnt->claimed[product], 1);
+                        walk.begin(plan, share);
+                        ok = post(walk);
+                        while (ok && walk.next(plan, s)) {
+                            const int e = plan.act[s.a];
+                            for (int kb = s.kb0; kb < s.kb1; ++kb) {
+                                if (!mbar_wait_bounded(smem_u32(&c.a_empty[st]), ph ^ 1, g.limit_ns,
+                                                       &c.abort_flag)) {
+                                    few_abort(c, g.status);
+                                    ok = false;
+                                    break;
+                                }
+                                mbar_arrive_expect_tx(smem_u32(&c.a_full[st]), kABytes);
+                                tma_load_3d(smem_u32(a_ring + st * kABytes), map,
+                                            smem_u32(&c.a_full[st]), kb * K::kBlock, s.m * kTileM, e);
+                                if (issued < g.a_stages) ++issued;
+                                if (++st == g.a_stages) { st = 0; ph ^= 1; }
+                            }
+                        }
                     }
-                    mbar_arrive_expect_tx(smem_u32(&c.a_full[st]), kABytes);
-                    tma_load_3d(smem_u32(a_ring + st * kABytes), map, smem_u32(&c.a_full[st]),
-                                kb * K::kBlock, s.m * kTileM, e);
-                    if (issued < g.a_stages) ++issued;
-                    if (++st == g.a_stages) { st = 0; ph ^= 1; }
+                    share = -1;
+                    const uint64_t t0 = globaltimer_ns();
+                    uint64_t t1 = t0;
+                    while (ok && load_acquire(&g.cnt->claimed[product]) < walk.shares) {
+                        const uint64_t now = globaltimer_ns();
+                        if (now - t1 > kTakeOverNs) {
+                            for (int i = 0; i < walk.shares && share < 0; ++i)
+                                if (load_acquire(&claim[i]) == 0 && atomicCAS(&claim[i], 0, 1) == 0)
+                                    share = i;
+                            if (share >= 0) break;
+                            t1 = globaltimer_ns();
+                        }
+                        if (now - t0 > g.limit_ns || *(volatile int*)&c.abort_flag) {
+                            few_abort(c, g.status);
+                            ok = false;
+                        }
+                    }
+                    if (share < 0) break;
                 }
             }
+            while (ok) {
+                walk.phase = kSum;
+                walk.me = atomicAdd(&g.cnt->sums, 1);
+                if (walk.me >= g.tiles2 * g.slices) break;
+                ok = post(walk);
+            }
+            walk.phase = kEnd;
+            if (ok) post(walk);
             // copies in flight land before the block ends
             for (int i = 0; i < issued; ++i) {
                 if (--st < 0) { st = g.a_stages - 1; ph ^= 1; }
@@ -877,90 +951,116 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
     } else if (warp == 1) {
         // ---- activations: all tokens' K block of x, or the expert's hidden rows -------
         if (lane == 0) {
-            int st = 0, issued = 0;
-            bool ready = false;
-            uint32_t ph = 0;
-            bool ok = true;
-            while (ok && walk.next(s)) {
-                const int e = plan.act[s.a];
-                const int row0 = s.phase == 0 ? 0 : plan.off[e] * RPS;
-                const int rows = s.phase == 0 ? g.tokens : (plan.off[e + 1] - plan.off[e]) * RPS;
-                const int boxes = (rows + BOX - 1) / BOX;
-                const CUtensorMap* map = s.phase == 0 ? &mapX : &mapH;
-                if (s.phase == 1 && !ready) {
+            Ring r;
+            r.set(c, b_ring, g.b_ring, kFirst, g.tokens, BOX);
+            int issued = 0;
+            bool second = false, ok = true;
+            // copies in flight land before the memory is put to another use
+            auto drain = [&]() {
+                for (int i = 0; i < issued; ++i) {
+                    if (--r.stage < 0) { r.stage = r.stages - 1; r.parity ^= 1; }
+                    mbar_wait_bounded(smem_u32(&r.full[r.stage]), r.parity, g.limit_ns, nullptr);
+                }
+                issued = 0;
+            };
+            while (ok && take()) {
+                if (walk.phase == kSum) continue;
+                if (walk.phase == kSecond && !second) {
+                    second = true;
+                    // every slot of the first product's ring has been read
+                    for (int i = 0; i < r.stages && ok; ++i) {
+                        ok = mbar_wait_bounded(smem_u32(&r.empty[r.stage]), r.parity ^ 1, g.limit_ns,
+                                               &c.abort_flag);
+                        r.step();
+                    }
                     // All hidden rows are written.  (One counter for all experts: the
                     // shares are equal, so that waiting for some of them first gains nothing,
                     // and each further poll would cost a round trip to the L2.)
                     const uint64_t t0 = globaltimer_ns();
-                    while (load_acquire(&g.cnt->done) < plan.nact * g.tiles1) {
-                        if (*(volatile int*)&c.abort_flag || globaltimer_ns() - t0 > g.limit_ns) {
+                    while (ok && load_acquire(&g.cnt->done) < plan.nact * g.tiles1)
+                        ok = !*(volatile int*)&c.abort_flag && globaltimer_ns() - t0 <= g.limit_ns;
+                    if (!ok) {
+                        few_abort(c, g.status);
+                        break;
+                    }
+                    fence_proxy_async_all();
+                    issued = 0;
+                    r.set(c, b_ring, g.b_ring, kSecond, plan.most_rows * RPS, BOX);
+                }
+                while (ok && walk.next(plan, s)) {
+                    const int e = plan.act[s.a];
+                    const int row0 = second ? plan.off[e] * RPS : 0;
+                    const int rows = second ? (plan.off[e + 1] - plan.off[e]) * RPS : g.tokens;
+                    const int boxes = (rows + BOX - 1) / BOX;
+                    const CUtensorMap* map = second ? &mapH : &mapX;
+                    for (int kb = s.kb0; kb < s.kb1; ++kb) {
+                        const uint32_t full = smem_u32(&r.full[r.stage]);
+                        if (!mbar_wait_bounded(smem_u32(&r.empty[r.stage]), r.parity ^ 1, g.limit_ns,
+                                               &c.abort_flag)) {
                             few_abort(c, g.status);
                             ok = false;
                             break;
                         }
+                        mbar_arrive_expect_tx(full, boxes * BOX * kBlockBytes);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(smem_u32(r.at() + i * BOX * kBlockBytes), map, full,
+                                        kb * K::kBlock, row0 + i * BOX);
+                        if (issued < r.stages) ++issued;
+                        r.step();
                     }
-                    if (!ok) break;
-                    fence_proxy_async_all();
-                    ready = true;
-                }
-                for (int kb = s.kb0; kb < s.kb1; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&c.b_empty[st]), ph ^ 1, g.limit_ns, &c.abort_flag)) {
-                        few_abort(c, g.status);
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(smem_u32(&c.b_full[st]), boxes * BOX * kBlockBytes);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(smem_u32(b_ring + st * g.b_bytes + i * BOX * kBlockBytes), map,
-                                    smem_u32(&c.b_full[st]), kb * K::kBlock, row0 + i * BOX);
-                    if (issued < g.b_stages) ++issued;
-                    if (++st == g.b_stages) { st = 0; ph ^= 1; }
                 }
             }
-            // copies in flight land before the block ends
-            for (int i = 0; i < issued; ++i) {
-                if (--st < 0) { st = g.b_stages - 1; ph ^= 1; }
-                mbar_wait_bounded(smem_u32(&c.b_full[st]), ph, g.limit_ns, nullptr);
-            }
+            drain();
         }
         __syncwarp();
     } else if (K::kTensor && warp == 2) {
         // ---- tensor core: D[128 weight rows][activation rows], one accumulator a segment --
         if (lane == 0) {
-            int as = 0, bs = 0, acc = 0;
-            uint32_t ap = 0, bp = 0, tp = 0;
-            bool ok = true;
-            while (ok && walk.next(s)) {
-                const int e = plan.act[s.a];
-                const int rows = s.phase == 0 ? g.tokens : (plan.off[e + 1] - plan.off[e]) * RPS;
-                const uint32_t idesc = idesc_bf16_f32(kTileM, (rows + 15) & ~15, false, false);
-                if (!mbar_wait_bounded(smem_u32(&c.t_empty[acc]), tp ^ 1, g.limit_ns, &c.abort_flag)) {
-                    few_abort(c, g.status);
-                    break;
+            Ring r;
+            r.set(c, b_ring, g.b_ring, kFirst, g.tokens, BOX);
+            int as = 0, acc = 0;
+            uint32_t ap = 0, tp = 0;
+            bool second = false, ok = true;
+            while (ok && take()) {
+                if (walk.phase == kSum) continue;
+                if (walk.phase == kSecond && !second) {
+                    second = true;
+                    r.set(c, b_ring, g.b_ring, kSecond, plan.most_rows * RPS, BOX);
                 }
-                tc_fence_after();
-                for (int kb = s.kb0; kb < s.kb1; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&c.a_full[as]), ap, g.limit_ns, &c.abort_flag) ||
-                        !mbar_wait_bounded(smem_u32(&c.b_full[bs]), bp, g.limit_ns, &c.abort_flag)) {
+                while (ok && walk.next(plan, s)) {
+                    const int e = plan.act[s.a];
+                    const int rows = second ? (plan.off[e + 1] - plan.off[e]) * RPS : g.tokens;
+                    const uint32_t idesc = idesc_bf16_f32(kTileM, (rows + 15) & ~15, false, false);
+                    if (!mbar_wait_bounded(smem_u32(&c.t_empty[acc]), tp ^ 1, g.limit_ns, &c.abort_flag)) {
                         few_abort(c, g.status);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = smem_desc_sw128(smem_u32(a_ring + as * kABytes), 16, 1024);
-                    const uint64_t bd = smem_desc_sw128(smem_u32(b_ring + bs * g.b_bytes), 16, 1024);
-                    #pragma unroll
-                    for (int kk = 0; kk < K::kBlock / 16; ++kk)
-                        tc_mma_bf16(tmem + acc * kAccCols, ad + kk * 2, bd + kk * 2, idesc,
-                                    kb > s.kb0 || kk > 0);
-                    tc_commit(smem_u32(&c.a_empty[as]));
-                    tc_commit(smem_u32(&c.b_empty[bs]));
-                    if (++as == g.a_stages) { as = 0; ap ^= 1; }
-                    if (++bs == g.b_stages) { bs = 0; bp ^= 1; }
+                    for (int kb = s.kb0; kb < s.kb1; ++kb) {
+                        if (!mbar_wait_bounded(smem_u32(&c.a_full[as]), ap, g.limit_ns, &c.abort_flag) ||
+                            !mbar_wait_bounded(smem_u32(&r.full[r.stage]), r.parity, g.limit_ns,
+                                               &c.abort_flag)) {
+                            few_abort(c, g.status);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = smem_desc_sw128(smem_u32(a_ring + as * kABytes), 16, 1024);
+                        const uint64_t bd = smem_desc_sw128(smem_u32(r.at()), 16, 1024);
+                        #pragma unroll
+                        for (int kk = 0; kk < K::kBlock / 16; ++kk)
+                            tc_mma_bf16(tmem + acc * kAccCols, ad + kk * 2, bd + kk * 2, idesc,
+                                        kb > s.kb0 || kk > 0);
+                        tc_commit(smem_u32(&c.a_empty[as]));
+                        tc_commit(smem_u32(&r.empty[r.stage]));
+                        if (++as == g.a_stages) { as = 0; ap ^= 1; }
+                        r.step();
+                    }
+                    if (!ok) break;
+                    tc_commit(smem_u32(&c.t_full[acc]));
+                    if (++acc == 2) { acc = 0; tp ^= 1; }
                 }
-                if (!ok) break;
-                tc_commit(smem_u32(&c.t_full[acc]));
-                if (++acc == 2) { acc = 0; tp ^= 1; }
             }
             // every MMA issued has completed before TMEM is freed
             tc_commit(smem_u32(&c.drain));
@@ -971,212 +1071,232 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
         // ---- epilogue -----------------------------------------------------------------
         // Thread i (of 128; fp32: two threads, alternate rows) owns weight row i of the
         // tile, i.e. one output feature, for all activation rows.
-        constexpr int NT = K::kEpilogue;
+        constexpr int NT = K::kEpilogue, STEP = NT / kTileM;
         const int tid = threadIdx.x - kWarpsBeforeEpilogue * 32;
-        const int ew = tid >> 5;
+        const int ew = tid >> 5, t_first = tid / kTileM;
         const int i = K::kTensor ? (warp & 3) * 32 + lane : tid & 127;
-        const int me = (int)blockIdx.x;
         const int64_t slot_floats = (int64_t)g.tokens * kTileM;
         T* hidden = (T*)g.hidden;
-        int acc = 0, as = 0, bs = 0;
-        uint32_t tp = 0, ap = 0, bp = 0;
         const T* residual = (const T*)g.residual;
         T* y = (T*)g.y;
-        auto put_y = [&](int t, int m, float v) {
-            const int col = m * kTileM + i;
-            if (col >= g.d) return;
-            const int64_t o = (int64_t)t * g.d + col;
+        int acc = 0, as = 0;
+        uint32_t tp = 0, ap = 0;
+        Ring ring;
+        if (!K::kTensor) ring.set(c, b_ring, g.b_ring, kFirst, g.tokens, BOX);
+        bool second = false, ok = true;
+        auto put_y = [&](int64_t o, float v) {
             if (residual) v += to_f32<T>(residual[o]);
             y[o] = from_f32<T>(v);
         };
-        bool more = walk.next(s);
-        bool fresh = true;     // yacc holds nothing yet
-        // tiles that other blocks add to as well: this block's first and last
-        int m_a = 0, d_a = 0, n_a = 0, m_b = 0, d_b = 0, n_b = 0;
-        bool gone = false;
-        while (more) {
-            const int e = plan.act[s.a];
-            const int r0 = plan.off[e], rows = plan.off[e + 1] - r0;
-            const int col = s.m * kTileM + i;
-            const bool whole = s.c0 == s.c1;   // no other block has a part of the unit
-            const bool live = col < (s.phase == 0 ? g.f : g.d);
-            const T* bias = (const T*)(s.phase == 0 ? g.b1 : g.b2);
-            const float b = bias && live && s.kb0 == 0
-                                ? to_f32<T>(bias[(int64_t)e * (s.phase == 0 ? g.f : g.d) + col]) : 0.f;
-            // unit of the first product cut over blocks c0..c1
-            const int c0 = s.c0, c1 = s.c1;
-            float* mine = g.part1 + (me * 2 + (me == c0)) * slot_floats;
-            if (s.phase == 1 && fresh) {
-                if (!K::kTensor) epilogue_barrier<NT>();
-                for (int t = tid / kTileM; t < g.tokens; t += NT / kTileM) yacc[t * kTileM + i] = 0.f;
-                if (!K::kTensor) epilogue_barrier<NT>();
-                fresh = false;
+        while (true) {
+            ok = mbar_wait_warp(smem_u32(&c.q_full[q.slot]), q.parity, g.limit_ns, &c.abort_flag);
+            if (!ok) few_abort(c, g.status);
+            if (!epilogue_all<NT>(ok)) break;
+            walk = c.queue[q.slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.q_empty[q.slot]));
+            q.step();
+            if (walk.phase == kEnd) break;
+            const int me = walk.me;
+            if (walk.phase == kSum) {
+                // A slice of the tokens of an output tile that several shares have a part
+                // of: once all parts are there, they are added in the shares' order.
+                const int m = me / g.slices, sl = me - m * g.slices;
+                const Walk& w = plan.second;
+                const int d0 = w.holder(plan, 0, m, 0);
+                const int d1 = w.holder(plan, plan.nact - 1, m, w.KB - 1);
+                const int lo = g.tokens * sl / g.slices, hi = g.tokens * (sl + 1) / g.slices;
+                if (d0 == d1 || lo == hi) continue;
+                if (tid == 0) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (ok && load_acquire(&g.tiles_done[m]) < d1 - d0 + 1)
+                        ok = !*(volatile int*)&c.abort_flag && globaltimer_ns() - t0 <= g.limit_ns;
+                    if (!ok) few_abort(c, g.status);
+                }
+                if (!epilogue_all<NT>(ok)) break;
+                // four columns a thread
+                const int col = (tid & 31) * 4;
+                if (m * kTileM + col >= g.d) continue;
+                #pragma unroll 2
+                for (int t = lo + ew; t < hi; t += NT / 32) {
+                    const float* from = g.part2 + t * kTileM + col;
+                    float4 v = __ldcg(reinterpret_cast<const float4*>(from + (d0 * 2 + 1) * slot_floats));
+                    #pragma unroll 4
+                    for (int b = d0 + 1; b <= d1; ++b) {
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(from + b * 2 * slot_floats));
+                        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+                    }
+                    const int64_t o = (int64_t)t * g.d + m * kTileM + col;
+                    put_y(o, v.x);
+                    put_y(o + 1, v.y);
+                    put_y(o + 2, v.z);
+                    put_y(o + 3, v.w);
+                }
+                continue;
             }
-            auto put_hidden = [&](int r, float h) {
-                if (!live) return;
+            if (walk.phase == kSecond && !second) {
+                second = true;
+                if (!K::kTensor) ring.set(c, b_ring, g.b_ring, kSecond, plan.most_rows * RPS, BOX);
+            }
+            bool fresh = true;     // yacc holds nothing yet
+            bool more = walk.next(plan, s);
+            while (more) {
+                const int e = plan.act[s.a];
+                const int r0 = plan.off[e], rows = plan.off[e + 1] - r0;
+                const int col = s.m * kTileM + i, width = second ? g.d : g.f;
+                const bool whole = s.c0 == s.c1;   // no other share has a part of the unit
+                const bool live = col < width;
+                const T* bias = (const T*)(second ? g.b2 : g.b1);
+                const float b = bias && live && s.kb0 == 0
+                                    ? to_f32<T>(bias[(int64_t)e * width + col]) : 0.f;
+                // unit of the first product cut over shares c0..c1
+                const int c0 = s.c0, c1 = s.c1;
+                float* mine = g.part1 + (me * 2 + (me == c0)) * slot_floats;
+                if (second && fresh) {
+                    if (!K::kTensor) epilogue_barrier<NT>();
+                    for (int t = t_first; t < g.tokens; t += STEP) yacc[t * kTileM + i] = 0.f;
+                    if (!K::kTensor) epilogue_barrier<NT>();
+                    fresh = false;
+                }
+                auto put_hidden = [&](int r, float h) {
+                    if (!live) return;
+                    if constexpr (K::kTensor) {
+                        // GELU in two bf16 parts, 16 bits together
+                        const float v = gelu_fast(h);
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                        const float rest = v - __bfloat162float(hi);
+                        __nv_bfloat16* p = hidden + (int64_t)(r0 + r) * 2 * g.f + col;
+                        p[0] = hi;
+                        p[g.f] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+                    } else {
+                        hidden[(int64_t)(r0 + r) * g.f + col] = gelu_f(h);
+                    }
+                };
+                auto emit = [&](int r, float v) {   // activation row r of the expert
+                    v += b;
+                    if (second) {
+                        float* p = yacc + plan.row_token[r0 + r] * kTileM + i;
+                        *p = fmaf(plan.row_w[r0 + r], v, *p);
+                    } else if (whole) {
+                        put_hidden(r, v);
+                    } else {
+                        __stcg(mine + r * kTileM + i, v);
+                    }
+                };
                 if constexpr (K::kTensor) {
-                    // GELU in two bf16 parts, 16 bits together
-                    const float a = gelu_fast(h);
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(a);
-                    const float rest = a - __bfloat162float(hi);
-                    __nv_bfloat16* p = hidden + (int64_t)(r0 + r) * 2 * g.f + col;
-                    p[0] = hi;
-                    p[g.f] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-                } else {
-                    hidden[(int64_t)(r0 + r) * g.f + col] = gelu_f(h);
-                }
-            };
-            auto emit = [&](int r, float v) {   // activation row r of the expert
-                v += b;
-                if (s.phase == 1) {
-                    float* p = yacc + plan.row_token[r0 + r] * kTileM + i;
-                    *p = fmaf(plan.row_w[r0 + r], v, *p);
-                } else if (whole) {
-                    put_hidden(r, v);
-                } else {
-                    __stcg(mine + r * kTileM + i, v);
-                }
-            };
-            if constexpr (K::kTensor) {
-                const bool ok = mbar_wait_warp(smem_u32(&c.t_full[acc]), tp, g.limit_ns, &c.abort_flag);
-                if (!ok) few_abort(c, g.status);
-                if (!epilogue_all<NT>(ok)) { gone = true; break; }
-                tc_fence_after();
-                const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * kAccCols;
-                if (s.phase == 0) {
-                    unsigned long long left = plan.tokens[e];
-                    int r = 0;
-                    for (int q = 0; q * 16 < g.tokens; ++q, left >>= 16) {
-                        if (!(left & 0xffffull)) continue;
-                        float v[16];
-                        tmem_ld16(base + q * 16, v);
-                        #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (left >> j & 1ull) emit(r++, v[j]);
+                    ok = mbar_wait_warp(smem_u32(&c.t_full[acc]), tp, g.limit_ns, &c.abort_flag);
+                    if (!ok) few_abort(c, g.status);
+                    if (!epilogue_all<NT>(ok)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * kAccCols;
+                    if (!second) {
+                        unsigned long long left = plan.tokens[e];
+                        int r = 0;
+                        #pragma unroll 1
+                        for (int x = 0; x * 16 < g.tokens; ++x, left >>= 16) {
+                            if (!(left & 0xffffull)) continue;
+                            float v[16];
+                            tmem_ld16(base + x * 16, v);
+                            #pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (left >> j & 1ull) emit(r++, v[j]);
+                        }
+                    } else {
+                        #pragma unroll 1
+                        for (int x = 0; x * 8 < rows; ++x) {
+                            float v[16];
+                            tmem_ld16(base + x * 16, v);
+                            #pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (x * 8 + j < rows) emit(x * 8 + j, v[2 * j] + v[2 * j + 1]);
+                        }
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&c.t_empty[acc]));
+                    if (++acc == 2) { acc = 0; tp ^= 1; }
                 } else {
-                    for (int q = 0; q * 8 < rows; ++q) {
-                        float v[16];
-                        tmem_ld16(base + q * 16, v);
-                        #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (q * 8 + j < rows) emit(q * 8 + j, v[2 * j] + v[2 * j + 1]);
+                    const int groups = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+                    const uint8_t* rt = plan.row_token + r0;
+                    int nc;
+                    if (rows <= 2) {
+                        nc = 2;
+                        ok = products_f32<2>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, 1, red);
+                    } else if (rows <= 4) {
+                        nc = 4;
+                        ok = products_f32<4>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, 1, red);
+                    } else {
+                        nc = 8;
+                        ok = products_f32<8>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, groups, red);
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&c.t_empty[acc]));
-                if (++acc == 2) { acc = 0; tp ^= 1; }
-            } else {
-                const int groups = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
-                const uint8_t* rt = plan.row_token + r0;
-                bool ok;
-                int nc;
-                if (rows <= 2) {
-                    nc = 2;
-                    ok = products_f32<2>(g, c, s, rows, rt, a_ring, b_ring, as, ap, bs, bp, ew, lane, 1, red);
-                } else if (rows <= 4) {
-                    nc = 4;
-                    ok = products_f32<4>(g, c, s, rows, rt, a_ring, b_ring, as, ap, bs, bp, ew, lane, 1, red);
-                } else {
-                    nc = 8;
-                    ok = products_f32<8>(g, c, s, rows, rt, a_ring, b_ring, as, ap, bs, bp, ew, lane, groups, red);
-                }
-                if (!ok) few_abort(c, g.status);
-                if (!epilogue_all<NT>(ok)) { gone = true; break; }
-                const int cols = groups * nc;
-                for (int r = tid / kTileM; r < rows; r += NT / kTileM) {
-                    float v = 0.f;
-                    for (int q = 0; q < 8 / groups; ++q) v += red[(q * cols + r) * kTileM + i];
-                    emit(r, v);
-                }
-                epilogue_barrier<NT>();
-            }
-            if (s.phase == 0) {
-                bool finished = whole;
-                if (!whole) {
-                    // the last block to write its part adds the parts, in block order
-                    __threadfence();
+                    if (!ok) few_abort(c, g.status);
+                    if (!epilogue_all<NT>(ok)) { ok = false; break; }
+                    const int cols = groups * nc;
+                    for (int r = t_first; r < rows; r += STEP) {
+                        float v = 0.f;
+                        for (int x = 0; x < 8 / groups; ++x) v += red[(x * cols + r) * kTileM + i];
+                        emit(r, v);
+                    }
                     epilogue_barrier<NT>();
-                    if (tid == 0) c.last = atomicAdd(&g.cnt->joined[c0], 1) == c1 - c0;
-                    epilogue_barrier<NT>();
-                    finished = c.last;
-                    if (finished) {
+                }
+                const int m = s.m;
+                more = walk.next(plan, s);
+                if (!second) {
+                    bool finished = whole;
+                    if (!whole) {
+                        // the last share to write its part adds the parts, in their order
                         __threadfence();
-                        // eight rows at a time, so that their loads overlap
-                        for (int r = tid / kTileM; r < rows; r += 8 * (NT / kTileM)) {
-                            float v[8];
-                            #pragma unroll
-                            for (int u = 0; u < 8; ++u) v[u] = 0.f;
-                            for (int q = c0; q <= c1; ++q) {
-                                const float* from = g.part1 + (q * 2 + (q == c0)) * slot_floats + i;
+                        epilogue_barrier<NT>();
+                        if (tid == 0) c.last = atomicAdd(&g.cnt->joined[c0], 1) == c1 - c0;
+                        epilogue_barrier<NT>();
+                        finished = c.last;
+                        if (finished) {
+                            __threadfence();
+                            // eight rows at a time, so that their loads overlap
+                            #pragma unroll 1
+                            for (int r = t_first; r < rows; r += 8 * STEP) {
+                                float v[8];
                                 #pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const int rr = r + u * (NT / kTileM);
-                                    if (rr < rows) v[u] += __ldcg(from + rr * kTileM);
+                                for (int u = 0; u < 8; ++u) v[u] = 0.f;
+                                for (int x = c0; x <= c1; ++x) {
+                                    const float* from = g.part1 + (x * 2 + (x == c0)) * slot_floats + i;
+                                    #pragma unroll
+                                    for (int u = 0; u < 8; ++u)
+                                        if (r + u * STEP < rows) v[u] += __ldcg(from + (r + u * STEP) * kTileM);
                                 }
-                            }
-                            #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const int rr = r + u * (NT / kTileM);
-                                if (rr < rows) put_hidden(rr, v[u]);
+                                #pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    if (r + u * STEP < rows) put_hidden(r + u * STEP, v[u]);
                             }
                         }
                     }
+                    if (finished) {
+                        __threadfence();
+                        fence_proxy_async_all();
+                        epilogue_barrier<NT>();
+                        if (tid == 0) add_release(&g.cnt->done, 1);
+                    }
+                    continue;
                 }
-                if (finished) {
-                    __threadfence();
-                    fence_proxy_async_all();
-                    epilogue_barrier<NT>();
-                    if (tid == 0) add_release(&g.cnt->done, 1);
+                // second product: the tile is left when the next segment is another's
+                if (more && s.m == m) continue;
+                fresh = true;
+                const int d0 = walk.holder(plan, 0, m, 0);
+                const int d1 = walk.holder(plan, plan.nact - 1, m, walk.KB - 1);
+                if (!K::kTensor) epilogue_barrier<NT>();
+                if (d0 == d1) {
+                    for (int t = t_first; t < g.tokens && live; t += STEP)
+                        put_y((int64_t)t * g.d + col, yacc[t * kTileM + i]);
+                    continue;
                 }
-                more = walk.next(s);
-                continue;
+                float* out = g.part2 + (me * 2 + (me == d0)) * slot_floats;
+                for (int t = t_first; t < g.tokens; t += STEP)
+                    __stcg(out + t * kTileM + i, yacc[t * kTileM + i]);
+                __threadfence();
+                epilogue_barrier<NT>();
+                if (tid == 0) add_release(&g.tiles_done[m], 1);
             }
-            // second product: the tile is left when the next segment is another's
-            const int m = s.m;
-            more = walk.next(s);
-            if (more && s.m == m) continue;
-            fresh = true;
-            const int last = walk.p->nact - 1;
-            const int d0 = walk.holder(0, m, 0), d1 = walk.holder(last, m, walk.KB - 1);
-            if (!K::kTensor) epilogue_barrier<NT>();
-            if (d0 == d1) {
-                for (int t = tid / kTileM; t < g.tokens; t += NT / kTileM)
-                    put_y(t, m, yacc[t * kTileM + i]);
-                continue;
-            }
-            float* out = g.part2 + (me * 2 + (me == d0)) * slot_floats;
-            for (int t = tid / kTileM; t < g.tokens; t += NT / kTileM)
-                __stcg(out + t * kTileM + i, yacc[t * kTileM + i]);
-            __threadfence();
-            epilogue_barrier<NT>();
-            if (tid == 0) add_release(&g.tiles_done[m], 1);
-            if (n_a == 0) { m_a = m; d_a = d0; n_a = d1 - d0 + 1; }
-            else { m_b = m; d_b = d0; n_b = d1 - d0 + 1; }
-        }
-        // Tiles that several blocks have a part of: once all parts are there, each of
-        // those blocks adds them, in block order, for its share of the tokens.
-        for (int q = 0; q < 2 && !gone; ++q) {
-            const int m = q ? m_b : m_a, d0 = q ? d_b : d_a, n = q ? n_b : n_a;
-            if (n == 0) break;
-            const int lo = g.tokens * (me - d0) / n, hi = g.tokens * (me - d0 + 1) / n;
-            if (lo == hi) continue;
-            bool ok = true;
-            if (tid == 0) {
-                const uint64_t t0 = globaltimer_ns();
-                while (ok && load_acquire(&g.tiles_done[m]) < n)
-                    ok = !*(volatile int*)&c.abort_flag && globaltimer_ns() - t0 <= g.limit_ns;
-                if (!ok) few_abort(c, g.status);
-            }
-            if (!epilogue_all<NT>(ok)) break;
-            for (int t = lo + tid / kTileM; t < hi; t += NT / kTileM) {
-                const float* from = g.part2 + t * kTileM + i;
-                float v = __ldcg(from + (d0 * 2 + 1) * slot_floats);
-                #pragma unroll 8
-                for (int b = d0 + 1; b < d0 + n; ++b) v += __ldcg(from + b * 2 * slot_floats);
-                put_y(t, m, v);
-            }
+            if (!ok) break;
         }
     }
 
@@ -1350,12 +1470,14 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
     e = few_smem_limit<T>(&most);
     if (e != cudaSuccess) return e;
     const int rows = t * K::kRowsPerSlot;     // activation rows a K block can have
-    g.b_bytes = (rows + K::kBox - 1) / K::kBox * K::kBox * kBlockBytes;
+    const int slot = (rows + K::kBox - 1) / K::kBox * K::kBox * kBlockBytes;   // at most
     const int nc = t <= 2 ? 2 : t <= 4 ? 4 : 8;
     int left = most - 1024 - t * kTileM * 4 - (K::kTensor ? 0 : 8 * nc * kTileM * 4);
-    g.b_stages = g.b_bytes <= 4096 ? kMaxBStages : 4;
-    left -= g.b_stages * g.b_bytes;
+    g.b_ring = slot * (slot <= 4096 ? kMaxBStages : 4);
+    left -= g.b_ring;
     g.a_stages = left / kABytes < kMaxAStages ? left / kABytes : kMaxAStages;
+    g.slices = (few_blocks() + g.tiles2 - 1) / g.tiles2;
+    if (g.slices > t) g.slices = t;
     if (g.a_stages < 2) return cudaErrorInvalidConfiguration;
 
     CUtensorMap w1, mx, w2, mh;
@@ -1364,20 +1486,16 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
         !few_map<T>(&mh, g.hidden, s.f, (uint64_t)t * s.k * K::kRowsPerSlot, 0, K::kBox))
         return cudaErrorInvalidValue;
 
-    // Blocks wait for one another's hidden rows: a cooperative launch, so that all
-    // of them are resident.
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeCooperative;
-    at[0].val.cooperative = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)few_blocks());
     cfg.blockDim = dim3(few_threads<T>());
     cfg.dynamicSmemBytes = (size_t)most;
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, few_experts_kernel<T>, w1, mx, w2, mh, g);
 }
 

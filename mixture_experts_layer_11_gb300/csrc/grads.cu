@@ -232,7 +232,7 @@ template <typename T> __device__ __forceinline__ void scale_chunk(const Chunk& c
     #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
         const int j = threadIdx.x + i * kGradThreads;
-        if (j < nv) u[i] = q[j];
+        if (j < nv) u[i] = __ldcs(q + j);
     }
     #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
