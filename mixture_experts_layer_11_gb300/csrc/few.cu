@@ -393,7 +393,7 @@ constexpr int kMaxAStages = 12, kMaxBStages = 8;
 constexpr int kWarpsBeforeEpilogue = 4;
 // Times that decide whether the first product's units are cut: a K block of
 // weights when all blocks stream, when few do, and adding the parts of cut units.
-constexpr float kBlockNs = 366.f, kLoneBlockNs = 250.f, kJoinNs = 3000.f;
+constexpr float kBlockNs = 366.f, kLoneBlockNs = 250.f, kJoinNs = 4000.f;
 constexpr uint64_t kTakeOverNs = 20000;   // a share without a block for so long is taken over
 
 template <typename T> struct Kind;
@@ -424,6 +424,7 @@ struct Counters {
     int ticket;                  // few_direct_kernel: tasks handed out
     int claimed[2];              // shares of each product that a block has taken
     int sums;                    // summing tasks handed out
+    int gated;                   // tokens whose gate is in `slots`
     int claim[2][kMaxBlocks];    // 1: the share is taken
     int joined[kMaxBlocks];      // per share: parts of the unit that starts in it and ends in another
     // then per output tile: parts written
@@ -435,6 +436,7 @@ struct FewArgs {
     int slices;                           // summing tasks an output tile
     int a_stages, b_ring;                 // shared-memory rings: weights (stages), activations (bytes)
     const float* logits;
+    float2* slots;         // [T k]: expert (as bits) and gate weight
     const void *b1, *b2, *residual;
     void* y;
     void* hidden;          // [T k kRowsPerSlot][f]
@@ -465,9 +467,9 @@ struct Sorted {
 
 // Relative time of one K block with `rows` activation rows: the bytes of the
 // weights, unless fp32 products take longer.
-constexpr int kMaxCost = 10;
+constexpr int kMaxCost = 17;
 template <typename T> __device__ __forceinline__ int block_cost(int rows) {
-    return sizeof(T) == 2 ? 1 : rows <= 16 ? 3 : rows <= 32 ? 5 : kMaxCost;
+    return sizeof(T) == 2 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : rows <= 32 ? 9 : kMaxCost;
 }
 
 // One block's consecutive K blocks of one (expert, tile).
@@ -503,7 +505,7 @@ struct Walk {
         const int x = line(p, a_, m_, kb_), cut = longer * (size + 1);
         return x < cut ? x / (size + 1) : longer + (x - cut) / size;
     }
-    __device__ void cut(const FewArgs& g, const Sorted& p, int product) {
+    template <typename T> __device__ void cut(const FewArgs& g, const Sorted& p, int product) {
         phase = product;
         tiles = product == kFirst ? g.tiles1 : g.tiles2;
         KB = product == kFirst ? g.KB1 : g.KB2;
@@ -511,10 +513,13 @@ struct Walk {
         const int units = nact * tiles;
         whole = false;
         if (product == kFirst) {
-            const int rounds = (units + grid - 1) / grid;
-            const float all = (float)units / (float)grid * kBlockNs;     // a K block of every unit
-            const float each = units < grid ? fmaxf(all, kLoneBlockNs) : kBlockNs;
-            whole = rounds * each * KB <= all * KB + kJoinNs;
+            // whole units: full rounds, and one of `rest` blocks that share the memory's
+            // bandwidth; cut units: all blocks all the time, and the adding of parts
+            const int full = units / grid, rest = units - full * grid;
+            const float ns = kBlockNs * (float)p.most / (float)block_cost<T>(1);
+            const float last = rest ? fmaxf(1.25f * ns * (float)rest / (float)grid, kLoneBlockNs * ns / kBlockNs) : 0.f;
+            whole = (float)KB * ((float)full * ns + last) <=
+                    (float)(KB * tiles) * (float)p.cost[nact] / (float)(grid * block_cost<T>(1)) * kBlockNs + kJoinNs;
         }
         const int total = whole ? units : p.cost[nact] * tiles * KB;
         // no share is shorter than a K block: each holds the beginning of one
@@ -592,13 +597,53 @@ struct Plan : Sorted {
     Walk first, second;
 };
 
+// The gate of all tokens.  More tokens than the block's warps do in two turns are
+// shared out, one to a block (measured for 64 tokens: 10 us for a block that does
+// them all, 4 so); a block that another's result does not reach soon, because
+// that block is not running, does them all.
+__device__ __forceinline__ void gate_plan(Sorted& p, const FewArgs& g) {
+    __shared__ int there;
+    const int tokens = g.tokens, k = g.k, warps = blockDim.x >> 5;
+    int32_t* status = blockIdx.x == 0 ? g.status : nullptr;
+    if (tokens > 2 * warps && (int)gridDim.x >= tokens) {
+        const int t = (int)blockIdx.x;
+        if (t < tokens && threadIdx.x < 32) {
+            gate_tokens(g.logits + t * g.E, 1, g.E, k, g.renorm, p.e_of, p.w, g.status);
+            __syncwarp();
+            if ((int)threadIdx.x < k)
+                __stcg(&g.slots[t * k + threadIdx.x],
+                       make_float2(__int_as_float(p.e_of[threadIdx.x]), p.w[threadIdx.x]));
+            __threadfence();
+            __syncwarp();
+            if (threadIdx.x == 0) add_release(&g.cnt->gated, 1);
+        }
+        if (threadIdx.x == 0) {
+            const uint64_t t0 = globaltimer_ns();
+            int n;
+            do n = load_acquire(&g.cnt->gated);
+            while (n < tokens && globaltimer_ns() - t0 < kTakeOverNs);
+            there = n >= tokens;
+        }
+        __syncthreads();
+        if (there) {
+            for (int i = threadIdx.x; i < tokens * k; i += blockDim.x) {
+                const float2 v = __ldcg(&g.slots[i]);
+                p.e_of[i] = (uint8_t)__float_as_int(v.x);
+                p.w[i] = v.y;
+            }
+            return;
+        }
+    }
+    gate_tokens(g.logits, tokens, g.E, k, g.renorm, p.e_of, p.w, status);
+}
+
 // Called by all threads of a block of at least 256.
 template <typename T>
 __device__ __forceinline__ void make_plan(Plan& p, const FewArgs& g) {
     const int tokens = g.tokens, k = g.k, E = g.E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < E; e += blockDim.x) p.tokens[e] = 0ull;
-    gate_tokens(g.logits, tokens, E, k, g.renorm, p.e_of, p.w, blockIdx.x == 0 ? g.status : nullptr);
+    gate_plan(p, g);
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * k; i += blockDim.x)
         atomicOr(&p.tokens[p.e_of[i]], 1ull << (i / k));
@@ -650,7 +695,7 @@ __device__ __forceinline__ void make_plan(Plan& p, const FewArgs& g) {
         p.row_token[r] = (uint8_t)t;
         p.row_w[r] = p.w[i];
     }
-    if (lane == 0 && warp >= 6 && warp < 8) (warp == 6 ? p.first : p.second).cut(g, p, warp - 6);
+    if (lane == 0 && warp >= 6 && warp < 8) (warp == 6 ? p.first : p.second).template cut<T>(g, p, warp - 6);
     __syncthreads();
 }
 
@@ -731,12 +776,12 @@ struct Reader {
 // activation rows.  With more than NC rows the warps split them into `groups`
 // (1, 2, 4 or 8) and K into 8 / groups; sums run over even and odd k apart, as
 // packed pairs.  The result goes to red[K slice][row][128].
-template <int NC>
+template <int NC, int GROUPS>
 __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const Seg& s, bool first,
                                              int rows, const uint8_t* row_token, uint8_t* a_ring,
                                              int& as, uint32_t& ap, Ring& b, int ew, int lane,
-                                             int groups, float* red) {
-    const int grp = ew % groups, slice = ew / groups;
+                                             float* red) {
+    const int grp = ew % GROUPS, slice = ew / GROUPS;
     uint32_t brow[NC];
     #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -755,8 +800,9 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
             return false;
         const uint8_t* A = a_ring + as * kABytes;
         const uint8_t* B = b.at();
-        for (int i = 0; i < groups; ++i) {
-            const int ch = slice * groups + i;   // 16-byte chunk of the K block
+        #pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            const int ch = slice * GROUPS + i;   // 16-byte chunk of the K block
             ulonglong2 a[4];
             #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -785,7 +831,7 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
         for (int q = 0; q < 4; ++q) {
             float e, o;
             f2_unpack(acc[q][j], e, o);
-            red[((slice * groups + grp) * NC + j) * kTileM + lane + 32 * q] = e + o;
+            red[((slice * GROUPS + grp) * NC + j) * kTileM + lane + 32 * q] = e + o;
         }
     return true;
 }
@@ -1117,20 +1163,44 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                 // four columns a thread
                 const int col = (tid & 31) * 4;
                 if (m * kTileM + col >= g.d) continue;
-                #pragma unroll 2
-                for (int t = lo + ew; t < hi; t += NT / 32) {
-                    const float* from = g.part2 + t * kTileM + col;
-                    float4 v = __ldcg(reinterpret_cast<const float4*>(from + (d0 * 2 + 1) * slot_floats));
-                    #pragma unroll 4
-                    for (int b = d0 + 1; b <= d1; ++b) {
-                        const float4 u = __ldcg(reinterpret_cast<const float4*>(from + b * 2 * slot_floats));
-                        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+                // two tokens and six parts at a time, so that their loads overlap
+                constexpr int TB = 2, PB = 6;
+                #pragma unroll 1
+                for (int t = lo + ew; t < hi; t += TB * (NT / 32)) {
+                    float4 v[TB];
+                    #pragma unroll
+                    for (int x = 0; x < TB; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    #pragma unroll 1
+                    for (int b = d0; b <= d1; b += PB) {
+                        float4 u[TB][PB];
+                        #pragma unroll
+                        for (int x = 0; x < TB; ++x)
+                            #pragma unroll
+                            for (int j = 0; j < PB; ++j) {
+                                const int tt = t + x * (NT / 32), bb = b + j;
+                                u[x][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (tt < hi && bb <= d1)
+                                    u[x][j] = __ldcg(reinterpret_cast<const float4*>(
+                                        g.part2 + (bb * 2 + (bb == d0)) * slot_floats + tt * kTileM + col));
+                            }
+                        #pragma unroll
+                        for (int x = 0; x < TB; ++x)
+                            #pragma unroll
+                            for (int j = 0; j < PB; ++j) {
+                                v[x].x += u[x][j].x; v[x].y += u[x][j].y;
+                                v[x].z += u[x][j].z; v[x].w += u[x][j].w;
+                            }
                     }
-                    const int64_t o = (int64_t)t * g.d + m * kTileM + col;
-                    put_y(o, v.x);
-                    put_y(o + 1, v.y);
-                    put_y(o + 2, v.z);
-                    put_y(o + 3, v.w);
+                    #pragma unroll
+                    for (int x = 0; x < TB; ++x) {
+                        const int tt = t + x * (NT / 32);
+                        if (tt >= hi) break;
+                        const int64_t o = (int64_t)tt * g.d + m * kTileM + col;
+                        put_y(o, v[x].x);
+                        put_y(o + 1, v[x].y);
+                        put_y(o + 2, v[x].z);
+                        put_y(o + 3, v[x].w);
+                    }
                 }
                 continue;
             }
@@ -1217,18 +1287,18 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     if (++acc == 2) { acc = 0; tp ^= 1; }
                 } else {
                     const int groups = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+                    const int nc = rows <= 4 ? 4 : 8;
                     const uint8_t* rt = plan.row_token + r0;
-                    int nc;
-                    if (rows <= 2) {
-                        nc = 2;
-                        ok = products_f32<2>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, 1, red);
-                    } else if (rows <= 4) {
-                        nc = 4;
-                        ok = products_f32<4>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, 1, red);
-                    } else {
-                        nc = 8;
-                        ok = products_f32<8>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, groups, red);
-                    }
+                    if (rows <= 4)
+                        ok = products_f32<4, 1>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                    else if (rows <= 8)
+                        ok = products_f32<8, 1>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                    else if (rows <= 16)
+                        ok = products_f32<8, 2>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                    else if (rows <= 32)
+                        ok = products_f32<8, 4>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                    else
+                        ok = products_f32<8, 8>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
                     if (!ok) few_abort(c, g.status);
                     if (!epilogue_all<NT>(ok)) { ok = false; break; }
                     const int cols = groups * nc;
@@ -1289,9 +1359,10 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                         put_y((int64_t)t * g.d + col, yacc[t * kTileM + i]);
                     continue;
                 }
-                float* out = g.part2 + (me * 2 + (me == d0)) * slot_floats;
-                for (int t = t_first; t < g.tokens; t += STEP)
-                    __stcg(out + t * kTileM + i, yacc[t * kTileM + i]);
+                float4* out = reinterpret_cast<float4*>(g.part2 + (me * 2 + (me == d0)) * slot_floats);
+                if (K::kTensor) epilogue_barrier<NT>();
+                for (int x = tid; x < g.tokens * (kTileM / 4); x += NT)
+                    __stcg(out + x, reinterpret_cast<const float4*>(yacc)[x]);
                 __threadfence();
                 epilogue_barrier<NT>();
                 if (tid == 0) add_release(&g.tiles_done[m], 1);
@@ -1318,7 +1389,7 @@ int few_blocks() {
 }
 
 struct FewLayout {
-    size_t logits, counters, hidden, part1, part2, total;
+    size_t logits, slots, counters, hidden, part1, part2, total;
 };
 FewLayout few_layout(const moe_shape& s) {
     FewLayout l;
@@ -1326,6 +1397,7 @@ FewLayout few_layout(const moe_shape& s) {
     auto take = [&](size_t n) { const size_t a = at; at += pad256(n); return a; };
     const size_t part = sizeof(float) * few_blocks() * 2 * s.T * kTileM;
     l.logits = take(sizeof(float) * s.T * s.E);
+    l.slots = take(sizeof(float2) * s.T * s.k);
     l.counters = take(sizeof(Counters) + sizeof(int) * ((s.d + kTileM - 1) / kTileM));
     l.hidden = take((size_t)4 * s.T * s.k * s.f);   // fp32, or two bf16 parts
     l.part1 = take(part);
@@ -1434,6 +1506,7 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
     g.KB1 = (s.d + KBlock - 1) / KBlock;
     g.KB2 = (s.f + KBlock - 1) / KBlock;
     g.logits = (float*)(ws + l.logits);
+    g.slots = (float2*)(ws + l.slots);
     g.b1 = p.b1; g.b2 = p.b2; g.residual = residual; g.y = y;
     g.hidden = ws + l.hidden;
     g.part1 = (float*)(ws + l.part1);
@@ -1471,13 +1544,13 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
     if (e != cudaSuccess) return e;
     const int rows = t * K::kRowsPerSlot;     // activation rows a K block can have
     const int slot = (rows + K::kBox - 1) / K::kBox * K::kBox * kBlockBytes;   // at most
-    const int nc = t <= 2 ? 2 : t <= 4 ? 4 : 8;
+    const int nc = t <= 4 ? 4 : 8;
     int left = most - 1024 - t * kTileM * 4 - (K::kTensor ? 0 : 8 * nc * kTileM * 4);
     g.b_ring = slot * (slot <= 4096 ? kMaxBStages : 4);
     left -= g.b_ring;
     g.a_stages = left / kABytes < kMaxAStages ? left / kABytes : kMaxAStages;
-    g.slices = (few_blocks() + g.tiles2 - 1) / g.tiles2;
-    if (g.slices > t) g.slices = t;
+    g.slices = few_blocks() / g.tiles2;
+    g.slices = g.slices < 1 ? 1 : g.slices > t ? t : g.slices;
     if (g.a_stages < 2) return cudaErrorInvalidConfiguration;
 
     CUtensorMap w1, mx, w2, mh;
