@@ -701,7 +701,7 @@ __device__ __forceinline__ void make_plan(Plan& p, const FewArgs& g) {
 
 struct FewCtrl {
     uint64_t a_full[kMaxAStages], a_empty[kMaxAStages];
-    uint64_t b_full[2][kMaxBStages], b_empty[2][kMaxBStages];   // of each product
+    uint64_t b_full[2][kMaxBStages];   // of each product
     uint64_t t_full[2], t_empty[2], drain;
     uint64_t q_full[2], q_empty[2];
     Walk queue[2];         // what the block's roles work on next
@@ -740,26 +740,29 @@ template <int N> __device__ __forceinline__ bool epilogue_all(bool ok) {
 }
 
 // The activations' ring.  A K block's slot is as large as the product needs, so
-// each product has its own number of stages in the same memory, and its own
-// barriers.
+// each product has its own number of slots in the same memory, and its own
+// barriers for their filling.  What empties a slot is the K block's weights'
+// stage being emptied (one completion for both): there are no more slots than
+// stages, so that the stage is not in use again before the slot's next K block.
 struct Ring {
-    uint8_t* base;
-    uint64_t *full, *empty;
-    int stages, bytes;     // slots, bytes of one
-    int stage;
+    uint32_t base, full;   // shared addresses of the slots and their barriers
+    int slots, bytes;
+    int slot;
     uint32_t parity;
-    __device__ void set(FewCtrl& c, uint8_t* memory, int size, int product, int rows, int box) {
-        base = memory;
-        full = c.b_full[product];
-        empty = c.b_empty[product];
+    __device__ void set(FewCtrl& c, const FewArgs& g, uint8_t* memory, int product, int rows, int box) {
+        base = smem_u32(memory);
+        full = smem_u32(c.b_full[product]);
         bytes = (rows + box - 1) / box * box * kBlockBytes;
-        stages = size / bytes < kMaxBStages ? size / bytes : kMaxBStages;
-        stage = 0;
+        slots = g.b_ring / bytes;
+        slots = slots < kMaxBStages ? slots : kMaxBStages;
+        slots = slots < g.a_stages ? slots : g.a_stages;
+        slot = 0;
         parity = 0;
     }
-    __device__ uint8_t* at() const { return base + stage * bytes; }
+    __device__ uint32_t at() const { return base + slot * bytes; }
+    __device__ uint32_t bar() const { return full + slot * 8; }
     __device__ void step() {
-        if (++stage == stages) { stage = 0; parity ^= 1; }
+        if (++slot == slots) { slot = 0; parity ^= 1; }
     }
 };
 
@@ -778,7 +781,8 @@ struct Reader {
 // packed pairs.  The result goes to red[K slice][row][128].
 template <int NC, int GROUPS>
 __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const Seg& s, bool first,
-                                             int rows, const uint8_t* row_token, uint8_t* a_ring,
+                                             int rows, const uint8_t* row_token,
+                                             const uint8_t* a_ring, const uint8_t* b_ring,
                                              int& as, uint32_t& ap, Ring& b, int ew, int lane,
                                              float* red) {
     const int grp = ew % GROUPS, slice = ew / GROUPS;
@@ -796,10 +800,10 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
         for (int j = 0; j < NC; ++j) acc[q][j] = 0ull;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
         if (!mbar_wait_warp(smem_u32(&c.a_full[as]), ap, g.limit_ns, &c.abort_flag) ||
-            !mbar_wait_warp(smem_u32(&b.full[b.stage]), b.parity, g.limit_ns, &c.abort_flag))
+            !mbar_wait_warp(b.bar(), b.parity, g.limit_ns, &c.abort_flag))
             return false;
         const uint8_t* A = a_ring + as * kABytes;
-        const uint8_t* B = b.at();
+        const uint8_t* B = b_ring + b.slot * b.bytes;
         #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
             const int ch = slice * GROUPS + i;   // 16-byte chunk of the K block
@@ -818,10 +822,7 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
             }
         }
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(smem_u32(&c.a_empty[as]));
-            mbar_arrive(smem_u32(&b.empty[b.stage]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&c.a_empty[as]));
         if (++as == g.a_stages) { as = 0; ap ^= 1; }
         b.step();
     }
@@ -863,7 +864,6 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
         #pragma unroll 1
         for (int i = 0; i < 2 * kMaxBStages; ++i) {
             mbar_init(smem_u32(&c.b_full[i / kMaxBStages][i % kMaxBStages]), 1);
-            mbar_init(smem_u32(&c.b_empty[i / kMaxBStages][i % kMaxBStages]), consumers);
         }
         #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
@@ -998,27 +998,21 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
         // ---- activations: all tokens' K block of x, or the expert's hidden rows -------
         if (lane == 0) {
             Ring r;
-            r.set(c, b_ring, g.b_ring, kFirst, g.tokens, BOX);
-            int issued = 0;
+            r.set(c, g, b_ring, kFirst, g.tokens, BOX);
+            int issued = 0, st = 0;        // st, ph: weights' stage to wait for next
+            uint32_t ph = 0;
             bool second = false, ok = true;
-            // copies in flight land before the memory is put to another use
-            auto drain = [&]() {
-                for (int i = 0; i < issued; ++i) {
-                    if (--r.stage < 0) { r.stage = r.stages - 1; r.parity ^= 1; }
-                    mbar_wait_bounded(smem_u32(&r.full[r.stage]), r.parity, g.limit_ns, nullptr);
-                }
-                issued = 0;
+            auto emptied = [&]() {         // the oldest K block not yet waited for
+                ok = mbar_wait_bounded(smem_u32(&c.a_empty[st]), ph, g.limit_ns, &c.abort_flag);
+                if (!ok) few_abort(c, g.status);
+                if (++st == g.a_stages) { st = 0; ph ^= 1; }
+                --issued;
             };
             while (ok && take()) {
                 if (walk.phase == kSum) continue;
                 if (walk.phase == kSecond && !second) {
                     second = true;
-                    // every slot of the first product's ring has been read
-                    for (int i = 0; i < r.stages && ok; ++i) {
-                        ok = mbar_wait_bounded(smem_u32(&r.empty[r.stage]), r.parity ^ 1, g.limit_ns,
-                                               &c.abort_flag);
-                        r.step();
-                    }
+                    while (ok && issued > 0) emptied();   // the first product's slots are free
                     // All hidden rows are written.  (One counter for all experts: the
                     // shares are equal, so that waiting for some of them first gains nothing,
                     // and each further poll would cost a round trip to the L2.)
@@ -1030,8 +1024,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                         break;
                     }
                     fence_proxy_async_all();
-                    issued = 0;
-                    r.set(c, b_ring, g.b_ring, kSecond, plan.most_rows * RPS, BOX);
+                    r.set(c, g, b_ring, kSecond, plan.most_rows * RPS, BOX);
                 }
                 while (ok && walk.next(plan, s)) {
                     const int e = plan.act[s.a];
@@ -1040,66 +1033,71 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     const int boxes = (rows + BOX - 1) / BOX;
                     const CUtensorMap* map = second ? &mapH : &mapX;
                     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-                        const uint32_t full = smem_u32(&r.full[r.stage]);
-                        if (!mbar_wait_bounded(smem_u32(&r.empty[r.stage]), r.parity ^ 1, g.limit_ns,
-                                               &c.abort_flag)) {
-                            few_abort(c, g.status);
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(full, boxes * BOX * kBlockBytes);
+                        if (issued == r.slots) emptied();
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(r.bar(), boxes * BOX * kBlockBytes);
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(smem_u32(r.at() + i * BOX * kBlockBytes), map, full,
-                                        kb * K::kBlock, row0 + i * BOX);
-                        if (issued < r.stages) ++issued;
+                            tma_load_2d(r.at() + i * BOX * kBlockBytes, map, r.bar(), kb * K::kBlock,
+                                        row0 + i * BOX);
+                        ++issued;
                         r.step();
                     }
                 }
             }
-            drain();
+            // copies in flight land before the block ends
+            for (int i = 0; i < issued; ++i) {
+                if (--r.slot < 0) { r.slot = r.slots - 1; r.parity ^= 1; }
+                mbar_wait_bounded(r.bar(), r.parity, g.limit_ns, nullptr);
+            }
         }
         __syncwarp();
     } else if (K::kTensor && warp == 2) {
         // ---- tensor core: D[128 weight rows][activation rows], one accumulator a segment --
         if (lane == 0) {
+            // One thread: between two K blocks it does as little as it can (the low words
+            // of the operands' descriptors move by the stage; the high words are alike).
             Ring r;
-            r.set(c, b_ring, g.b_ring, kFirst, g.tokens, BOX);
+            r.set(c, g, b_ring, kFirst, g.tokens, BOX);
             int as = 0, acc = 0;
             uint32_t ap = 0, tp = 0;
             bool second = false, ok = true;
+            const uint64_t a0 = smem_desc_sw128(smem_u32(a_ring), 16, 1024);
+            const uint64_t b0 = smem_desc_sw128(r.base, 16, 1024);
+            const uint32_t a_full = smem_u32(c.a_full), a_empty = smem_u32(c.a_empty);
             while (ok && take()) {
                 if (walk.phase == kSum) continue;
                 if (walk.phase == kSecond && !second) {
                     second = true;
-                    r.set(c, b_ring, g.b_ring, kSecond, plan.most_rows * RPS, BOX);
+                    r.set(c, g, b_ring, kSecond, plan.most_rows * RPS, BOX);
                 }
                 while (ok && walk.next(plan, s)) {
                     const int e = plan.act[s.a];
                     const int rows = second ? (plan.off[e + 1] - plan.off[e]) * RPS : g.tokens;
                     const uint32_t idesc = idesc_bf16_f32(kTileM, (rows + 15) & ~15, false, false);
+                    const uint32_t d_tmem = tmem + acc * kAccCols;
                     if (!mbar_wait_bounded(smem_u32(&c.t_empty[acc]), tp ^ 1, g.limit_ns, &c.abort_flag)) {
                         few_abort(c, g.status);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    for (int kb = s.kb0; kb < s.kb1; ++kb) {
-                        if (!mbar_wait_bounded(smem_u32(&c.a_full[as]), ap, g.limit_ns, &c.abort_flag) ||
-                            !mbar_wait_bounded(smem_u32(&r.full[r.stage]), r.parity, g.limit_ns,
-                                               &c.abort_flag)) {
+                    uint32_t more = 0;
+                    for (int n = s.kb1 - s.kb0; n > 0; --n) {
+                        if (!mbar_wait_bounded(a_full + as * 8, ap, g.limit_ns, &c.abort_flag) ||
+                            !mbar_wait_bounded(r.bar(), r.parity, g.limit_ns, &c.abort_flag)) {
                             few_abort(c, g.status);
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t ad = smem_desc_sw128(smem_u32(a_ring + as * kABytes), 16, 1024);
-                        const uint64_t bd = smem_desc_sw128(smem_u32(r.at()), 16, 1024);
+                        const uint64_t ad = a0 + as * (kABytes >> 4);
+                        const uint64_t bd = b0 + r.slot * (r.bytes >> 4);
                         #pragma unroll
-                        for (int kk = 0; kk < K::kBlock / 16; ++kk)
-                            tc_mma_bf16(tmem + acc * kAccCols, ad + kk * 2, bd + kk * 2, idesc,
-                                        kb > s.kb0 || kk > 0);
-                        tc_commit(smem_u32(&c.a_empty[as]));
-                        tc_commit(smem_u32(&r.empty[r.stage]));
+                        for (int kk = 0; kk < K::kBlock / 16; ++kk) {
+                            tc_mma_bf16(d_tmem, ad + kk * 2, bd + kk * 2, idesc, more);
+                            more = 1;
+                        }
+                        tc_commit(a_empty + as * 8);
                         if (++as == g.a_stages) { as = 0; ap ^= 1; }
                         r.step();
                     }
@@ -1128,7 +1126,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
         int acc = 0, as = 0;
         uint32_t tp = 0, ap = 0;
         Ring ring;
-        if (!K::kTensor) ring.set(c, b_ring, g.b_ring, kFirst, g.tokens, BOX);
+        if (!K::kTensor) ring.set(c, g, b_ring, kFirst, g.tokens, BOX);
         bool second = false, ok = true;
         auto put_y = [&](int64_t o, float v) {
             if (residual) v += to_f32<T>(residual[o]);
@@ -1206,7 +1204,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
             }
             if (walk.phase == kSecond && !second) {
                 second = true;
-                if (!K::kTensor) ring.set(c, b_ring, g.b_ring, kSecond, plan.most_rows * RPS, BOX);
+                if (!K::kTensor) ring.set(c, g, b_ring, kSecond, plan.most_rows * RPS, BOX);
             }
             bool fresh = true;     // yacc holds nothing yet
             bool more = walk.next(plan, s);
@@ -1290,15 +1288,15 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     const int nc = rows <= 4 ? 4 : 8;
                     const uint8_t* rt = plan.row_token + r0;
                     if (rows <= 4)
-                        ok = products_f32<4, 1>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<4, 1>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
                     else if (rows <= 8)
-                        ok = products_f32<8, 1>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 1>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
                     else if (rows <= 16)
-                        ok = products_f32<8, 2>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 2>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
                     else if (rows <= 32)
-                        ok = products_f32<8, 4>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 4>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
                     else
-                        ok = products_f32<8, 8>(g, c, s, !second, rows, rt, a_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 8>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
                     if (!ok) few_abort(c, g.status);
                     if (!epilogue_all<NT>(ok)) { ok = false; break; }
                     const int cols = groups * nc;
