@@ -201,6 +201,13 @@ __device__ __forceinline__ int load_acquire(const int* p) {
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+// Writes of the block's other threads that a barrier has ordered before these two
+// are published with them, as the calling thread's own are.
+__device__ __forceinline__ int add_acq_rel(int* p, int v) {
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
 __device__ __forceinline__ void add_release(int* p, int v) {
     asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -376,7 +383,6 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
                     ((T*)g.y)[o] = from_f32<T>(v);
                 }
             }
-            if (one) __threadfence();
         }
         if (threadIdx.x == 0) next = claimed;
         __syncthreads();
@@ -393,7 +399,7 @@ constexpr int kMaxAStages = 12, kMaxBStages = 8;
 constexpr int kWarpsBeforeEpilogue = 4;
 // Times that decide whether the first product's units are cut: a K block of
 // weights when all blocks stream, when few do, and adding the parts of cut units.
-constexpr float kBlockNs = 366.f, kLoneBlockNs = 250.f, kJoinNs = 4000.f;
+constexpr float kBlockNs = 366.f, kLoneBlockNs = 280.f, kJoinNs = 2000.f;
 constexpr uint64_t kTakeOverNs = 20000;   // a share without a block for so long is taken over
 
 template <typename T> struct Kind;
@@ -613,7 +619,6 @@ __device__ __forceinline__ void gate_plan(Sorted& p, const FewArgs& g) {
             if ((int)threadIdx.x < k)
                 __stcg(&g.slots[t * k + threadIdx.x],
                        make_float2(__int_as_float(p.e_of[threadIdx.x]), p.w[threadIdx.x]));
-            __threadfence();
             __syncwarp();
             if (threadIdx.x == 0) add_release(&g.cnt->gated, 1);
         }
@@ -1226,6 +1231,33 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     if (!K::kTensor) epilogue_barrier<NT>();
                     fresh = false;
                 }
+                // The share that a cut unit starts in comes to it last, and mostly finds the
+                // others' parts written: then it adds them up (in yacc, which the first
+                // product does not use) while the tensor core works on its own.
+                bool rest = false;
+                if (!second && !whole && me == c0) {
+                    if (tid == 0) rest = load_acquire(&g.cnt->joined[c0]) == c1 - c0;
+                    rest = epilogue_all<NT>(tid != 0 || rest);
+                    if (rest) {
+                        // eight rows at a time, so that their loads overlap
+                        #pragma unroll 1
+                        for (int r = t_first; r < rows; r += 8 * STEP) {
+                            float v[8];
+                            #pragma unroll
+                            for (int u = 0; u < 8; ++u) v[u] = 0.f;
+                            #pragma unroll 1
+                            for (int x = c0 + 1; x <= c1; ++x) {
+                                const float* from = g.part1 + x * 2 * slot_floats + i;
+                                #pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    if (r + u * STEP < rows) v[u] += __ldcg(from + (r + u * STEP) * kTileM);
+                            }
+                            #pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                if (r + u * STEP < rows) yacc[(r + u * STEP) * kTileM + i] = v[u];
+                        }
+                    }
+                }
                 auto put_hidden = [&](int r, float h) {
                     if (!live) return;
                     if constexpr (K::kTensor) {
@@ -1247,6 +1279,8 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                         *p = fmaf(plan.row_w[r0 + r], v, *p);
                     } else if (whole) {
                         put_hidden(r, v);
+                    } else if (rest) {
+                        put_hidden(r, v + yacc[r * kTileM + i]);
                     } else {
                         __stcg(mine + r * kTileM + i, v);
                     }
@@ -1310,39 +1344,41 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                 const int m = s.m;
                 more = walk.next(plan, s);
                 if (!second) {
-                    bool finished = whole;
-                    if (!whole) {
+                    bool finished = whole || rest;
+                    if (!finished) {
                         // the last share to write its part adds the parts, in their order
-                        __threadfence();
                         epilogue_barrier<NT>();
-                        if (tid == 0) c.last = atomicAdd(&g.cnt->joined[c0], 1) == c1 - c0;
+                        if (tid == 0) c.last = add_acq_rel(&g.cnt->joined[c0], 1) == c1 - c0;
                         epilogue_barrier<NT>();
                         finished = c.last;
                         if (finished) {
-                            __threadfence();
-                            // eight rows at a time, so that their loads overlap
                             #pragma unroll 1
                             for (int r = t_first; r < rows; r += 8 * STEP) {
-                                float v[8];
+                                float v[8], own[8];
                                 #pragma unroll
-                                for (int u = 0; u < 8; ++u) v[u] = 0.f;
+                                for (int u = 0; u < 8; ++u) v[u] = own[u] = 0.f;
+                                #pragma unroll 1
                                 for (int x = c0; x <= c1; ++x) {
                                     const float* from = g.part1 + (x * 2 + (x == c0)) * slot_floats + i;
                                     #pragma unroll
                                     for (int u = 0; u < 8; ++u)
-                                        if (r + u * STEP < rows) v[u] += __ldcg(from + (r + u * STEP) * kTileM);
+                                        if (r + u * STEP < rows) {
+                                            const float part = __ldcg(from + (r + u * STEP) * kTileM);
+                                            if (x == c0) own[u] = part; else v[u] += part;
+                                        }
                                 }
                                 #pragma unroll
                                 for (int u = 0; u < 8; ++u)
-                                    if (r + u * STEP < rows) put_hidden(r + u * STEP, v[u]);
+                                    if (r + u * STEP < rows) put_hidden(r + u * STEP, own[u] + v[u]);
                             }
                         }
                     }
                     if (finished) {
-                        __threadfence();
-                        fence_proxy_async_all();
                         epilogue_barrier<NT>();
-                        if (tid == 0) add_release(&g.cnt->done, 1);
+                        if (tid == 0) {
+                            fence_proxy_async_all();   // the rows are read by TMA
+                            add_release(&g.cnt->done, 1);
+                        }
                     }
                     continue;
                 }
@@ -1361,7 +1397,6 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                 if (K::kTensor) epilogue_barrier<NT>();
                 for (int x = tid; x < g.tokens * (kTileM / 4); x += NT)
                     __stcg(out + x, reinterpret_cast<const float4*>(yacc)[x]);
-                __threadfence();
                 epilogue_barrier<NT>();
                 if (tid == 0) add_release(&g.tiles_done[m], 1);
             }
