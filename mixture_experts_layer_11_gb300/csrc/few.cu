@@ -729,6 +729,24 @@ template <int N> __device__ __forceinline__ void epilogue_barrier() {
     asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
+// Columns of this thread's TMEM lane: four in a row, or any two.
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, float (&v)[4]) {
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_pair(uint32_t addr0, uint32_t addr1, float& a, float& b) {
+    uint32_t r0, r1;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r0) : "r"(addr0));
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r1) : "r"(addr1));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    a = __uint_as_float(r0);
+    b = __uint_as_float(r1);
+}
+
 // a barrier that also says whether `ok` holds on every thread: the epilogue goes
 // on or gives up as one
 template <int N> __device__ __forceinline__ bool epilogue_all(bool ok) {
@@ -1137,6 +1155,26 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
             if (residual) v += to_f32<T>(residual[o]);
             y[o] = from_f32<T>(v);
         };
+        auto put_y4 = [&](int64_t o, float4 v) {   // four columns (o is a multiple of four)
+            if constexpr (K::kTensor) {
+                if (residual) {
+                    const uint2 q = *reinterpret_cast<const uint2*>(residual + o);
+                    v.x += __uint_as_float(q.x << 16);
+                    v.y += __uint_as_float(q.x & 0xffff0000u);
+                    v.z += __uint_as_float(q.y << 16);
+                    v.w += __uint_as_float(q.y & 0xffff0000u);
+                }
+                const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+                *reinterpret_cast<uint2*>(y + o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                              *reinterpret_cast<const uint32_t*>(&b));
+            } else {
+                if (residual) {
+                    const float4 q = *reinterpret_cast<const float4*>(residual + o);
+                    v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+                }
+                *reinterpret_cast<float4*>(y + o) = v;
+            }
+        };
         while (true) {
             ok = mbar_wait_warp(smem_u32(&c.q_full[q.slot]), q.parity, g.limit_ns, &c.abort_flag);
             if (!ok) few_abort(c, g.status);
@@ -1166,44 +1204,26 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                 // four columns a thread
                 const int col = (tid & 31) * 4;
                 if (m * kTileM + col >= g.d) continue;
-                // two tokens and six parts at a time, so that their loads overlap
-                constexpr int TB = 2, PB = 6;
+                constexpr int PB = 8;   // parts at a time, so that their loads overlap
                 #pragma unroll 1
-                for (int t = lo + ew; t < hi; t += TB * (NT / 32)) {
-                    float4 v[TB];
-                    #pragma unroll
-                    for (int x = 0; x < TB; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int t = lo + ew; t < hi; t += NT / 32) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     #pragma unroll 1
                     for (int b = d0; b <= d1; b += PB) {
-                        float4 u[TB][PB];
+                        float4 u[PB];
                         #pragma unroll
-                        for (int x = 0; x < TB; ++x)
-                            #pragma unroll
-                            for (int j = 0; j < PB; ++j) {
-                                const int tt = t + x * (NT / 32), bb = b + j;
-                                u[x][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (tt < hi && bb <= d1)
-                                    u[x][j] = __ldcg(reinterpret_cast<const float4*>(
-                                        g.part2 + (bb * 2 + (bb == d0)) * slot_floats + tt * kTileM + col));
-                            }
+                        for (int j = 0; j < PB; ++j) {
+                            u[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (b + j <= d1)
+                                u[j] = __ldcg(reinterpret_cast<const float4*>(
+                                    g.part2 + ((b + j) * 2 + (b + j == d0)) * slot_floats + t * kTileM + col));
+                        }
                         #pragma unroll
-                        for (int x = 0; x < TB; ++x)
-                            #pragma unroll
-                            for (int j = 0; j < PB; ++j) {
-                                v[x].x += u[x][j].x; v[x].y += u[x][j].y;
-                                v[x].z += u[x][j].z; v[x].w += u[x][j].w;
-                            }
+                        for (int j = 0; j < PB; ++j) {
+                            v.x += u[j].x; v.y += u[j].y; v.z += u[j].z; v.w += u[j].w;
+                        }
                     }
-                    #pragma unroll
-                    for (int x = 0; x < TB; ++x) {
-                        const int tt = t + x * (NT / 32);
-                        if (tt >= hi) break;
-                        const int64_t o = (int64_t)tt * g.d + m * kTileM + col;
-                        put_y(o, v[x].x);
-                        put_y(o + 1, v[x].y);
-                        put_y(o + 2, v[x].z);
-                        put_y(o + 3, v[x].w);
-                    }
+                    put_y4((int64_t)t * g.d + m * kTileM + col, v);
                 }
                 continue;
             }
@@ -1258,31 +1278,47 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                         }
                     }
                 }
-                auto put_hidden = [&](int r, float h) {
+                // activation rows r and, with `two`, r + 1 of the expert
+                auto put_hidden = [&](int r, bool two, float h0, float h1) {
                     if (!live) return;
                     if constexpr (K::kTensor) {
                         // GELU in two bf16 parts, 16 bits together
-                        const float v = gelu_fast(h);
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                        const float rest = v - __bfloat162float(hi);
+                        float v0, v1;
+                        f2_unpack(f2_mul(f2_pack(h0, h1), gelu_parts_fast2(h0, h1).Phi), v0, v1);
+                        const __nv_bfloat162 hi = __floats2bfloat162_rn(v0, v1);
+                        const float l0 = v0 - __low2float(hi), l1 = v1 - __high2float(hi);
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(isfinite(l0) ? l0 : 0.f,
+                                                                        isfinite(l1) ? l1 : 0.f);
                         __nv_bfloat16* p = hidden + (int64_t)(r0 + r) * 2 * g.f + col;
-                        p[0] = hi;
-                        p[g.f] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+                        p[0] = hi.x;
+                        p[g.f] = lo.x;
+                        if (two) {
+                            p[2 * (int64_t)g.f] = hi.y;
+                            p[3 * (int64_t)g.f] = lo.y;
+                        }
                     } else {
-                        hidden[(int64_t)(r0 + r) * g.f + col] = gelu_f(h);
+                        hidden[(int64_t)(r0 + r) * g.f + col] = gelu_f(h0);
                     }
                 };
-                auto emit = [&](int r, float v) {   // activation row r of the expert
-                    v += b;
+                auto emit = [&](int r, bool two, float v0, float v1) {
+                    v0 += b;
+                    v1 += b;
                     if (second) {
                         float* p = yacc + plan.row_token[r0 + r] * kTileM + i;
-                        *p = fmaf(plan.row_w[r0 + r], v, *p);
-                    } else if (whole) {
-                        put_hidden(r, v);
-                    } else if (rest) {
-                        put_hidden(r, v + yacc[r * kTileM + i]);
+                        *p = fmaf(plan.row_w[r0 + r], v0, *p);
+                        if (two) {
+                            p = yacc + plan.row_token[r0 + r + 1] * kTileM + i;
+                            *p = fmaf(plan.row_w[r0 + r + 1], v1, *p);
+                        }
+                    } else if (whole || rest) {
+                        if (rest) {
+                            v0 += yacc[r * kTileM + i];
+                            if (two) v1 += yacc[(r + 1) * kTileM + i];
+                        }
+                        put_hidden(r, two, v0, v1);
                     } else {
-                        __stcg(mine + r * kTileM + i, v);
+                        __stcg(mine + r * kTileM + i, v0);
+                        if (two) __stcg(mine + (r + 1) * kTileM + i, v1);
                     }
                 };
                 if constexpr (K::kTensor) {
@@ -1291,27 +1327,21 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     if (!epilogue_all<NT>(ok)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * kAccCols;
-                    if (!second) {
-                        unsigned long long left = plan.tokens[e];
-                        int r = 0;
-                        #pragma unroll 1
-                        for (int x = 0; x * 16 < g.tokens; ++x, left >>= 16) {
-                            if (!(left & 0xffffull)) continue;
-                            float v[16];
-                            tmem_ld16(base + x * 16, v);
-                            #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (left >> j & 1ull) emit(r++, v[j]);
+                    // Two rows a turn, not unrolled: instructions that run once cost more to
+                    // fetch than these turns cost to wait for (7 us a unit of 16 rows against 2).
+                    #pragma unroll 1
+                    for (int r = 0; r < rows; r += 2) {
+                        const bool two = r + 1 < rows;
+                        float v[4];
+                        if (second) {
+                            tmem_ld4(base + 2 * r, v);   // high and low part of both rows
+                            v[0] += v[1];
+                            v[1] = v[2] + v[3];
+                        } else {
+                            tmem_ld_pair(base + plan.row_token[r0 + r],
+                                         base + plan.row_token[r0 + (two ? r + 1 : r)], v[0], v[1]);
                         }
-                    } else {
-                        #pragma unroll 1
-                        for (int x = 0; x * 8 < rows; ++x) {
-                            float v[16];
-                            tmem_ld16(base + x * 16, v);
-                            #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (x * 8 + j < rows) emit(x * 8 + j, v[2 * j] + v[2 * j + 1]);
-                        }
+                        emit(r, two, v[0], v[1]);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -1337,7 +1367,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     for (int r = t_first; r < rows; r += STEP) {
                         float v = 0.f;
                         for (int x = 0; x < 8 / groups; ++x) v += red[(x * cols + r) * kTileM + i];
-                        emit(r, v);
+                        emit(r, false, v, 0.f);
                     }
                     epilogue_barrier<NT>();
                 }
@@ -1369,7 +1399,8 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                                 }
                                 #pragma unroll
                                 for (int u = 0; u < 8; ++u)
-                                    if (r + u * STEP < rows) put_hidden(r + u * STEP, own[u] + v[u]);
+                                    if (r + u * STEP < rows)
+                                        put_hidden(r + u * STEP, false, own[u] + v[u], 0.f);
                             }
                         }
                     }
