@@ -179,6 +179,13 @@ __device__ __forceinline__ void gate_tokens(const float* logits, int tokens, int
 // task waits only for tasks that running blocks hold, so blocks need not be
 // resident together.
 constexpr int kDirectTokens = 4;
+// With two to four tokens, up to so many weights (each token's counted): measured
+// on 8 experts, top-2, against the kernel below: d = 256, f = 1024, 4 tokens 15.4
+// against 20.1 us in bf16 and 14.7 against 23.9 in fp32; d = 512, f = 2048, 4 tokens
+// (17 M weights) 20.0 against 20.9 and 25.6 against 29.1; d = 768, f = 3072, 2 tokens
+// 24.3 against 23.1 and 28.5 against 34.5, 4 tokens 37.2 against 28.6 and 45.6
+// against 42.2.
+constexpr int64_t kDirectWeights = int64_t(17) << 20;
 constexpr int kDirectThreads = 256;
 // 64, 80 or 128 registers a thread
 template <int TT> constexpr int direct_blocks_per_sm() { return TT == 1 ? 4 : TT == 2 ? 3 : 2; }
@@ -419,7 +426,7 @@ template <> struct Kind<float> {
 };
 // bf16: the warps beyond the epilogue's only gate
 template <typename T> constexpr int few_threads() {
-    return Kind<T>::kTensor ? 384 : kWarpsBeforeEpilogue * 32 + Kind<T>::kEpilogue;
+    return Kind<T>::kTensor ? 512 : kWarpsBeforeEpilogue * 32 + Kind<T>::kEpilogue;
 }
 
 constexpr int kMaxBlocks = 512;
@@ -700,7 +707,11 @@ __device__ __forceinline__ void make_plan(Plan& p, const FewArgs& g) {
         p.row_token[r] = (uint8_t)t;
         p.row_w[r] = p.w[i];
     }
-    if (lane == 0 && warp >= 6 && warp < 8) (warp == 6 ? p.first : p.second).template cut<T>(g, p, warp - 6);
+    if (lane == 0 && warp >= 6 && warp < 8) {
+        Walk& w = warp == 6 ? p.first : p.second;
+        w.template cut<T>(g, p, warp - 6);
+        if ((int)blockIdx.x < w.shares) w.begin(p, (int)blockIdx.x);
+    }
     __syncthreads();
 }
 
@@ -963,7 +974,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                 while (ok) {
                     if (share >= 0) {
                         atomicAdd(&g.cnt->claimed[product], 1);
-                        walk.begin(plan, share);
+                        if (share != (int)blockIdx.x) walk.begin(plan, share);
                         ok = post(walk);
                         while (ok && walk.next(plan, s)) {
                             const int e = plan.act[s.a];
@@ -1502,7 +1513,7 @@ bool few_map(CUtensorMap* m, const void* p, uint64_t n0, uint64_t n1, uint64_t n
 
 // Of the 227 KB a block may have; the rest lets blocks of the logits kernel share
 // the SM, so that this kernel's blocks are set up while those run.
-constexpr int kFewSmem = 222 * 1024;
+constexpr int kFewSmem = 227 * 1024;
 
 template <typename T> cudaError_t few_smem_limit(int* dynamic) {
     // what the static part leaves; looked up once
@@ -1585,11 +1596,11 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
         few_logits_kernel<T, 2, 1><<<(s.E + 1) / 2, kLogitThreads, 0, st>>>(
             t, s.d, s.E, x, (const T*)p.Wg, p.logit_bias, (float*)g.logits, (int*)g.cnt, words);
     else
-        few_logits_kernel<T, 4, 8><<<dim3((s.E + 3) / 4, (t + 7) / 8), kLogitThreads, 0, st>>>(
+        few_logits_kernel<T, 4, 4><<<dim3((s.E + 3) / 4, (t + 3) / 4), kLogitThreads, 0, st>>>(
             t, s.d, s.E, x, (const T*)p.Wg, p.logit_bias, (float*)g.logits, (int*)g.cnt, words);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (t <= kDirectTokens) {
+    if (t == 1 || (t <= kDirectTokens && (int64_t)t * s.k * 2 * s.d * s.f <= kDirectWeights)) {
         DirectArgs q;
         q.d = s.d; q.f = s.f; q.E = s.E; q.k = s.k; q.renorm = s.renorm; q.tokens = t;
         q.logits = g.logits;
@@ -1599,7 +1610,7 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
         q.done = &g.cnt->done;
         q.status = status;
         q.limit_ns = g.limit_ns;
-        return t == 1 ? launch_direct<T, 1, 2, 4>(q, st) : t == 2 ? launch_direct<T, 2, 2, 4>(q, st)
+        return t == 1 ? launch_direct<T, 1, 4, 2>(q, st) : t == 2 ? launch_direct<T, 2, 2, 4>(q, st)
                                                                   : launch_direct<T, 4, 4, 2>(q, st);
     }
 
@@ -1610,7 +1621,7 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
     const int slot = (rows + K::kBox - 1) / K::kBox * K::kBox * kBlockBytes;   // at most
     const int nc = t <= 4 ? 4 : 8;
     int left = most - 1024 - t * kTileM * 4 - (K::kTensor ? 0 : 8 * nc * kTileM * 4);
-    g.b_ring = slot * (slot <= 4096 ? kMaxBStages : 4);
+    g.b_ring = slot * (slot <= 4096 ? kMaxBStages : slot <= 8192 ? 4 : 2);
     left -= g.b_ring;
     g.a_stages = left / kABytes < kMaxAStages ? left / kABytes : kMaxAStages;
     g.slices = few_blocks() / g.tiles2;
