@@ -1,5 +1,29 @@
-// few.cu -- one whole MoE layer for a few tokens (T <= MOE_FEW_MAX_TOKENS):
-// router, top-k gate, experts, combine and residual, for decode steps.
+// few.cu -- one whole MoE layer for a few tokens (T <= MOE_FEW_MAX_TOKENS), for
+// decode steps, in two launches:
+//
+//   few_logits_kernel   L = x Wg^T + beta
+//   few_direct_kernel   one token, or up to four of a small layer, or
+//   few_experts_kernel  everything else:
+//     gate of L;  a = GELU(W1[e] x_t + b1[e]) for every chosen (t, e);
+//     y_t = residual_t + sum_j w_tj (W2[e_j] a_tj + b2[e_j])
+//
+// The weights of the chosen experts are nearly all the bytes, and with at most 64
+// tokens a weight meets at most 64 of them: memory bounds the layer (64 flop a
+// byte in bf16 against 290 that the GPU has), and beside it the latencies between
+// its dependent steps.  So both expert kernels stream every chosen weight once, in
+// equal shares over all SMs, and do all the rest of the layer in the same launch:
+// what a step waits for is a counter in memory, not a launch.  The launch itself
+// overlaps the logits kernel's.
+//
+// Measured on a GB300 (device time of both launches in a graph, weights from HBM):
+//   bf16, d = 4096, f = 1024, 128 experts, top-8:  64 tokens (all 2.1 GB of weights)
+//     349 us, 6.1 TB/s; one token (134 MB) 35 us, 3.9 TB/s
+//   bf16, d = 2048, f = 8192, 16 experts, top-2:   13 tokens (0.87 GB) 153 us, 5.7 TB/s
+//   bf16, d = 768, f = 3072, 8 experts, top-2:     64 tokens (76 MB) 46 us; one 13 us
+//   fp32, d = 768, f = 3072, 64 experts, top-1, skewed: 33 tokens (38 MB) 65 us
+// At the large sizes memory bounds it (its streams alone run at 6.7 to 6.9 TB/s);
+// about 35 us are the logits, the gate, the hand-over between the products and
+// the adding of split tiles, which bound the small sizes.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -55,6 +79,7 @@ __global__ void __launch_bounds__(kLogitThreads)
                       const float* __restrict__ beta, float* __restrict__ logits,
                       int* __restrict__ counters, int words) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < words; i += kLogitThreads) counters[i] = 0;
     constexpr int N = Vec<T>::N, W = kLogitThreads / 32, V = EE * TT;
@@ -398,14 +423,28 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
 }
 
 // ---- experts ----------------------------------------------------------------------
-// See the file's header for the scheme.
+// Both products with the weights as the 128-row operand and the tokens as the
+// narrow one: D[128 output features][rows] = W tile x activations^T, K blocks of 128
+// bytes.  One block an SM:
+//   warp 0  takes shares (below) and loads their weights by TMA, 16 KB a K block,
+//           the second product's right behind the first's;
+//   warp 1  loads the activations: all tokens' K block of x (columns of tokens that
+//           are not the expert's are left unused), then the expert's hidden rows;
+//   warp 2  (bf16) issues the MMAs, into one of two accumulators;
+//   4 or 8 warps  take the accumulators out: GELU and hidden rows, or the gate-weighted
+//           sum over the experts of an output tile in shared memory.  fp32: they do
+//           the products themselves.
+// In bf16 hidden activations are stored as two bf16 numbers each, high and low
+// part, and enter the second product as two columns: 16 bits of them count, for
+// no more than twice the narrow operand's bytes.
 constexpr int kTileM = 128;          // weight rows (output features) of a tile
 constexpr int kBlockBytes = 128;     // one K block of a row: 64 bf16 or 32 fp32
 constexpr int kABytes = kTileM * kBlockBytes;
 constexpr int kMaxAStages = 12, kMaxBStages = 8;
 constexpr int kWarpsBeforeEpilogue = 4;
 // Times that decide whether the first product's units are cut: a K block of
-// weights when all blocks stream, when few do, and adding the parts of cut units.
+// weights when all blocks stream (16 KB of each of 152 at 6.8 TB/s), when few do
+// (measured: 60 GB/s an SM), and adding the parts of cut units.
 constexpr float kBlockNs = 366.f, kLoneBlockNs = 280.f, kJoinNs = 2000.f;
 constexpr uint64_t kTakeOverNs = 20000;   // a share without a block for so long is taken over
 
@@ -479,7 +518,8 @@ struct Sorted {
 };
 
 // Relative time of one K block with `rows` activation rows: the bytes of the
-// weights, unless fp32 products take longer.
+// weights, unless fp32 products take longer (measured: 1.7 us for 32 rows against
+// 0.37 for the bytes; shared memory feeds 5 packed FMAs a load).
 constexpr int kMaxCost = 17;
 template <typename T> __device__ __forceinline__ int block_cost(int rows) {
     return sizeof(T) == 2 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : rows <= 32 ? 9 : kMaxCost;
@@ -1592,13 +1632,20 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
     g.limit_ns = wait_limit_ns();
 
     const int words = (int)((sizeof(Counters) + sizeof(int) * ((s.d + kTileM - 1) / kTileM)) / 4);
-    if (t == 1)
-        few_logits_kernel<T, 2, 1><<<(s.E + 1) / 2, kLogitThreads, 0, st>>>(
-            t, s.d, s.E, x, (const T*)p.Wg, p.logit_bias, (float*)g.logits, (int*)g.cnt, words);
-    else
-        few_logits_kernel<T, 4, 4><<<dim3((s.E + 3) / 4, (t + 3) / 4), kLogitThreads, 0, st>>>(
-            t, s.d, s.E, x, (const T*)p.Wg, p.logit_bias, (float*)g.logits, (int*)g.cnt, words);
-    cudaError_t e = cudaGetLastError();
+    // Both launches may begin while the kernel before them in the stream ends; each
+    // kernel waits for that one's end before it touches memory.
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.stream = st;
+    cfg.gridDim = t == 1 ? dim3((s.E + 1) / 2) : dim3((s.E + 3) / 4, (t + 3) / 4);
+    cfg.blockDim = dim3(kLogitThreads);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, t == 1 ? few_logits_kernel<T, 2, 1> : few_logits_kernel<T, 4, 4>,
+                                       t, s.d, s.E, x, (const T*)p.Wg, p.logit_bias, (float*)g.logits,
+                                       (int*)g.cnt, words);
     if (e != cudaSuccess) return e;
     if (t == 1 || (t <= kDirectTokens && (int64_t)t * s.k * 2 * s.d * s.f <= kDirectWeights)) {
         DirectArgs q;
@@ -1634,16 +1681,9 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
         !few_map<T>(&mh, g.hidden, s.f, (uint64_t)t * s.k * K::kRowsPerSlot, 0, K::kBox))
         return cudaErrorInvalidValue;
 
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)few_blocks());
     cfg.blockDim = dim3(few_threads<T>());
     cfg.dynamicSmemBytes = (size_t)most;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, few_experts_kernel<T>, w1, mx, w2, mh, g);
 }
 

@@ -241,6 +241,39 @@ def test_two_layers_on_two_streams_at_once():
         assert torch.equal(a.y, y) and int(a.status.item()) == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_beside_kernels_that_hold_most_of_the_gpu(dtype):
+    # its blocks come to run a few at a time, and take over the shares of those that do not
+    p = make(40, 512, 1024, 32, 2, dtype)
+    fp = layer(p, 2, 1)
+    want = fp.forward(p["x"], p["residual"]).clone()
+    big = torch.randn(8192, 8192, device=DEV, dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                torch.matmul(big, big)
+        for _ in range(10):
+            assert torch.equal(fp.forward(p["x"], p["residual"]), want)
+        torch.cuda.synchronize()
+    assert int(fp.status.item()) == 0
+
+
+def test_right_behind_the_kernels_that_make_its_inputs():
+    # the launches overlap the end of the kernel before them, not its results
+    p = make(3, 256, 512, 8, 2, "bf16")
+    fp = layer(p, 2, 1)
+    xs = torch.randn(50, 3, 256, device=DEV).to(torch.bfloat16)
+    want = [fp.forward(x, x).clone() for x in xs]
+    out = torch.empty_like(xs)
+    x = torch.empty_like(xs[0])
+    for i in range(50):
+        x.copy_(xs[i])
+        out[i].copy_(fp.forward(x, x))
+    assert torch.equal(out, torch.stack(want))
+
+
 @pytest.mark.parametrize("name", ["tiny_f32", "moe_s_bf16"])
 def test_agrees_with_the_layer_on_batches(name):
     cfg = synth.CONFIGS[name].scaled(T=64)

@@ -188,6 +188,21 @@ def test_same_bits_every_time_on_any_stream():
     assert abs(float(c.total) - 3 * float(n)) <= 2e-2 * float(n)
 
 
+def test_right_behind_the_kernels_that_make_the_gradients():
+    # the launches overlap the end of the kernel before them, not its results
+    src = [torch.randn(300001, device=DEV) * (i + 1) for i in range(20)]
+    t = torch.empty(300001, device=DEV)
+    c = GradClip([t])
+    norms = []
+    for s in src:
+        t.copy_(s)
+        norms.append(c.clip(1.0).clone())
+        norms.append(c.norm().clone())
+    for s, a, b in zip(src, norms[::2], norms[1::2]):
+        assert abs(float(a) - exact([s])) <= NORM * exact([s])
+        assert abs(float(b) - 1.0) <= 3 * NORM
+
+
 def test_beyond_32_bits():
     n = 2 ** 31 + 5
     t = torch.full((n,), 0.5, dtype=BF16, device=DEV)
