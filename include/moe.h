@@ -400,6 +400,8 @@ MOE_API size_t moe_layer_few_workspace_size(const moe_shape* s);
  *   ws        workspace (contents need no initialisation, garbage after)
  *   dev_status  MOE_ERR_NONFINITE on a NaN or infinite logit (the experts then
  *             chosen are in range, y is unspecified), MOE_ERR_TIMEOUT
+ * The launches may overlap the end of the kernel before them in the stream;
+ * they touch memory only when that kernel has completed.
  * Hidden activations and the sums over slots are held to more than bf16's
  * precision in both dtypes; y is rounded once.  Deterministic: the same inputs
  * give the same bits.  Can be captured in a CUDA graph. */
