@@ -446,6 +446,9 @@ constexpr int kWarpsBeforeEpilogue = 4;
 // weights when all blocks stream (16 KB of each of 152 at 6.8 TB/s), when few do
 // (measured: 60 GB/s an SM), and adding the parts of cut units.
 constexpr float kBlockNs = 366.f, kLoneBlockNs = 280.f, kJoinNs = 2000.f;
+// Copies and MMAs in flight end by themselves: waits for them at a block's end have
+// a bound of their own, however short the caller's is.
+constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr uint64_t kTakeOverNs = 20000;   // a share without a block for so long is taken over
 
 template <typename T> struct Kind;
@@ -1064,7 +1067,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
             // copies in flight land before the block ends
             for (int i = 0; i < issued; ++i) {
                 if (--st < 0) { st = g.a_stages - 1; ph ^= 1; }
-                mbar_wait_bounded(smem_u32(&c.a_full[st]), ph, g.limit_ns, nullptr);
+                mbar_wait_bounded(smem_u32(&c.a_full[st]), ph, kDrainNs, nullptr);
             }
         }
         __syncwarp();
@@ -1121,7 +1124,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
             // copies in flight land before the block ends
             for (int i = 0; i < issued; ++i) {
                 if (--r.slot < 0) { r.slot = r.slots - 1; r.parity ^= 1; }
-                mbar_wait_bounded(r.bar(), r.parity, g.limit_ns, nullptr);
+                mbar_wait_bounded(r.bar(), r.parity, kDrainNs, nullptr);
             }
         }
         __syncwarp();
@@ -1182,7 +1185,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
             }
             // every MMA issued has completed before TMEM is freed
             tc_commit(smem_u32(&c.drain));
-            mbar_wait_bounded(smem_u32(&c.drain), 0, g.limit_ns, nullptr);
+            mbar_wait_bounded(smem_u32(&c.drain), 0, kDrainNs, nullptr);
         }
         __syncwarp();
     } else if (warp >= kWarpsBeforeEpilogue && warp < kWarpsBeforeEpilogue + K::kEpilogue / 32) {

@@ -78,7 +78,7 @@ template <int CAP> __device__ __forceinline__ int find_tensor(const GradTable<CA
 __device__ __noinline__ double rare_squares(float a, float b, float c, float d, float scale) {
     a *= scale; b *= scale; c *= scale; d *= scale;
     const double s = fmaf(a, a, fmaf(b, b, fmaf(c, c, d * d)));
-    return s * (scale < 1.f ? 0x1p160 : 0x1p-160);
+    return s * (scale < 1.f ? 0x1p160 : 0x1p-200);
 }
 
 struct SquareSum {
@@ -89,7 +89,7 @@ struct SquareSum {
         if (m <= 0x1p40f && (m >= 0x1p-40f || m == 0.f))
             sum = fmaf(a, a, fmaf(b, b, fmaf(c, c, fmaf(d, d, sum))));
         else
-            rare += rare_squares(a, b, c, d, m > 1.f ? 0x1p-80f : 0x1p80f);
+            rare += rare_squares(a, b, c, d, m > 1.f ? 0x1p-80f : 0x1p100f);
     }
     // the sum of one chunk's squares (at most 72 a thread)
     __device__ __forceinline__ void flush(float sum) {

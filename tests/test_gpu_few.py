@@ -9,6 +9,9 @@ kind.  In bf16 the hidden activations are held in 16 bits (2^-16 of A) and GELU
 is evaluated to 1.5e-7 of |h| (within 2^-16 of B).  Tokens whose k-th and
 (k+1)-th logit are closer than their rounding are left out."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -300,6 +303,33 @@ def test_weights_beyond_32_bit_offsets():
     fp = FewTokenPass(T, Wg, W1, None, W2, None, 2, 1, beta=beta.to(DEV))
     small["b1"] = small["b2"] = None
     check(fp.forward(small["x"], small["residual"]), small, 2, 1)
+
+
+SHORT_WAIT = """
+import torch
+from mixture_experts_layer_11_gb300 import ops, synth
+from mixture_experts_layer_11_gb300.decode import FewTokenPass
+cfg = synth.MoEConfig("few", T=16, d=2048, f=4096, E=16, k=2, renorm=1, dtype={dtype!r})
+p = synth.make_inputs(cfg, device="cuda")
+fp = FewTokenPass(16, p["Wg"], p["W1"], p["b1"], p["W2"], p["b2"], 2, 1)
+for _ in range(3):
+    fp.status.zero_()
+    fp.forward(p["x"])
+    torch.cuda.synchronize()
+    print(int(fp.status.item()))
+assert int(torch.arange(10, device="cuda").sum()) == 45
+"""
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_waits_that_run_out_are_reported(dtype):
+    # 3 us: less than the second product waits for the first, so the call gives up,
+    # says so, ends, and leaves the context usable
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SHORT_WAIT.format(dtype=dtype)], cwd=root, timeout=120,
+                       env=dict(os.environ, MOE_WAIT_TIMEOUT_NS="3000"), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == [str(ops.MOE_ERR_TIMEOUT)] * 3
 
 
 def test_refusals():

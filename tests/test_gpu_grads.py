@@ -92,7 +92,7 @@ def test_nothing_outside_is_written():
         assert (buf[5:20001] != 3).all()
 
 
-@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-20, 1e-12, 1e-6, 1e6, 1e15, 1e20, 1e30, 1e34])
+@pytest.mark.parametrize("scale", [1e-42, 1e-38, 1e-30, 1e-20, 1e-12, 1e-6, 1e6, 1e15, 1e20, 1e30, 1e34])
 def test_the_whole_range(scale):
     ts = [t.float() * scale for t in make([40000, 17])]
     check(ts, 0.5 * exact(ts))
