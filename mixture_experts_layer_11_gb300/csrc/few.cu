@@ -66,6 +66,29 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
+// The warp's sums of V values (a power of two): each step sends half of what a lane
+// holds and keeps the sums of the rest, so that V values take V + log2(32 / V)
+// exchanges. Lane l returns the sum of value `which`; the lanes that hold the same
+// one have the same.
+template <int V> __device__ __forceinline__ float warp_sums(float (&v)[V], int& which) {
+    const int lane = threadIdx.x & 31;
+    which = 0;
+    int o = 16;
+    #pragma unroll
+    for (int n = V; n > 1; n /= 2, o /= 2) {
+        const bool up = lane & o;
+        which += up ? n / 2 : 0;
+        #pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = up ? v[i + n / 2] : v[i], send = up ? v[i] : v[i + n / 2];
+            v[i] = keep + __shfl_xor_sync(kFull, send, o);
+        }
+    }
+    #pragma unroll
+    for (int q = 16 / V; q > 0; q /= 2) v[0] += __shfl_xor_sync(kFull, v[0], q);
+    return v[0];
+}
+
 // ---- router logits -----------------------------------------------------------------
 // L[t,e] = <x_t, Wg_e> + beta_e in fp32.  A block computes EE experts x TT tokens;
 // its warps split d (16 bytes a lane and step), their sums are added in warp order.
@@ -86,7 +109,7 @@ __global__ void __launch_bounds__(kLogitThreads)
     __shared__ float part[W][V];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e0 = blockIdx.x * EE, t0 = blockIdx.y * TT;
-    float acc[EE][TT] = {};
+    float acc[V] = {};
     #pragma unroll 2
     for (int i = threadIdx.x * N; i < d; i += kLogitThreads * N) {
         float g[EE][N];
@@ -100,18 +123,13 @@ __global__ void __launch_bounds__(kLogitThreads)
             #pragma unroll
             for (int a = 0; a < EE; ++a)
                 #pragma unroll
-                for (int n = 0; n < N; ++n) acc[a][b] = fmaf(g[a][n], v[n], acc[a][b]);
+                for (int n = 0; n < N; ++n)
+                    acc[a * TT + b] = fmaf(g[a][n], v[n], acc[a * TT + b]);
         }
     }
-    #pragma unroll
-    for (int a = 0; a < EE; ++a)
-        #pragma unroll
-        for (int b = 0; b < TT; ++b) {
-            float v = acc[a][b];
-            #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-            if (lane == 0) part[warp][a * TT + b] = v;
-        }
+    int which;
+    const float sum = warp_sums(acc, which);
+    if (lane % (32 / V) == 0) part[warp][which] = sum;
     __syncthreads();
     const int a = threadIdx.x / TT, b = threadIdx.x % TT;
     if (a < EE && e0 + a < E && t0 + b < tokens) {
@@ -309,7 +327,7 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
         const int nk = (K + 32 * N - 1) / (32 * N);      // steps of 32 lanes along K
         const int steps = one ? nk : nact * nk;
         const T* Wm = (const T*)(one ? g.W1 : g.W2);
-        float acc[RW][TT] = {};
+        float acc[RW * TT] = {};
         int c = warp % S;
         int a = one ? a1 : c / nk, ck = one ? c : c % nk;
         bool more = row0 < M && c < steps;
@@ -367,7 +385,8 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
                     #pragma unroll
                     for (int r = 0; r < RW; ++r)
                         #pragma unroll
-                        for (int n = 0; n < N; ++n) acc[r][t] = fmaf(wf[r][n], v[n], acc[r][t]);
+                        for (int n = 0; n < N; ++n)
+                            acc[r * TT + t] = fmaf(wf[r][n], v[n], acc[r * TT + t]);
                 }
             }
             more = more && c < steps;
@@ -383,17 +402,11 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
                                             to_f32<T>(((const T*)g.b2)[(int64_t)e_of[t * g.k + lane] * M + row0 + r]);
                             #pragma unroll
                             for (int q = 0; q < TT; ++q)
-                                if (q == t) acc[r][q] += v;
+                                if (q == t) acc[r * TT + q] += v;
                         }
-        #pragma unroll
-        for (int r = 0; r < RW; ++r)
-            #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                float v = acc[r][t];
-                #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-                if (lane == 0) part[warp][r * TT + t] = v;
-            }
+        int which;
+        const float sum = warp_sums(acc, which);
+        if (lane % (32 / (RW * TT)) == 0) part[warp][which] = sum;
         __syncthreads();
         // thread (group of warps, row, token): the warps' sums in order
         if ((int)threadIdx.x < W / S * RW * TT) {
