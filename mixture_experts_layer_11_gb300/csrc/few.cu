@@ -927,6 +927,34 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
     return true;
 }
 
+// Adds the parts that shares wrote of a unit, in their order, to[r] = own[r] + (0 + p_1[r] +
+// p_2[r] + ...), for rows t0, t0 + STEP, ...: eight at a time, so that their loads overlap.
+// A function of its own, since a launch runs it about once: one copy to fetch, not two.
+template <int STEP>
+__device__ __noinline__ void add_parts(const float* own, const float* from, int64_t stride, int parts,
+                                       int t0, int rows, float* to) {
+    #pragma unroll 1
+    for (int r = t0; r < rows; r += 8 * STEP) {
+        float v[8];
+        #pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = 0.f;
+        #pragma unroll 1
+        for (int x = 0; x <= parts; ++x) {
+            const float* p = x < parts ? from + x * stride : own;
+            if (!p) break;
+            float w[8];
+            #pragma unroll
+            for (int u = 0; u < 8; ++u)
+                w[u] = r + u * STEP < rows ? __ldcg(p + (r + u * STEP) * kTileM) : 0.f;
+            #pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] += w[u];
+        }
+        #pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (r + u * STEP < rows) to[(r + u * STEP) * kTileM] = v[u];
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(few_threads<T>(), 1)
     few_experts_kernel(const __grid_constant__ CUtensorMap mapW1, const __grid_constant__ CUtensorMap mapX,
@@ -1326,23 +1354,8 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     if (tid == 0) rest = load_acquire(&g.cnt->joined[c0]) == c1 - c0;
                     rest = epilogue_all<NT>(tid != 0 || rest);
                     if (rest) {
-                        // eight rows at a time, so that their loads overlap
-                        #pragma unroll 1
-                        for (int r = t_first; r < rows; r += 8 * STEP) {
-                            float v[8];
-                            #pragma unroll
-                            for (int u = 0; u < 8; ++u) v[u] = 0.f;
-                            #pragma unroll 1
-                            for (int x = c0 + 1; x <= c1; ++x) {
-                                const float* from = g.part1 + x * 2 * slot_floats + i;
-                                #pragma unroll
-                                for (int u = 0; u < 8; ++u)
-                                    if (r + u * STEP < rows) v[u] += __ldcg(from + (r + u * STEP) * kTileM);
-                            }
-                            #pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                if (r + u * STEP < rows) yacc[(r + u * STEP) * kTileM + i] = v[u];
-                        }
+                        add_parts<STEP>(nullptr, g.part1 + (c0 + 1) * 2 * slot_floats + i, 2 * slot_floats,
+                                        c1 - c0, t_first, rows, yacc + i);
                     }
                 }
                 // activation rows r and, with `two`, r + 1 of the expert
@@ -1449,25 +1462,15 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                         epilogue_barrier<NT>();
                         finished = c.last;
                         if (finished) {
+                            add_parts<STEP>(g.part1 + (c0 * 2 + 1) * slot_floats + i,
+                                            g.part1 + (c0 + 1) * 2 * slot_floats + i, 2 * slot_floats,
+                                            c1 - c0, t_first, rows, yacc + i);
+                            // one row (bf16: two) a turn, short code: it runs once
+                            constexpr int W = K::kTensor ? 2 : 1;
                             #pragma unroll 1
-                            for (int r = t_first; r < rows; r += 8 * STEP) {
-                                float v[8], own[8];
-                                #pragma unroll
-                                for (int u = 0; u < 8; ++u) v[u] = own[u] = 0.f;
-                                #pragma unroll 1
-                                for (int x = c0; x <= c1; ++x) {
-                                    const float* from = g.part1 + (x * 2 + (x == c0)) * slot_floats + i;
-                                    #pragma unroll
-                                    for (int u = 0; u < 8; ++u)
-                                        if (r + u * STEP < rows) {
-                                            const float part = __ldcg(from + (r + u * STEP) * kTileM);
-                                            if (x == c0) own[u] = part; else v[u] += part;
-                                        }
-                                }
-                                #pragma unroll
-                                for (int u = 0; u < 8; ++u)
-                                    if (r + u * STEP < rows)
-                                        put_hidden(r + u * STEP, false, own[u] + v[u], 0.f);
+                            for (int r = t_first; r < rows; r += W * STEP) {
+                                const bool two = K::kTensor && r + 1 < rows;
+                                put_hidden(r, two, yacc[r * kTileM + i], two ? yacc[(r + 1) * kTileM + i] : 0.f);
                             }
                         }
                     }
