@@ -534,11 +534,12 @@ struct Sorted {
 };
 
 // Relative time of one K block with `rows` activation rows: the bytes of the
-// weights, unless fp32 products take longer (measured: 1.7 us for 32 rows against
-// 0.37 for the bytes; shared memory feeds 5 packed FMAs a load).
-constexpr int kMaxCost = 17;
+// weights (4), unless fp32 products take longer.  Of ten such tables these shares
+// took the least time over 44 fp32 layers of 6 to 64 tokens (geometric mean 99.0 us;
+// 4, 6, 12, 24: 100.4; 4, 8, 18, 34: 101.0).
+constexpr int kMaxCost = 25;
 template <typename T> __device__ __forceinline__ int block_cost(int rows) {
-    return sizeof(T) == 2 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : rows <= 32 ? 9 : kMaxCost;
+    return sizeof(T) == 2 ? 1 : rows <= 8 ? 4 : rows <= 16 ? 7 : rows <= 32 ? 13 : kMaxCost;
 }
 
 // One block's consecutive K blocks of one (expert, tile).
@@ -865,15 +866,25 @@ struct Reader {
     }
 };
 
+// 16 bytes of shared memory at a 32-bit address
+__device__ __forceinline__ ulonglong2 lds16(uint32_t at) {
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
 // fp32 products on the CUDA cores: 8 warps, a lane holding 4 weight rows and NC
 // activation rows.  With more than NC rows the warps split them into `groups`
 // (1, 2, 4 or 8) and K into 8 / groups; sums run over even and odd k apart, as
-// packed pairs.  The result goes to red[K slice][row][128].
+// packed pairs.  The result goes to red[K slice][row][128].  One 16-byte chunk of
+// the K block a turn, all its loads first, and the turns not unrolled: five copies
+// of this loop share the instruction cache, and each runs for a few microseconds
+// (33 tokens on 64 experts of 768 x 3072: 57.9 us, unrolled 62.2; 8 tokens on 16
+// of 2048 x 8192: 226 us against 237, of which the products cost 5).
 template <int NC, int GROUPS>
 __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const Seg& s, bool first,
                                              int rows, const uint8_t* row_token,
-                                             const uint8_t* a_ring, const uint8_t* b_ring,
-                                             int& as, uint32_t& ap, Ring& b, int ew, int lane,
+                                             uint32_t a_ring, int& as, uint32_t& ap, Ring& b, int ew, int lane,
                                              float* red) {
     const int grp = ew % GROUPS, slice = ew / GROUPS;
     uint32_t brow[NC];
@@ -881,7 +892,8 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
     for (int j = 0; j < NC; ++j) {
         int r = grp * NC + j;
         r = r < rows ? r : rows - 1;
-        brow[j] = first ? row_token[r] : r;
+        const uint32_t q = first ? row_token[r] : r;
+        brow[j] = q * 128 + ((q & 7) << 4);   // the row with its swizzle
     }
     uint64_t acc[4][NC];
     #pragma unroll
@@ -892,24 +904,25 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
         if (!mbar_wait_warp(smem_u32(&c.a_full[as]), ap, g.limit_ns, &c.abort_flag) ||
             !mbar_wait_warp(b.bar(), b.parity, g.limit_ns, &c.abort_flag))
             return false;
-        const uint8_t* A = a_ring + as * kABytes;
-        const uint8_t* B = b_ring + b.slot * b.bytes;
-        #pragma unroll
+        const uint32_t A = a_ring + as * kABytes + (lane << 7) + ((lane & 7) << 4);
+        const uint32_t B = b.at();
+        #pragma unroll 1
         for (int i = 0; i < GROUPS; ++i) {
-            const int ch = slice * GROUPS + i;   // 16-byte chunk of the K block
+            const uint32_t ch = (slice * GROUPS + i) << 4;   // 16-byte chunk of the K block
             ulonglong2 a[4];
             #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                a[q] = *reinterpret_cast<const ulonglong2*>(A + (lane + 32 * q) * 128 +
-                                                            ((ch ^ (lane & 7)) << 4));
+            for (int q = 0; q < 4; ++q) a[q] = lds16((A ^ ch) + q * 4096);
+            ulonglong2 x[NC];
             #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(
-                    B + brow[j] * 128 + ((ch ^ (brow[j] & 7)) << 4));
+            for (int j = 0; j < NC; ++j) x[j] = lds16(B + (brow[j] ^ ch));
+            #pragma unroll
+            for (int j = 0; j < NC; ++j)
                 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[q][j] = f2_fma(a[q].y, x.y, f2_fma(a[q].x, x.x, acc[q][j]));
-            }
+                for (int q = 0; q < 4; ++q) acc[q][j] = f2_fma(a[q].x, x[j].x, acc[q][j]);
+            #pragma unroll
+            for (int j = 0; j < NC; ++j)
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) acc[q][j] = f2_fma(a[q].y, x[j].y, acc[q][j]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.a_empty[as]));
@@ -1432,15 +1445,15 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     const int nc = rows <= 4 ? 4 : 8;
                     const uint8_t* rt = plan.row_token + r0;
                     if (rows <= 4)
-                        ok = products_f32<4, 1>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<4, 1>(g, c, s, !second, rows, rt, smem_u32(a_ring), as, ap, ring, ew, lane, red);
                     else if (rows <= 8)
-                        ok = products_f32<8, 1>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 1>(g, c, s, !second, rows, rt, smem_u32(a_ring), as, ap, ring, ew, lane, red);
                     else if (rows <= 16)
-                        ok = products_f32<8, 2>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 2>(g, c, s, !second, rows, rt, smem_u32(a_ring), as, ap, ring, ew, lane, red);
                     else if (rows <= 32)
-                        ok = products_f32<8, 4>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 4>(g, c, s, !second, rows, rt, smem_u32(a_ring), as, ap, ring, ew, lane, red);
                     else
-                        ok = products_f32<8, 8>(g, c, s, !second, rows, rt, a_ring, b_ring, as, ap, ring, ew, lane, red);
+                        ok = products_f32<8, 8>(g, c, s, !second, rows, rt, smem_u32(a_ring), as, ap, ring, ew, lane, red);
                     if (!ok) few_abort(c, g.status);
                     if (!epilogue_all<NT>(ok)) { ok = false; break; }
                     const int cols = groups * nc;
