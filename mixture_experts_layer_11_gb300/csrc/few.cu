@@ -940,31 +940,46 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
     return true;
 }
 
-// Adds the parts that shares wrote of a unit, in their order, to[r] = own[r] + (0 + p_1[r] +
-// p_2[r] + ...), for rows t0, t0 + STEP, ...: eight at a time, so that their loads overlap.
-// A function of its own, since a launch runs it about once: one copy to fetch, not two.
-template <int STEP>
-__device__ __noinline__ void add_parts(const float* own, const float* from, int64_t stride, int parts,
-                                       int t0, int rows, float* to) {
+// Adds the parts that shares wrote of a unit, in their order: to = (p[c0 + 1] + ... + p[c1]),
+// + p[c0] with `own`.  Four float4 and two parts at a time, so that their loads overlap (28
+// rows in five parts: 3 us with one value and one part at a time, under 2 so).  A function of
+// its own, since a launch runs it about once: one copy to fetch, not two.
+template <int NT>
+__device__ __noinline__ void add_parts(const float* part1, int tokens, int c0, int c1, bool own,
+                                       int rows, int tid, float4* to) {
+    const int n = rows * (kTileM / 4), parts = c1 - c0 + (own ? 1 : 0);
+    const int64_t slot = (int64_t)tokens * (kTileM / 4);
+    const float4* base = reinterpret_cast<const float4*>(part1) + c0 * 2 * slot;
+    auto part = [&](int x) {   // the x-th to be added; a share that a unit starts in uses its second slot
+        return x >= parts ? nullptr : x < c1 - c0 ? base + (x + 1) * 2 * slot : base + slot;
+    };
     #pragma unroll 1
-    for (int r = t0; r < rows; r += 8 * STEP) {
-        float v[8];
+    for (int i = tid; i < n; i += 4 * NT) {
+        float4 v[4];
         #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = 0.f;
+        for (int u = 0; u < 4; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         #pragma unroll 1
-        for (int x = 0; x <= parts; ++x) {
-            const float* p = x < parts ? from + x * stride : own;
-            if (!p) break;
-            float w[8];
+        for (int x = 0; x < parts; x += 2) {
+            const float4* p0 = part(x);
+            const float4* p1 = part(x + 1);
+            float4 w[2][4];
             #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                w[u] = r + u * STEP < rows ? __ldcg(p + (r + u * STEP) * kTileM) : 0.f;
+            for (int u = 0; u < 4; ++u) {
+                const int at = i + u * NT;
+                w[0][u] = at < n ? __ldcg(p0 + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+                w[1][u] = p1 && at < n ? __ldcg(p1 + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
             #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] += w[u];
+            for (int u = 0; u < 4; ++u) {
+                v[u].x = v[u].x + w[0][u].x + w[1][u].x;
+                v[u].y = v[u].y + w[0][u].y + w[1][u].y;
+                v[u].z = v[u].z + w[0][u].z + w[1][u].z;
+                v[u].w = v[u].w + w[0][u].w + w[1][u].w;
+            }
         }
         #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (r + u * STEP < rows) to[(r + u * STEP) * kTileM] = v[u];
+        for (int u = 0; u < 4; ++u)
+            if (i + u * NT < n) to[i + u * NT] = v[u];
     }
 }
 
@@ -1141,9 +1156,11 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
             };
             while (ok && take()) {
                 if (walk.phase == kSum) continue;
+                bool more = walk.next(plan, s);
                 if (walk.phase == kSecond && !second) {
                     second = true;
                     while (ok && issued > 0) emptied();   // the first product's slots are free
+                    r.set(c, g, b_ring, kSecond, plan.most_rows * RPS, BOX);
                     // All hidden rows are written.  (One counter for all experts: the
                     // shares are equal, so that waiting for some of them first gains nothing,
                     // and each further poll would cost a round trip to the L2.)
@@ -1155,9 +1172,8 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                         break;
                     }
                     fence_proxy_async_all();
-                    r.set(c, g, b_ring, kSecond, plan.most_rows * RPS, BOX);
                 }
-                while (ok && walk.next(plan, s)) {
+                for (; ok && more; more = walk.next(plan, s)) {
                     const int e = plan.act[s.a];
                     const int row0 = second ? plan.off[e] * RPS : 0;
                     const int rows = second ? (plan.off[e + 1] - plan.off[e]) * RPS : g.tokens;
@@ -1367,8 +1383,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     if (tid == 0) rest = load_acquire(&g.cnt->joined[c0]) == c1 - c0;
                     rest = epilogue_all<NT>(tid != 0 || rest);
                     if (rest) {
-                        add_parts<STEP>(nullptr, g.part1 + (c0 + 1) * 2 * slot_floats + i, 2 * slot_floats,
-                                        c1 - c0, t_first, rows, yacc + i);
+                        add_parts<NT>(g.part1, g.tokens, c0, c1, false, rows, tid, reinterpret_cast<float4*>(yacc));
                     }
                 }
                 // activation rows r and, with `two`, r + 1 of the expert
@@ -1475,9 +1490,8 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                         epilogue_barrier<NT>();
                         finished = c.last;
                         if (finished) {
-                            add_parts<STEP>(g.part1 + (c0 * 2 + 1) * slot_floats + i,
-                                            g.part1 + (c0 + 1) * 2 * slot_floats + i, 2 * slot_floats,
-                                            c1 - c0, t_first, rows, yacc + i);
+                            add_parts<NT>(g.part1, g.tokens, c0, c1, true, rows, tid, reinterpret_cast<float4*>(yacc));
+                            epilogue_barrier<NT>();
                             // one row (bf16: two) a turn, short code: it runs once
                             constexpr int W = K::kTensor ? 2 : 1;
                             #pragma unroll 1
