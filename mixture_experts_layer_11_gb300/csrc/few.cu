@@ -17,12 +17,12 @@
 //
 // Measured on a GB300 (device time of both launches in a graph, weights from HBM):
 //   bf16, d = 4096, f = 1024, 128 experts, top-8:  64 tokens (all 2.1 GB of weights)
-//     349 us, 6.1 TB/s; one token (134 MB) 35 us, 3.9 TB/s
+//     339 us, 6.2 TB/s; one token (134 MB) 35 us, 3.9 TB/s
 //   bf16, d = 2048, f = 8192, 16 experts, top-2:   13 tokens (0.87 GB) 153 us, 5.7 TB/s
-//   bf16, d = 768, f = 3072, 8 experts, top-2:     64 tokens (76 MB) 46 us; one 13 us
-//   fp32, d = 768, f = 3072, 64 experts, top-1, skewed: 33 tokens (38 MB) 65 us
+//   bf16, d = 768, f = 3072, 8 experts, top-2:     64 tokens (76 MB) 41 us; one 13 us
+//   fp32, d = 768, f = 3072, 64 experts, top-1, skewed: 33 tokens (38 MB) 56 us
 // At the large sizes memory bounds it (its streams alone run at 6.7 to 6.9 TB/s);
-// about 35 us are the logits, the gate, the hand-over between the products and
+// about 25 us are the logits, the gate, the hand-over between the products and
 // the adding of split tiles, which bound the small sizes.
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -223,12 +223,14 @@ __device__ __forceinline__ void gate_tokens(const float* logits, int tokens, int
 // resident together.
 constexpr int kDirectTokens = 4;
 // With two to four tokens, up to so many weights (each token's counted): measured
-// on 8 experts, top-2, against the kernel below: d = 256, f = 1024, 4 tokens 15.4
-// against 20.1 us in bf16 and 14.7 against 23.9 in fp32; d = 512, f = 2048, 4 tokens
-// (17 M weights) 20.0 against 20.9 and 25.6 against 29.1; d = 768, f = 3072, 2 tokens
-// 24.3 against 23.1 and 28.5 against 34.5, 4 tokens 37.2 against 28.6 and 45.6
-// against 42.2.
-constexpr int64_t kDirectWeights = int64_t(17) << 20;
+// on 8 experts, top-2, against the kernel below: d = 256, f = 1024, 4 tokens 14.8
+// against 19.9 us in bf16 and 14.0 against 22.7 in fp32; d = 512, f = 2048, 4 tokens
+// (17 M weights) 19.5 against 20.4 and 25.1 against 27.6; d = 768, f = 3072, 2 tokens
+// (19 M) 24.3 against 23.1 and 28 against 32.7, 3 tokens (28 M) 28.5 against 24.2
+// and 36.6 against 34.6.
+template <typename T> constexpr int64_t direct_weights() {
+    return int64_t(sizeof(T) == 2 ? 17 : 24) << 20;
+}
 constexpr int kDirectThreads = 256;
 // 64, 80 or 128 registers a thread
 template <int TT> constexpr int direct_blocks_per_sm() { return TT == 1 ? 4 : TT == 2 ? 3 : 2; }
@@ -941,8 +943,8 @@ __device__ __forceinline__ bool products_f32(const FewArgs& g, FewCtrl& c, const
 }
 
 // Adds the parts that shares wrote of a unit, in their order: to = (p[c0 + 1] + ... + p[c1]),
-// + p[c0] with `own`.  Four float4 and two parts at a time, so that their loads overlap (28
-// rows in five parts: 3 us with one value and one part at a time, under 2 so).  A function of
+// + p[c0] with `own`.  Four float4 and two parts at a time, so that their loads overlap (33
+// fp32 tokens on 64 experts: 57.3 us with one value and one part at a time, 55.6 so).  A function of
 // its own, since a launch runs it about once: one copy to fetch, not two.
 template <int NT>
 __device__ __noinline__ void add_parts(const float* part1, int tokens, int c0, int c1, bool own,
@@ -1691,7 +1693,7 @@ cudaError_t run(const moe_shape& s, const moe_layer_params& p, const T* x, const
                                        t, s.d, s.E, x, (const T*)p.Wg, p.logit_bias, (float*)g.logits,
                                        (int*)g.cnt, words);
     if (e != cudaSuccess) return e;
-    if (t == 1 || (t <= kDirectTokens && (int64_t)t * s.k * 2 * s.d * s.f <= kDirectWeights)) {
+    if (t == 1 || (t <= kDirectTokens && (int64_t)t * s.k * 2 * s.d * s.f <= direct_weights<T>())) {
         DirectArgs q;
         q.d = s.d; q.f = s.f; q.E = s.E; q.k = s.k; q.renorm = s.renorm; q.tokens = t;
         q.logits = g.logits;
