@@ -1152,7 +1152,10 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
             bool second = false, ok = true;
             auto emptied = [&]() {         // the oldest K block not yet waited for
                 ok = mbar_wait_bounded(smem_u32(&c.a_empty[st]), ph, g.limit_ns, &c.abort_flag);
-                if (!ok) few_abort(c, g.status);
+                if (!ok) {   // its copy may still be in flight: it stays among the issued ones
+                    few_abort(c, g.status);
+                    return;
+                }
                 if (++st == g.a_stages) { st = 0; ph ^= 1; }
                 --issued;
             };
@@ -1160,8 +1163,9 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                 if (walk.phase == kSum) continue;
                 bool more = walk.next(plan, s);
                 if (walk.phase == kSecond && !second) {
-                    second = true;
                     while (ok && issued > 0) emptied();   // the first product's slots are free
+                    if (!ok) break;                       // (or their ring is the one to drain)
+                    second = true;
                     r.set(c, g, b_ring, kSecond, plan.most_rows * RPS, BOX);
                     // All hidden rows are written.  (One counter for all experts: the
                     // shares are equal, so that waiting for some of them first gains nothing,
