@@ -39,6 +39,11 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kFewMax = MOE_FEW_MAX_TOKENS;
 constexpr int kMaxSlots = kFewMax * 16;   // T * k
 
+// These kernels begin while the kernel before them may still write what they read
+// after their wait.  So nothing is read through the non-coherent path, whose data
+// must not change while a kernel runs: no ld.global.nc, no const __restrict__ pointer
+// that would let the compiler choose it.
+
 // 16 bytes of T as floats
 template <typename T> struct Vec;
 template <> struct Vec<float> {
@@ -98,9 +103,8 @@ constexpr int kLogitThreads = 256;
 
 template <typename T, int EE, int TT>
 __global__ void __launch_bounds__(kLogitThreads)
-    few_logits_kernel(int tokens, int d, int E, const T* __restrict__ x, const T* __restrict__ Wg,
-                      const float* __restrict__ beta, float* __restrict__ logits,
-                      int* __restrict__ counters, int words) {
+    few_logits_kernel(int tokens, int d, int E, const T* x, const T* Wg, const float* beta,
+                      float* logits, int* counters, int words) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -267,7 +271,7 @@ __device__ __forceinline__ void add_release(int* p, int v) {
 // 16 bytes of T, streamed past L1
 __device__ __forceinline__ uint4 stream16(const void* p) {
     uint4 u;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
     return u;
 }

@@ -151,7 +151,7 @@ __device__ __forceinline__ void square_chunk(const Chunk& c, SquareSum& sum) {
     #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
         const int j = threadIdx.x + i * kGradThreads;
-        u[i] = j < nv ? __ldg(q + j) : make_uint4(0u, 0u, 0u, 0u);
+        u[i] = j < nv ? __ldcg(q + j) : make_uint4(0u, 0u, 0u, 0u);
     }
     const int rest = c.n - nv * N;   // head and tail, fewer than 2 N
     if ((int)threadIdx.x < rest) {
@@ -180,10 +180,11 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
     return s;
 }
 
+// It begins while the kernel before it may still write the gradients: they are read
+// past the L1, and not through the non-coherent path, after the wait.
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
-    grad_square_kernel(const __grid_constant__ GradTable<CAP> t, double* __restrict__ partial,
-                       int* __restrict__ ticket) {
+    grad_square_kernel(const __grid_constant__ GradTable<CAP> t, double* partial, int* ticket) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ double buf[kGradThreads / 32];
@@ -215,7 +216,7 @@ __device__ __forceinline__ float finish_norm(const double* partial, int np, doub
 }
 
 __global__ void __launch_bounds__(kGradThreads)
-    grad_norm_kernel(const double* __restrict__ partial, int np, float* norm, int32_t* status) {
+    grad_norm_kernel(const double* partial, int np, float* norm, int32_t* status) {
     __shared__ double buf[kGradThreads / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     finish_norm(partial, np, buf, norm, status, true);
@@ -263,9 +264,9 @@ template <typename T> __device__ __forceinline__ void scale_chunk(const Chunk& c
 // 0: the norm is there.
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kScaleBlocksPerSm)
-    grad_scale_kernel(const __grid_constant__ GradTable<CAP> t, const double* __restrict__ partial,
-                      int np, float max_norm, float* norm, int writes_norm, int in_place,
-                      int* __restrict__ ticket, int32_t* status) {
+    grad_scale_kernel(const __grid_constant__ GradTable<CAP> t, const double* partial, int np,
+                      float max_norm, float* norm, int writes_norm, int in_place, int* ticket,
+                      int32_t* status) {
     __shared__ double buf[kGradThreads / 32];
     __shared__ int next[2];
     int c = t.first[t.count] - 1 - (int)blockIdx.x;
