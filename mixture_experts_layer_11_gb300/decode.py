@@ -22,8 +22,9 @@ class FewTokenPass:
     or fp32; k experts per token; renorm; beta [E] fp32 or None.  The tensors
     are read at every call, so weights updated in place take effect.
 
-    ``y``, the workspace and the status word are this object's: calls of one
-    object run in order on one stream (use an object per stream)."""
+    ``y``, the workspace and the status word are this object's, on the weights'
+    device, whichever is current: calls of one object run in order on one stream
+    (use an object per stream), the current one of that device."""
 
     def __init__(self, T: int, Wg, W1, b1, W2, b2, k: int, renorm: int,
                  beta: Optional[torch.Tensor] = None):
@@ -41,7 +42,8 @@ class FewTokenPass:
         self._weights = (Wg, beta, W1, b1, W2, b2)   # kept alive
         self.params = ops.make_layer_params(self.shape, *self._weights)
         dev = W1.device
-        n = ops.moe_layer_few_workspace_size(self.shape)
+        with torch.cuda.device(dev):
+            n = ops.moe_layer_few_workspace_size(self.shape)
         if n == 0:
             raise ValueError("the layer's shape is not one that moe_layer_few takes")
         self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
@@ -66,7 +68,18 @@ class FewTokenPass:
             raise ValueError(f"x is {tuple(size)}, expected [t, {self.d}] with t <= {self.T}")
         if residual is not None and residual.shape != size:
             raise ValueError(f"residual is {tuple(residual.shape)}, expected {tuple(size)}")
+        for t in (x, residual, out):
+            if t is not None and t.get_device() != self._device:
+                raise ops.MoEError("moe_layer_few", ops.MOE_ERR_INVALID,
+                                   f"tensor on {t.device}, the weights on cuda:{self._device}")
         self.shape.T = size[0]
+        if torch.cuda.current_device() == self._device:
+            self._launch(x, residual, y)
+        else:
+            with torch.cuda.device(self._device):
+                self._launch(x, residual, y)
+        return y
+
+    def _launch(self, x, residual, y):
         ops.moe_layer_few(self.shape, self.params, x, residual, y, *self._owned,
                           stream=ops.raw_stream(self._device))
-        return y

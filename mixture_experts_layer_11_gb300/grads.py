@@ -17,18 +17,20 @@ from . import ops
 
 
 class GradClip:
-    """tensors: the gradients (CUDA, contiguous, fp32 or bf16; any sizes, views
-    of flat buffers included, none twice); outs: for each a tensor of its size
-    and type that ``clip`` writes, or None for all: in place.  The norm, the
-    workspace and the status word are this object's: calls of one object run in
-    order on one stream."""
+    """tensors: the gradients (on one CUDA device, whichever is current;
+    contiguous, fp32 or bf16; any sizes, views of flat buffers included, none
+    twice); outs: for each a tensor of its size and type that ``clip`` writes, or
+    None for all: in place.  The norm, the workspace and the status word are this
+    object's: calls of one object run in order on one stream, the current one of
+    the gradients' device."""
 
     def __init__(self, tensors, outs=None):
         self._tensors = (list(tensors), None if outs is None else list(outs))   # kept alive
         self.grads = ops.make_grads(*self._tensors)
         dev = self._tensors[0][0].device if self._tensors[0] else torch.device("cuda")
-        self.ws = torch.empty(ops.moe_grad_workspace_size(len(self.grads)), dtype=torch.uint8,
-                              device=dev)
+        with torch.cuda.device(dev):
+            n = ops.moe_grad_workspace_size(len(self.grads))
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
         self.total = torch.zeros((), dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._device = self.total.device.index
@@ -37,12 +39,18 @@ class GradClip:
     def norm(self) -> torch.Tensor:
         """The norm of all gradients (a fp32 scalar owned by this object); sets
         ``status`` to MOE_ERR_NONFINITE when it is infinite or NaN."""
-        ops.moe_grad_norm(self.grads, *self._owned, stream=ops.raw_stream(self._device))
-        return self.total
+        return self._launch(ops.moe_grad_norm, self.grads)
 
     def clip(self, max_norm: float) -> torch.Tensor:
         """Scale the gradients by max_norm / norm if norm > max_norm (else, and
         with a norm that is not finite, they stay or are copied to outs as they
         are).  Returns the norm before."""
-        ops.moe_grad_clip(self.grads, max_norm, *self._owned, stream=ops.raw_stream(self._device))
+        return self._launch(ops.moe_grad_clip, self.grads, max_norm)
+
+    def _launch(self, call, *args):
+        if torch.cuda.current_device() == self._device:
+            call(*args, *self._owned, stream=ops.raw_stream(self._device))
+        else:
+            with torch.cuda.device(self._device):
+                call(*args, *self._owned, stream=ops.raw_stream(self._device))
         return self.total

@@ -333,6 +333,22 @@ def raw_stream(device_index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device_index)
 
 
+def one_device(fn: str, *tensors):
+    """The CUDA device that all tensors (None: not given) are on; None without
+    tensors.  The library launches on the current device and takes addresses,
+    so it cannot tell that a tensor is on another one."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise MoEError(fn, MOE_ERR_INVALID, "tensor is not on a CUDA device")
+        if dev is not None and t.device != dev:
+            raise MoEError(fn, MOE_ERR_INVALID, f"tensors on {dev} and {t.device}")
+        dev = t.device
+    return dev
+
+
 FEW_MAX_TOKENS = 64  # MOE_FEW_MAX_TOKENS in include/moe.h
 
 
@@ -340,6 +356,7 @@ def make_layer_params(s, Wg, logit_bias, W1, b1, W2, b2) -> moe_layer_params:
     """The parameter struct of moe_layer_few.  It holds addresses only: keep the
     tensors alive while it is used."""
     act = _act(s)
+    one_device("make_layer_params", Wg, logit_bias, W1, b1, W2, b2)
     return moe_layer_params(_ptr(Wg, act), _ptr(logit_bias, _F32), _ptr(W1, act), _ptr(b1, act),
                             _ptr(W2, act), _ptr(b2, act))
 
@@ -357,13 +374,14 @@ def moe_layer_few(s, params: moe_layer_params, x, residual, y, ws, dev_status, s
 def make_grads(tensors, outs=None):
     """A list of gradients as moe_grad_norm / moe_grad_clip take it: a ctypes
     array of moe_grad (a fresh one for other tensors; it holds addresses only:
-    keep the tensors alive while it is used).  tensors: CUDA tensors, contiguous,
-    fp32 or bf16, any sizes; outs: a tensor or None (in place) for each."""
+    keep the tensors alive while it is used).  tensors: on one CUDA device,
+    contiguous, fp32 or bf16, any sizes; outs: a tensor or None (in place) for each."""
     fn = "make_grads"
     tensors = list(tensors)
     outs = [None] * len(tensors) if outs is None else list(outs)
     if len(outs) != len(tensors):
         raise MoEError(fn, MOE_ERR_INVALID, f"{len(outs)} outs for {len(tensors)} gradients")
+    one_device(fn, *tensors, *outs)
     arr = (moe_grad * len(tensors))()
     for a, t, o in zip(arr, tensors, outs):
         if t.dtype not in (torch.float32, torch.bfloat16):
