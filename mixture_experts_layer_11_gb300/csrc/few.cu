@@ -1610,20 +1610,26 @@ bool few_map(CUtensorMap* m, const void* p, uint64_t n0, uint64_t n1, uint64_t n
 constexpr int kFewSmem = 227 * 1024;
 
 template <typename T> cudaError_t few_smem_limit(int* dynamic) {
-    // what the static part leaves; looked up once
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int most = 0;
-    std::call_once(once, [] {
+    // what the static part leaves; set once for each device, as the limit is the device's
+    static std::mutex lock;
+    static int limit[64] = {0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> hold(lock);
+    if (limit[dev] == 0) {
         cudaFuncAttributes a;
         err = cudaFuncGetAttributes(&a, few_experts_kernel<T>);
-        if (err != cudaSuccess) return;
-        most = (kFewSmem - (int)a.sharedSizeBytes) & ~127;
+        if (err != cudaSuccess) return err;
+        const int most = (kFewSmem - (int)a.sharedSizeBytes) & ~127;
         err = cudaFuncSetAttribute(few_experts_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    most);
-    });
-    *dynamic = most;
-    return err;
+        if (err != cudaSuccess) return err;
+        limit[dev] = most;
+    }
+    *dynamic = limit[dev];
+    return cudaSuccess;
 }
 
 template <typename T, int TT, int RW, int U>
