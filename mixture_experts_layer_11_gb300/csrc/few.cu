@@ -94,6 +94,62 @@ template <int V> __device__ __forceinline__ float warp_sums(float (&v)[V], int& 
     return v[0];
 }
 
+// ---- GELU ------------------------------------------------------------------------------
+// x Phi(x) with a small relative error in both tails, as hidden activations are held to
+// more than bf16's precision each: 1 + erf(x / sqrt 2) would lose all of it from -5 on.
+// Phi(-|x|) = R(|x|) phi(x) with the Mills ratio R; R / t, t = 1 / (1 + p |x|), is a
+// smooth function of t, here the polynomial with the least relative error for |x| <=
+// 13.2, beyond which phi is below 2^-126 and taken as 0.
+
+// One value, to 2^-21: degree 7 (2^-24), p = 0.3041, phi's factor in the polynomial; the
+// rounding errors of the exponent enter as a factor 1 + ln 2 * low.
+__device__ __forceinline__ float gelu_one(float x) {
+    const float a = fminf(fabsf(x), 16.f), t = rcp_approx(fmaf(0.3041f, a, 1.0f));
+    float r = 0.036699917f;
+    r = fmaf(t, r, -0.1545382f);
+    r = fmaf(t, r, 0.190735817f);
+    r = fmaf(t, r, -0.0419697948f);
+    r = fmaf(t, r, 0.123010464f);
+    r = fmaf(t, r, 0.102595039f);
+    r = fmaf(t, r, 0.122191094f);
+    r = fmaf(t, r, 0.121275641f);
+    constexpr float c = -0.72134752f, c_low = -9.62981495e-9f;   // -log2(e) / 2 in two parts
+    const float s = a * a, power = s * c;
+    const float low = fmaf(fmaf(a, a, -s), c, fmaf(s, c_low, fmaf(s, c, -power)));
+    float e = ex2_approx(power);
+    e = fmaf(e * low, 0.693147181f, e);
+    const float q = t * r * e;                         // Phi(-|x|)
+    return x * (x >= 0.f ? 1.0f - q : q);
+}
+// One copy of it for the expert kernel, whose instructions run once or twice a launch (33
+// fp32 tokens of the skewed layer: 55.9 us so, inlined 56.6, with CUDA's normcdff 57.7).
+__device__ __noinline__ float gelu_call(float x) { return gelu_one(x); }
+
+// Two values, for hidden activations of 16 bits: degree 6 (2^-21), p = 0.2638.  Off by at
+// most 2^-18.4 for |x| <= 8 and 2^-16.5 for |x| <= 13 (the rounding of the exponent).
+__device__ __forceinline__ uint64_t gelu_two(float x0, float x1) {
+    const float t0 = rcp_approx(fmaf(0.2638f, fabsf(x0), 1.0f));
+    const float t1 = rcp_approx(fmaf(0.2638f, fabsf(x1), 1.0f));
+    const uint64_t x = f2_pack(x0, x1), t = f2_pack(t0, t1);
+    // log2 of phi: -x^2 log2(e) / 2 - log2(sqrt(2 pi))
+    const uint64_t arg = f2_fma(f2_mul(x, x), f2_pack(-0.72134752f, -0.72134752f),
+                                f2_pack(-1.32574806f, -1.32574806f));
+    float a0, a1;
+    f2_unpack(arg, a0, a1);
+    const uint64_t phi = f2_pack(ex2_approx(a0), ex2_approx(a1));
+    uint64_t r = f2_pack(-0.174574688f, -0.174574688f);
+    r = f2_fma(t, r, f2_pack(0.51463443f, 0.51463443f));
+    r = f2_fma(t, r, f2_pack(-0.197119161f, -0.197119161f));
+    r = f2_fma(t, r, f2_pack(0.376498967f, 0.376498967f));
+    r = f2_fma(t, r, f2_pack(0.200137436f, 0.200137436f));
+    r = f2_fma(t, r, f2_pack(0.2703242f, 0.2703242f));
+    r = f2_fma(t, r, f2_pack(0.263412178f, 0.263412178f));
+    const uint64_t q = f2_mul(f2_mul(t, r), phi);                                 // Phi(-|x|)
+    const uint64_t w = f2_fma(q, f2_pack(-2.0f, -2.0f), f2_pack(1.0f, 1.0f));     // 1 - 2q
+    const uint64_t st = f2_pack(x0 >= 0.f ? 1.0f : 0.0f, x1 >= 0.f ? 1.0f : 0.0f);
+    return f2_mul(x, f2_fma(st, w, q));
+}
+
 // ---- router logits -----------------------------------------------------------------
 // L[t,e] = <x_t, Wg_e> + beta_e in fp32.  A block computes EE experts x TT tokens;
 // its warps split d (16 bytes a lane and step), their sums are added in warp order.
@@ -426,7 +482,7 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
                     const int s = slot[a1][t];
                     if (s != 255) {
                         if (g.b1) v += to_f32<T>(((const T*)g.b1)[(int64_t)act[a1] * M + row]);
-                        g.hidden[(int64_t)s * M + row] = w[s] * gelu_f(v);
+                        g.hidden[(int64_t)s * M + row] = w[s] * gelu_one(v);
                     }
                 } else {
                     const int64_t o = (int64_t)t * M + row;
@@ -454,8 +510,9 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
 //           sum over the experts of an output tile in shared memory.  fp32: they do
 //           the products themselves.
 // In bf16 hidden activations are stored as two bf16 numbers each, high and low
-// part, and enter the second product as two columns: 16 bits of them count, for
-// no more than twice the narrow operand's bytes.
+// part, and enter the second product as two columns: they are held to 2^-16 of each,
+// for no more than twice the narrow operand's bytes.  (few_direct_kernel holds them in
+// fp32, as this kernel does in fp32.)
 constexpr int kTileM = 128;          // weight rows (output features) of a tile
 constexpr int kBlockBytes = 128;     // one K block of a row: 64 bf16 or 32 fp32
 constexpr int kABytes = kTileM * kBlockBytes;
@@ -1401,7 +1458,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                     if constexpr (K::kTensor) {
                         // GELU in two bf16 parts, 16 bits together
                         float v0, v1;
-                        f2_unpack(f2_mul(f2_pack(h0, h1), gelu_parts_fast2(h0, h1).Phi), v0, v1);
+                        f2_unpack(gelu_two(h0, h1), v0, v1);
                         const __nv_bfloat162 hi = __floats2bfloat162_rn(v0, v1);
                         const float l0 = v0 - __low2float(hi), l1 = v1 - __high2float(hi);
                         const __nv_bfloat162 lo = __floats2bfloat162_rn(isfinite(l0) ? l0 : 0.f,
@@ -1414,7 +1471,7 @@ __global__ void __launch_bounds__(few_threads<T>(), 1)
                             p[3 * (int64_t)g.f] = lo.y;
                         }
                     } else {
-                        hidden[(int64_t)(r0 + r) * g.f + col] = gelu_f(h0);
+                        hidden[(int64_t)(r0 + r) * g.f + col] = gelu_call(h0);
                     }
                 };
                 auto emit = [&](int r, bool two, float v0, float v1) {
