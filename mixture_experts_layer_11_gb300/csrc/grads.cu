@@ -222,14 +222,17 @@ __global__ void __launch_bounds__(kGradThreads)
     finish_norm(partial, np, buf, norm, status, true);
 }
 
-template <typename T> __device__ __forceinline__ void scale_chunk(const Chunk& c, float f) {
+// out = grad * f * f2; f2 is 1, or 2^-126 where the factor alone would not be a normal
+// number: that happens next to never, so the vectors' path goes without it.
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const Chunk& c, float f, float f2) {
     constexpr int N = Vec<T>::N;
     const T* p = (const T*)c.src;
     T* o = (T*)c.dst;
     const int head = head_of<T>(p, c.n);
     const bool vec = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
-    if (!vec) {   // the two sides never meet a 16-byte boundary together
-        for (int i = threadIdx.x; i < c.n; i += kGradThreads) o[i] = from_f32<T>(to_f32<T>(p[i]) * f);
+    if (!vec || f2 != 1.f) {   // the two sides never meet a 16-byte boundary together, or as above
+        for (int i = threadIdx.x; i < c.n; i += kGradThreads) o[i] = from_f32<T>(to_f32<T>(p[i]) * f * f2);
         return;
     }
     const int nv = (c.n - head) / N;
@@ -275,15 +278,22 @@ __global__ void __launch_bounds__(kGradThreads, kScaleBlocksPerSm)
     const float n = np > 0 ? finish_norm(partial, np, buf, norm, status, writes_norm && blockIdx.x == 0)
                            : __ldcg(norm);
     // a norm within the bound, or none (infinite, NaN): the gradients as they are
-    const float f = isfinite(n) && n > max_norm ? max_norm / n : 1.f;
+    float f = isfinite(n) && n > max_norm ? max_norm / n : 1.f;
+    // Below fp32's normal range the factor would lose bits that the products, up to
+    // max_norm, have: 2^126 of it at first (n > 2^-23 then, max_norm < 4).
+    float f2 = 1.f;
+    if (f < 0x1p-126f && max_norm > 0.f) {
+        f = (max_norm * 0x1p63f) / (n * 0x1p-63f);
+        f2 = 0x1p-126f;
+    }
     if (f == 1.f && in_place) return;
     for (int turn = 0; c >= 0; turn ^= 1) {
         if (threadIdx.x == 0) next[turn] = (int)gridDim.x + atomicAdd(ticket, 1);
         while (c < t.first[i]) --i;
         const Chunk k = chunk_of(t, i, c);
         if (f != 1.f || k.src != k.dst) {
-            if (k.bf16) scale_chunk<__nv_bfloat16>(k, f);
-            else scale_chunk<float>(k, f);
+            if (k.bf16) scale_chunk<__nv_bfloat16>(k, f, f2);
+            else scale_chunk<float>(k, f, f2);
         }
         __syncthreads();
         c = t.first[t.count] - 1 - next[turn];
