@@ -438,9 +438,12 @@ MOE_API size_t moe_grad_workspace_size(int n);
  *   n, g  HOST array of n >= 0 tensors (copied before the call returns); more
  *         than 2^45 bytes in all are MOE_ERR_UNSUPPORTED
  *   norm  [1] fp32, out
- * Sums are held in 64 bits, and squares beyond fp32's range are scaled: the
- * norm is as good for gradients of 1e-30 or 1e30.  An infinite or NaN norm
- * sets *dev_status to MOE_ERR_NONFINITE.  Deterministic for a given list. */
+ * A thread adds at most 65 squares in fp32 and those sums as a pair of fp32
+ * numbers; what the threads have is added in 64 bits: the norm is off by at
+ * most 34 * 2^-24 of itself.  Squares beyond fp32's range are scaled, which
+ * holds for gradients of 1e-30 or 1e30 too.  An infinite or NaN norm (also one
+ * beyond fp32's largest number) sets *dev_status to MOE_ERR_NONFINITE.
+ * Deterministic for a given list. */
 MOE_API moe_status moe_grad_norm(int n, const moe_grad* g, float* norm, void* ws,
                                  int32_t* dev_status, moe_stream_t stream);
 

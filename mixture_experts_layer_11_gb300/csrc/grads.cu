@@ -91,7 +91,7 @@ struct SquareSum {
         else
             rare += rare_squares(a, b, c, d, m > 1.f ? 0x1p-80f : 0x1p100f);
     }
-    // the sum of one chunk's squares (at most 72 a thread)
+    // the sum of one chunk's squares (at most 64 in vectors and one beside them a thread)
     __device__ __forceinline__ void flush(float sum) {
         const float s = __fadd_rn(high, sum), b = __fsub_rn(s, high);
         low = __fadd_rn(low, __fadd_rn(__fsub_rn(high, __fsub_rn(s, b)), __fsub_rn(sum, b)));
