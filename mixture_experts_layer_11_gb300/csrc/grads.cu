@@ -68,10 +68,12 @@ template <int CAP> __device__ __forceinline__ int find_tensor(const GradTable<CA
     return lo;
 }
 
-// Sum of squares over the whole range of fp32 inputs: values whose squares
-// leave fp32's range are scaled by a power of two first and go to 64 bits.  Four
-// values go by their largest magnitude: what the others lose then is below 2^-40
-// of that value's square.  The common sum is kept as an unevaluated
+// Sum of squares over the whole range of fp32 inputs: values whose squares would
+// leave it are scaled by a power of two first and go to 64 bits.  Four values go by
+// their largest magnitude: between 2^-60 and 2^40 its square is 2^-120 at least, of
+// which the others' squares, rounded to 2^-150, lose less than 2^-28, and a sum of
+// 2^47 such squares stays finite.  Gradients below 1e-18 take the other way: 537 M in
+// 787 us, against 295 (bf16 777, against 153).  The common sum is kept as an unevaluated
 // pair of fp32 (each chunk's sum added exactly, by the error of an addition being
 // an fp32 number itself), since 64-bit additions run at a small fraction of the
 // rate here.
@@ -86,7 +88,7 @@ struct SquareSum {
     double rare = 0.0;
     __device__ __forceinline__ void add(float a, float b, float c, float d, float& sum) {
         const float m = fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d)));   // no NaN
-        if (m <= 0x1p40f && (m >= 0x1p-40f || m == 0.f))
+        if (m <= 0x1p40f && (m >= 0x1p-60f || m == 0.f))
             sum = fmaf(a, a, fmaf(b, b, fmaf(c, c, fmaf(d, d, sum))));
         else
             rare += rare_squares(a, b, c, d, m > 1.f ? 0x1p-80f : 0x1p100f);

@@ -49,6 +49,20 @@ def test_factors_below_the_normal_numbers(dtype, in_place, size, scale, bound):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("power", list(range(-66, -36)) + [38, 39, 40, 41])
+def test_norm_where_the_way_of_adding_changes(dtype, power):
+    # groups of four around the magnitudes where squares are scaled, alone and beside much smaller ones
+    g = torch.Generator(device=DEV)
+    g.manual_seed(power + 100)
+    t = torch.randn(70001, generator=g, device=DEV) * 2.0 ** power
+    small = torch.randn(70001, generator=g, device=DEV) * 2.0 ** (power - 12)
+    mixed = torch.where(torch.arange(70001, device=DEV) % 4 == 1, t, small)
+    for v in (t.to(dtype), mixed.to(dtype)):
+        want = norm64([v])
+        assert abs(float(GradClip([v]).norm()) - want) <= NORM * want
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("value", [1.0, 1.0 + 2.0 ** -7, 0.3, 2.0 ** -30])
 def test_norm_where_every_rounding_goes_one_way(dtype, value):
     # equal values: the fp32 sums of a thread grow by the same term each time
