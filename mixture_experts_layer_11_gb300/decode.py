@@ -83,3 +83,8 @@ class FewTokenPass:
     def _launch(self, x, residual, y):
         ops.moe_layer_few(self.shape, self.params, x, residual, y, *self._owned,
                           stream=ops.raw_stream(self._device))
+
+    def check_status(self):
+        """Synchronises and raises if one of the calls since the last check
+        reported a device-side error (the first of them)."""
+        ops.take_status(self.status)

@@ -54,3 +54,8 @@ class GradClip:
             with torch.cuda.device(self._device):
                 call(*args, *self._owned, stream=ops.raw_stream(self._device))
         return self.total
+
+    def check_status(self):
+        """Synchronises and raises if one of the calls since the last check
+        reported a device-side error (the first of them)."""
+        ops.take_status(self.status)

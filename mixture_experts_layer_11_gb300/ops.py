@@ -327,6 +327,15 @@ def moe_route_noalloc(s, x, Wg, logit_bias, logits, compute_logits, idx, w, coun
         _ptr(dev_status, _I32), _stream(stream)))
 
 
+def take_status(status):
+    """Synchronises and raises if a kernel reported a device-side error in the
+    status word, which keeps the first one; the word is then empty again."""
+    code = int(status.item())
+    if code != MOE_OK:
+        status.zero_()
+        raise MoEError("device", code, moe_status_string(code))
+
+
 def raw_stream(device_index: int) -> int:
     """The current stream's handle, for calls a few microseconds long: without
     the torch.cuda.Stream object that torch.cuda.current_stream() makes."""
