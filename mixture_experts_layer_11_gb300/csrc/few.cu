@@ -12,8 +12,10 @@
 // byte in bf16 against 290 that the GPU has), and beside it the latencies between
 // its dependent steps.  So both expert kernels stream every chosen weight once, in
 // equal shares over all SMs, and do all the rest of the layer in the same launch:
-// what a step waits for is a counter in memory, not a launch.  The launch itself
-// overlaps the logits kernel's.
+// what a step waits for is a counter in memory, not a launch.  The second launch may
+// begin during the first, so that a block is set up as soon as its SM is free.  (A block
+// of the large kernel needs an SM's whole shared memory and nearly all its registers, so
+// that it never shares one with a block of the logits kernel.)
 //
 // Measured on a GB300 (device time of both launches in a graph, weights from HBM):
 //   bf16, d = 4096, f = 1024, 128 experts, top-8:  64 tokens (all 2.1 GB of weights)
@@ -287,7 +289,10 @@ constexpr int kDirectTokens = 4;
 // against 19.9 us in bf16 and 14.0 against 22.7 in fp32; d = 512, f = 2048, 4 tokens
 // (17 M weights) 19.5 against 20.4 and 25.1 against 27.6; d = 768, f = 3072, 2 tokens
 // (19 M) 24.3 against 23.1 and 28 against 32.7, 3 tokens (28 M) 28.5 against 24.2
-// and 36.6 against 34.6.
+// and 36.6 against 34.6.  Over ten more layers (1 to 128 experts, top-1 to top-8, the L2
+// flushed) this kernel was the faster one below the limits, but for one by 1 us; above
+// them as fast or slower, by up to 43 us (4 tokens, top-8 of 128 experts of 4096 x 1024),
+// unless tokens share experts (one expert of 1024 x 4096: 5 to 7 us faster).
 template <typename T> constexpr int64_t direct_weights() {
     return int64_t(sizeof(T) == 2 ? 17 : 24) << 20;
 }
@@ -506,8 +511,8 @@ __global__ void __launch_bounds__(kDirectThreads, direct_blocks_per_sm<TT>())
 //   warp 1  loads the activations: all tokens' K block of x (columns of tokens that
 //           are not the expert's are left unused), then the expert's hidden rows;
 //   warp 2  (bf16) issues the MMAs, into one of two accumulators;
-//   4 or 8 warps  take the accumulators out: GELU and hidden rows, or the gate-weighted
-//           sum over the experts of an output tile in shared memory.  fp32: they do
+//   8 (fp32) or 12 warps  take the accumulators out: GELU and hidden rows, or the gate-
+//           weighted sum over the experts of an output tile in shared memory.  fp32: they do
 //           the products themselves.
 // In bf16 hidden activations are stored as two bf16 numbers each, high and low
 // part, and enter the second product as two columns: they are held to 2^-16 of each,
@@ -579,9 +584,10 @@ struct FewArgs {
 };
 
 // ---- dispatch -----------------------------------------------------------------------
-// Every block of the expert kernel works out the gate for itself and sorts the
-// (token, slot) pairs (1024 of them at most): rows by expert, then by token.  That
-// takes it less time than to wait for another block's result.
+// Every block of the expert kernel sorts the (token, slot) pairs (1024 of them at
+// most) for itself: rows by expert, then by token.  With few tokens each also works out
+// the gate, which takes it less time than to wait for another block's result; with more
+// the blocks share it out (gate_plan).
 struct Sorted {
     unsigned long long tokens[256];   // bit t: token t goes to this expert
     int off[257];                     // first row of each expert
@@ -1662,8 +1668,8 @@ bool few_map(CUtensorMap* m, const void* p, uint64_t n0, uint64_t n1, uint64_t n
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Of the 227 KB a block may have; the rest lets blocks of the logits kernel share
-// the SM, so that this kernel's blocks are set up while those run.
+// All that a block may have: with less it would still not share an SM with a block of the
+// logits kernel, for want of registers.
 constexpr int kFewSmem = 227 * 1024;
 
 template <typename T> cudaError_t few_smem_limit(int* dynamic) {
