@@ -22,7 +22,7 @@
 //     339 us, 6.2 TB/s; one token (134 MB) 35 us, 3.9 TB/s
 //   bf16, d = 2048, f = 8192, 16 experts, top-2:   13 tokens (0.87 GB) 153 us, 5.7 TB/s
 //   bf16, d = 768, f = 3072, 8 experts, top-2:     64 tokens (76 MB) 41 us; one 13 us
-//   fp32, d = 768, f = 3072, 64 experts, top-1, skewed: 33 tokens (38 MB) 56 us
+//   fp32, d = 768, f = 3072, 64 experts, top-1, skewed: 33 tokens (38 or 57 MB) 53 to 56 us
 // At the large sizes memory bounds it (its streams alone run at 6.7 to 6.9 TB/s);
 // about 25 us are the logits, the gate, the hand-over between the products and
 // the adding of split tiles, which bound the small sizes.
@@ -98,7 +98,7 @@ template <int V> __device__ __forceinline__ float warp_sums(float (&v)[V], int& 
 
 // ---- GELU ------------------------------------------------------------------------------
 // x Phi(x) with a small relative error in both tails, as hidden activations are held to
-// more than bf16's precision each: 1 + erf(x / sqrt 2) would lose all of it from -5 on.
+// more than bf16's precision each: 1 + erf(x / sqrt 2) would lose nearly all of it below -5.
 // Phi(-|x|) = R(|x|) phi(x) with the Mills ratio R; R / t, t = 1 / (1 + p |x|), is a
 // smooth function of t, here the polynomial with the least relative error for |x| <=
 // 13.2, beyond which phi is below 2^-126 and taken as 0.
