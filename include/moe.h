@@ -453,6 +453,88 @@ MOE_API moe_status moe_grad_norm(int n, const moe_grad* g, float* norm, void* ws
 MOE_API moe_status moe_grad_clip(int n, const moe_grad* g, float max_norm, float* norm, void* ws,
                                  int32_t* dev_status, moe_stream_t stream);
 
+/* ---- losses over a vocabulary head -----------------------------------------------------
+ *
+ * The end of a model's forward pass and the start of its backward pass: a head
+ * W [V,d] turns the last hidden states x [T,d] into logits x W^T over a
+ * vocabulary, and a loss of them into dx and dW ("Flattening Every Memory Peak in
+ * Long-Context Mixture-of-Experts Training", abstract: the vocabulary projection
+ * with an online log-sum-exp, whose logits are that training's largest buffer).
+ * The logits are never kept: each product's tile of them goes straight into the
+ * rows' running maxima and sums.  The gradients hold one 16-bit number (fp32: one
+ * of 32 bits) a logit for `piece` tokens at a time.
+ *
+ * With z = x W^T / temperature, lse = log(sum_v exp(z_v)), p = exp(z - lse), a
+ * token's loss and its gradient by the logits (before weight and scale) are
+ *   moe_head_ce       lse - z_y                           p - [v = y]
+ *   moe_head_distill  temperature^2 sum_j q_j (log q_j - z_{v_j} + lse)
+ *                                           temperature (p - sum_j q_j [v = v_j])
+ * where y is the token's target (temperature 1), and (v_j, q_j) are a teacher's
+ * entries for the token: q the softmax of logits_j / temperature over the entries
+ * that are present.  An entry is absent when its index is below 0 or its logit is
+ * -infinity; a vocabulary index twice in a list counts with the sum of both.
+ * A token without a target (below 0), or with no entry present, is ignored: its
+ * loss, lse and dx are 0, and x there is not looked at (it may hold NaN).  An index
+ * of V or more counts as absent and sets *dev_status to MOE_ERR_INVALID. */
+#define MOE_HEAD_MAX_ENTRIES 128
+
+typedef struct {
+    int64_t T;        /* tokens of this call, 0 <= T < 2^31 */
+    int64_t piece;    /* tokens of which the gradients hold the probabilities at a time;
+                         rounded up to a multiple of 256; 0: as many as 2 GiB hold */
+    int32_t V;        /* vocabulary, 1 <= V <= 2^22 */
+    int32_t d;        /* width, d % 8 == 0, d <= 2^20 */
+    int32_t entries;  /* moe_head_distill: entries of a token's list, 1 to
+                         MOE_HEAD_MAX_ENTRIES; moe_head_ce: 1 */
+    int32_t dtype;    /* moe_dtype of x, W and dx */
+} moe_head;
+
+/* What the gradients need beside the loss.  With row factors
+ *   g_t = scale * weight[t] / (mean ? number of tokens not ignored : 1)
+ * dx = (g G) W and dW (+)= (g G)^T x, G the gradients by the logits above. */
+typedef struct {
+    const float* weight;  /* [T] fp32 or NULL (1) */
+    void* dx;             /* [T,d] dtype, out, or NULL: not wanted */
+    void* dW;             /* [V,d], out, or NULL: not wanted */
+    float scale;
+    int32_t mean;         /* 0 or 1 */
+    int32_t dW_dtype;     /* MOE_F32, or dtype */
+    int32_t accumulate;   /* 1: dW is added to (fp32 only), 0: overwritten */
+} moe_head_grad;
+
+/* Bytes of workspace for one call, and for any with fewer tokens; g as in the
+ * call (its pointers say only what is wanted), NULL for the losses alone.  0 for
+ * arguments that the calls refuse. */
+MOE_API size_t moe_head_workspace_size(const moe_head* h, const moe_head_grad* g);
+
+/*   x       [T,d] dtype       W  [V,d] dtype
+ *   target  [T] int64
+ *   loss    [T] fp32, out     lse  [T] fp32, out, or NULL
+ *   g       gradients, or NULL: the losses alone (scores of given tokens)
+ *   ws      workspace (contents need no initialisation, garbage after)
+ *   dev_status  MOE_ERR_NONFINITE on a loss that is not finite, MOE_ERR_INVALID
+ *           on an index of V or more, MOE_ERR_TIMEOUT
+ * Precision: products are summed in fp32 (bf16: by the tensor cores, which drop
+ * what is below the accumulator's last bit), softmax statistics, losses and the
+ * entries' own logits are fp32.  bf16 gradients: weight[t] G is rounded to bf16
+ * once, before the products with W and x; scale and the mean are applied to their
+ * fp32 sums; dx and dW are rounded once.  Deterministic: the same inputs give the
+ * same bits on the same GPU.  Can be captured in a CUDA graph. */
+MOE_API moe_status moe_head_ce(const moe_head* h, const void* x, const void* W,
+                               const int64_t* target, float* loss, float* lse,
+                               const moe_head_grad* g, void* ws, int32_t* dev_status,
+                               moe_stream_t stream);
+
+/*   idx     [T,entries] int64, logits [T,entries] fp32: the teacher's entries, in
+ *           any order
+ *   temperature  > 0, finite
+ *   others as moe_head_ce (lse is that of z = x W^T / temperature). */
+MOE_API moe_status moe_head_distill(const moe_head* h, const void* x, const void* W,
+                                    const int64_t* idx, const float* logits,
+                                    float temperature, float* loss, float* lse,
+                                    const moe_head_grad* g, void* ws, int32_t* dev_status,
+                                    moe_stream_t stream);
+
 /* Diagnostics: launch one kernel that waits on a device flag that nothing
  * sets, with the library's bounded wait (limit_ns nanoseconds), then writes
  * MOE_ERR_TIMEOUT to *dev_status and returns.  It exercises the timeout path

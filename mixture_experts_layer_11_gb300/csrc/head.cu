@@ -1,0 +1,471 @@
+// head.cu -- losses over a vocabulary head: cross entropy and distillation from a
+// teacher's top logits, with the gradients of the hidden states and the head.
+//
+// With z the logits over the temperature in bits (times log2 e) and blocks b of
+// 128 vocabulary entries, the first product's epilogue leaves, a row,
+//   m_b = max z - 15,  s_b = sum 2^(z - m_b)   and   E = 2^(z - m_b)
+// so that  lse = m + log2(sum_b s_b 2^(m_b - m)),  p = E 2^(m_b - lse).  E has 16
+// bits (fp16: 11 of precision, 2^-12 at most off), a piece of rows at a time; the
+// logits are not kept.  head_gradient_kernel turns E into the gradients
+//   G = w (p - q)
+// in place, the only rounding to bf16 in front of the other two products, with the
+// targets' own entries from their fp32 logits (p - 1 of a token that the model is
+// sure of would have none of E's bits).  6 T V d operations; working out the logits
+// a second time instead of keeping E would take 8 T V d, and E costs 10 bytes of
+// memory traffic a logit: at d = 768 three quarters of what those operations take.
+//
+// Ignored tokens cost nothing: the live rows of x are gathered in front (their
+// count stays on the device; grids are made for all tokens, tiles past the count
+// end at once), which also keeps what ignored rows hold out of every product.
+#include "head.h"
+
+namespace moe {
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int64_t kPieceBytes = int64_t(2) << 30;   // of E, where the caller sets no piece
+constexpr int kFewRows = 128;    // losses alone of up to this many rows: no gathering
+
+inline int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+struct Plan {
+    int64_t T, piece, pieces, Tp, Vp;
+    int nblk, K, esize;
+    bool few, backward, wide;   // wide: dW is summed in an fp32 buffer of the workspace
+    size_t ctl, live, xc, sidx, q, lq, ent, start, lz, stats, lse2, P, dW32, total;
+};
+
+Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
+    Plan p{};
+    p.T = h.T;
+    p.esize = h.dtype == MOE_BF16 ? 2 : 4;
+    p.K = h.entries;
+    p.backward = g != nullptr;
+    p.few = !p.backward && h.T <= kFewRows;
+    p.Vp = up(h.V, 64);
+    p.nblk = (h.V + kHeadBlock - 1) / kHeadBlock;
+    p.Tp = up(h.T > 0 ? h.T : 1, kHeadRows);
+    int64_t piece = p.Tp;
+    if (p.backward) {
+        int64_t most = h.piece;
+        if (most == 0) most = kPieceBytes / (p.Vp * p.esize) / kHeadRows * kHeadRows;
+        most = up(most > 0 ? most : 1, kHeadRows);
+        if (most < piece) piece = most;
+    }
+    p.piece = piece;
+    p.pieces = h.T > 0 ? (h.T + piece - 1) / piece : 0;
+    p.wide = p.backward && p.pieces > 1 && g->dW_dtype != MOE_F32;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t a = at;
+        at += (bytes + kAlign - 1) / kAlign * kAlign;
+        return a;
+    };
+    const size_t T = (size_t)(h.T > 0 ? h.T : 1), K = (size_t)p.K;
+    p.ctl = take(256);
+    p.lz = take(T * K * 4);
+    p.stats = take((size_t)p.nblk * piece * sizeof(float2));
+    p.lse2 = take((size_t)piece * 4);
+    if (distill) {
+        p.sidx = take(T * K * 4);
+        p.q = take(T * K * 4);
+        p.lq = take(T * K * 4);
+        p.ent = take(T * 4);
+        if (p.K > 1) p.start = take(T * (size_t)p.nblk);
+    }
+    if (!p.few) {
+        p.live = take((size_t)p.Tp * 4);
+        p.xc = take((size_t)p.Tp * h.d * p.esize);
+    }
+    if (p.backward) {
+        p.P = take((size_t)piece * p.Vp * p.esize);
+        if (p.wide) p.dW32 = take((size_t)h.V * h.d * 4);
+    }
+    p.total = at;
+    return p;
+}
+
+// ---- a teacher's entries ---------------------------------------------------------
+//
+// A warp a token: the softmax of the logits that are present, the entries in
+// ascending order of their index (absent ones behind), and the first entry of each
+// vocabulary block, so that a product's epilogue finds a tile's entries with one
+// load.
+__global__ void __launch_bounds__(128)
+    head_entries_kernel(const HeadDev h, const int64_t* idx, const float* logits, float inv_temp,
+                        int* sidx, float* q, float* lq, int* ent, uint8_t* start) {
+    __shared__ int key[4][MOE_HEAD_MAX_ENTRIES], sorted[4][MOE_HEAD_MAX_ENTRIES];
+    constexpr int N = MOE_HEAD_MAX_ENTRIES / 32;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * 4 + w;
+    if (t >= h.T) return;
+    const int64_t at = (int64_t)t * h.K;
+    float v[N], top = -INFINITY;
+    int k[N];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int j = i * 32 + lane;
+        k[i] = INT_MAX;
+        v[i] = -INFINITY;
+        if (j < h.K) {
+            const int64_t g = idx[at + j];
+            bad |= g >= h.V;
+            if (g >= 0 && g < h.V && logits[at + j] != -INFINITY) {
+                k[i] = (int)g;
+                v[i] = logits[at + j];
+                // NaN must not be lost in the maximum
+                top = isnan(v[i]) || isnan(top) ? NAN : fmaxf(top, v[i]);
+            }
+        }
+        key[w][j] = k[i];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, top, o);
+        top = isnan(u) || isnan(top) ? NAN : fmaxf(top, u);
+    }
+    float sum = 0.f;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool has = k[i] != INT_MAX;
+        count += has;
+        sum += has ? expf((v[i] - top) * inv_temp) : 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        count += __shfl_xor_sync(0xffffffffu, count, o);
+    }
+    if (bad) report(h.status, MOE_ERR_INVALID);
+    if (lane == 0) ent[t] = count;
+    __syncwarp();
+    const float lsum = logf(sum);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int j = i * 32 + lane;
+        if (j >= h.K) continue;
+        int rank = 0;
+        for (int u = 0; u < h.K; ++u) rank += key[w][u] < k[i] || (key[w][u] == k[i] && u < j);
+        const bool has = k[i] != INT_MAX;
+        const float l = has ? (v[i] - top) * inv_temp - lsum : 0.f;
+        sorted[w][rank] = k[i];
+        sidx[at + rank] = k[i];
+        const float e = has ? expf(l) : 0.f;
+        q[at + rank] = e;
+        lq[at + rank] = e == 0.f ? 0.f : l;   // l may be -infinity there; NaN stays
+    }
+    __syncwarp();
+    if (h.K == 1) return;
+    for (int b = lane; b < h.nblk; b += 32) {
+        const int first = b * kHeadBlock;
+        int lo = 0, hi = count;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (sorted[w][mid] < first) lo = mid + 1;
+            else hi = mid;
+        }
+        start[(int64_t)t * h.nblk + b] = (uint8_t)lo;
+    }
+}
+
+// ---- live rows ---------------------------------------------------------------------
+
+__device__ __forceinline__ bool token_live(const HeadDev& h, int t) {
+    if (!h.target) return h.ent[t] > 0;
+    const int64_t y = h.target[t];
+    return y >= 0 && y < h.V;
+}
+
+// One block: the live tokens in order, and their count.
+__global__ void __launch_bounds__(1024) head_scan_kernel(const HeadDev h, int* live, int* n_live) {
+    __shared__ int part[32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int base = 0;
+    for (int t0 = 0; t0 < h.T; t0 += 1024) {
+        const int t = t0 + threadIdx.x;
+        const bool on = t < h.T && token_live(h, t);
+        if (h.target && t < h.T && h.target[t] >= h.V) report(h.status, MOE_ERR_INVALID);
+        const unsigned mask = __ballot_sync(0xffffffffu, on);
+        if (lane == 0) part[w] = __popc(mask);
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int i = 0; i < 32; ++i) {
+            before += i < w ? part[i] : 0;
+            all += part[i];
+        }
+        if (on) live[base + before + __popc(mask & ((1u << lane) - 1))] = t;
+        base += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) *n_live = base;
+}
+
+// Warp i: row i of the gathered x (zeros behind the live rows, up to a whole tile),
+// and, if token i is ignored, its outputs.
+__global__ void __launch_bounds__(256)
+    head_gather_kernel(const HeadDev h, const uint4* x, uint4* xc, uint4* dx, int vecs, int64_t Tp) {
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (i >= Tp) return;
+    const int n = *h.n_live;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (i < n) {
+        const uint4* src = x + (int64_t)h.live[i] * vecs;
+        for (int v = lane; v < vecs; v += 32) xc[i * vecs + v] = src[v];
+    } else if (i < (int64_t)(n + kHeadRows - 1) / kHeadRows * kHeadRows) {
+        for (int v = lane; v < vecs; v += 32) xc[i * vecs + v] = zero;
+    }
+    if (i < h.T && !token_live(h, (int)i)) {
+        if (lane == 0) {
+            h.loss[i] = 0.f;
+            if (h.lse) h.lse[i] = 0.f;
+        }
+        if (dx)
+            for (int v = lane; v < vecs; v += 32) dx[i * vecs + v] = zero;
+    }
+}
+
+// ---- statistics to losses ----------------------------------------------------------
+//
+// A block takes 32 rows; lane = row, a warp every 32nd vocabulary block.
+__global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
+    __shared__ float ms[32][33], ss[32][33];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = head_rows(h), r0 = blockIdx.x * 32;
+    if (r0 >= n) return;
+    float m = -INFINITY, s = 0.f;
+    if (r0 + lane < n) {
+        for (int b = w; b < h.nblk; b += 32) {
+            const float2 v = h.stats[(int64_t)b * h.srows + r0 + lane];
+            // (NaN: the comparison fails, and the sum takes it on)
+            if (v.x > m) {
+                s = s * exp2f(m - v.x) + v.y;
+                m = v.x;
+            } else {
+                s += v.y * exp2f(v.x - m);
+            }
+        }
+    }
+    ms[w][lane] = m;
+    ss[w][lane] = s;
+    __syncthreads();
+    // now lane = warp's share, warp = row
+    const int r = r0 + w;
+    if (r >= n) return;
+    m = ms[lane][w];
+    s = ss[lane][w];
+    float top = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // (a share without blocks has m = -inf and s = 0)
+    s = s == 0.f ? 0.f : s * exp2f(m - top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float lse2 = top + log2f(s);
+    const int t = head_token(h, r);
+    if (!h.n_live && !token_live(h, t)) {
+        if (lane == 0) {
+            if (h.target && h.target[t] >= h.V) report(h.status, MOE_ERR_INVALID);
+            h.loss[t] = 0.f;
+            if (h.lse) h.lse[t] = 0.f;
+        }
+        return;
+    }
+    const int64_t at = (int64_t)t * h.K;
+    float loss = 0.f;
+    if (h.target) {
+        loss = (lse2 - h.lz[at] * h.c) * kLn2;
+    } else {
+        const int e = h.ent[t];
+        for (int j = lane; j < e; j += 32)
+            loss += h.q[at + j] * (h.lq[at + j] + (lse2 - h.lz[at + j] * h.c) * kLn2);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+        loss *= h.loss_scale;
+    }
+    if (lane == 0) {
+        if (!isfinite(loss) || !isfinite(lse2)) report(h.status, MOE_ERR_NONFINITE);
+        h.loss[t] = loss;
+        if (h.lse) h.lse[t] = lse2 * kLn2;
+        h.lse2[r] = lse2;
+    }
+}
+
+// ---- exponentials to gradients, in place ------------------------------------------------
+
+template <typename T> struct Pair;   // T: the gradients' type
+template <> struct Pair<__nv_bfloat16> {
+    static constexpr int N = 8;      // values of 16 bytes
+    static __device__ __forceinline__ uint4 scale(uint4 u, float f, int left) {
+        __half2* e = reinterpret_cast<__half2*>(&u);
+        uint4 out;
+        __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(&out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = __half22float2(e[i]);
+            o[i] = __floats2bfloat162_rn(2 * i < left ? v.x * f : 0.f, 2 * i + 1 < left ? v.y * f : 0.f);
+        }
+        return out;
+    }
+};
+template <> struct Pair<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ uint4 scale(uint4 u, float f, int left) {
+        return make_uint4(left > 0 ? __float_as_uint(__uint_as_float(u.x) * f) : 0u,
+                          left > 1 ? __float_as_uint(__uint_as_float(u.y) * f) : 0u,
+                          left > 2 ? __float_as_uint(__uint_as_float(u.z) * f) : 0u,
+                          left > 3 ? __float_as_uint(__uint_as_float(u.w) * f) : 0u);
+    }
+};
+
+constexpr int kGradCols = 4096;   // columns of a row a block turns
+
+template <typename T>
+__global__ void __launch_bounds__(256) head_gradient_kernel(const HeadDev h) {
+    const int r = blockIdx.x, c0 = blockIdx.y * kGradCols;
+    const int n = head_rows(h);
+    if (r >= (n + 63) / 64 * 64) return;
+    constexpr int N = Pair<T>::N;
+    T* row = (T*)h.P + (int64_t)r * h.Vp;
+    const int c1 = c0 + kGradCols < h.Vp ? c0 + kGradCols : h.Vp;
+    if (r >= n) {   // the last K block's rows behind the live ones
+        for (int c = c0 + threadIdx.x * N; c < c1; c += 256 * N)
+            *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int t = head_token(h, r);
+    const float lse2 = h.lse2[r];
+    const float weight = h.weight ? h.weight[t] : 1.f;
+    for (int c = c0 + threadIdx.x * N; c < c1; c += 256 * N) {
+        const float m = h.stats[(int64_t)(c / kHeadBlock) * h.srows + r].x;
+        uint4* p = reinterpret_cast<uint4*>(row + c);
+        *p = Pair<T>::scale(*p, weight * exp2f(m - lse2), h.V - c);
+    }
+    __syncthreads();
+    // the targets' entries, from their own logits
+    const int64_t at = (int64_t)t * h.K;
+    const int e = h.target ? 1 : h.ent[t];
+    for (int j = threadIdx.x; j < e; j += 256) {
+        const int k = h.target ? (int)h.target[t] : h.sidx[at + j];
+        if (k < c0 || k >= c1) continue;
+        float q = 1.f;
+        if (!h.target) {
+            if (j > 0 && h.sidx[at + j - 1] == k) continue;   // the first of equals writes
+            q = h.q[at + j];
+            for (int i = j + 1; i < e && h.sidx[at + i] == k; ++i) q += h.q[at + i];
+        }
+        row[k] = from_f32<T>(weight * (exp2f(fmaf(h.lz[at + j], h.c, -lse2)) - q));
+    }
+}
+
+__global__ void __launch_bounds__(256) head_round_kernel(const float4* in, uint2* out, int64_t n4) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+        const float4 v = in[i];
+        __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        out[i] = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    }
+}
+
+}  // namespace
+
+size_t head_workspace(const moe_head& h, const moe_head_grad* g) {
+    return make_plan(h, g, true).total;
+}
+
+cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
+    const moe_head& s = c.h;
+    const bool bf16 = s.dtype == MOE_BF16;
+    const bool distill = c.teacher != nullptr;
+    const moe_head_grad* g = c.g;
+    const bool want_dx = g && g->dx, want_dW = g && g->dW;
+    if (s.T == 0) {
+        if (want_dW && !g->accumulate)
+            return cudaMemsetAsync(g->dW, 0, (size_t)s.V * s.d * (g->dW_dtype == MOE_F32 ? 4 : 2), st);
+        return cudaSuccess;
+    }
+    const Plan p = make_plan(s, g, distill);
+    uint8_t* ws = (uint8_t*)c.ws;
+    HeadDev h{};
+    h.T = (int)s.T;
+    h.V = s.V;
+    h.d = s.d;
+    h.K = s.entries;
+    h.Vp = (int)p.Vp;
+    h.nblk = p.nblk;
+    h.rows = (int)p.piece;
+    h.srows = (int)p.piece;
+    if (!p.few) {
+        h.n_live = (const int*)(ws + p.ctl);
+        h.live = (const int*)(ws + p.live);
+    }
+    if (distill) {
+        h.sidx = (const int*)(ws + p.sidx);
+        h.q = (const float*)(ws + p.q);
+        h.lq = (const float*)(ws + p.lq);
+        h.ent = (const int*)(ws + p.ent);
+        h.start = ws + p.start;
+    } else {
+        h.target = c.idx;
+    }
+    h.lz = (float*)(ws + p.lz);
+    h.stats = (float2*)(ws + p.stats);
+    h.lse2 = (float*)(ws + p.lse2);
+    h.P = ws + p.P;
+    h.c = kLog2e / c.temperature;
+    h.loss_scale = c.temperature * c.temperature;
+    if (g) {
+        h.weight = g->weight;
+        h.grad_scale = g->scale * c.temperature;
+        h.mean = g->mean;
+    }
+    h.loss = c.loss;
+    h.lse = c.lse;
+    h.status = c.status;
+
+    if (distill)
+        head_entries_kernel<<<(unsigned)((s.T + 3) / 4), 128, 0, st>>>(
+            h, c.idx, c.teacher, 1.f / c.temperature, (int*)(ws + p.sidx), (float*)(ws + p.q),
+            (float*)(ws + p.lq), (int*)(ws + p.ent), ws + p.start);
+    const void* xc = c.x;
+    if (!p.few) {
+        head_scan_kernel<<<1, 1024, 0, st>>>(h, (int*)(ws + p.live), (int*)(ws + p.ctl));
+        head_gather_kernel<<<(unsigned)(p.Tp / 8), 256, 0, st>>>(
+            h, (const uint4*)c.x, (uint4*)(ws + p.xc), want_dx ? (uint4*)g->dx : nullptr,
+            s.d * p.esize / 16, p.Tp);
+        xc = ws + p.xc;
+    }
+    cudaError_t e = cudaGetLastError();
+    for (int64_t i = 0; i < p.pieces && e == cudaSuccess; ++i) {
+        h.p0 = (int)(i * p.piece);
+        const int64_t left = p.Tp - h.p0;
+        h.rows = (int)(left < p.piece ? left : p.piece);
+        const uint8_t* xp = (const uint8_t*)xc + (size_t)h.p0 * s.d * p.esize;
+        e = launch_head_simt(h, bf16, xp, c.W, p.backward, st);
+        if (e != cudaSuccess) break;
+        head_loss_kernel<<<(unsigned)(h.rows / 32), 1024, 0, st>>>(h);
+        e = cudaGetLastError();
+        if (!p.backward || e != cudaSuccess) continue;
+        const dim3 grid((unsigned)h.rows, (unsigned)((p.Vp + kGradCols - 1) / kGradCols));
+        if (bf16) head_gradient_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(h);
+        else head_gradient_kernel<float><<<grid, 256, 0, st>>>(h);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && want_dx) e = launch_head_simt_dx(h, bf16, c.W, HeadOut{g->dx, 0, 0}, st);
+        if (e == cudaSuccess && want_dW) {
+            HeadOut o{p.wide ? (void*)(ws + p.dW32) : g->dW, p.wide || g->dW_dtype == MOE_F32,
+                      g->accumulate || i > 0};
+            e = launch_head_simt_dw(h, bf16, xp, o, st);
+        }
+    }
+    if (e == cudaSuccess && want_dW && p.wide) {
+        const int64_t n4 = (int64_t)s.V * s.d / 4;
+        const int64_t blocks = (n4 + 255) / 256;
+        head_round_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(
+            (const float4*)(ws + p.dW32), (uint2*)g->dW, n4);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace moe

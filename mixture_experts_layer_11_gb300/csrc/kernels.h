@@ -164,6 +164,24 @@ cudaError_t launch_grad_norm(int n, const moe_grad* g, bool clip, float max_norm
 size_t grad_workspace(int n);
 constexpr int64_t kGradMostBytes = int64_t(1) << 45;   // of a list
 
+// Losses over a vocabulary head.  idx: targets [T] (teacher null), or the teacher's
+// indices [T, entries] with its logits.
+struct HeadCall {
+    moe_head h;
+    const void* x;
+    const void* W;
+    const int64_t* idx;
+    const float* teacher;
+    float temperature;
+    float* loss;
+    float* lse;          // or null
+    const moe_head_grad* g;   // or null: losses alone
+    void* ws;
+    int32_t* status;
+};
+cudaError_t launch_head(const HeadCall& c, cudaStream_t st);
+size_t head_workspace(const moe_head& h, const moe_head_grad* g);
+
 // Diagnostics
 cudaError_t launch_bounded_wait(uint64_t limit_ns, int32_t* status, cudaStream_t st);
 cudaError_t launch_debug_gelu(int64_t n, const float* x, float* g, float* gd, int fast,

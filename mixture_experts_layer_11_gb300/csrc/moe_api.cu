@@ -694,6 +694,66 @@ moe_status moe_grad_clip(int n, const moe_grad* g, float max_norm, float* norm, 
                                         (cudaStream_t)stream));
 }
 
+}  // extern "C"
+
+namespace {
+
+moe_status check_head(const moe_head* h, const moe_head_grad* g) {
+    if (h == nullptr || h->T < 0 || h->piece < 0 || h->V < 1 || h->d < 1 || h->entries < 1 ||
+        (h->dtype != MOE_F32 && h->dtype != MOE_BF16))
+        return MOE_ERR_INVALID;
+    if (g != nullptr) {
+        if ((g->mean != 0 && g->mean != 1) || (g->accumulate != 0 && g->accumulate != 1) ||
+            (g->dW_dtype != MOE_F32 && g->dW_dtype != h->dtype))
+            return MOE_ERR_INVALID;
+        if (g->accumulate && g->dW_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+    }
+    if (h->T >= (int64_t(1) << 31) || h->piece >= (int64_t(1) << 31) || h->V > (1 << 22) ||
+        h->d % 8 || h->d > (1 << 20) || h->entries > MOE_HEAD_MAX_ENTRIES)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status run_head(const moe_head* h, const void* x, const void* W, const int64_t* idx,
+                    const float* logits, bool distill, float temperature, float* loss, float* lse,
+                    const moe_head_grad* g, void* ws, int32_t* dev_status, moe_stream_t stream) {
+    moe_status r = check_head(h, g);
+    if (r != MOE_OK) return r;
+    if (!distill && h->entries != 1) return MOE_ERR_INVALID;
+    if (!(temperature > 0.f) || temperature > 3.0e38f) return MOE_ERR_INVALID;
+    if (g && (!ok_opt(g->dW) || !ok_opt(g->dx) || ((uintptr_t)g->weight & 3u)))
+        return MOE_ERR_INVALID;
+    if (h->T > 0) {
+        if (!ok_ptr(x) || !ok_ptr(W) || idx == nullptr || ((uintptr_t)idx & 7u) ||
+            (distill && (logits == nullptr || ((uintptr_t)logits & 3u))) || loss == nullptr ||
+            ((uintptr_t)loss & 3u) || ((uintptr_t)lse & 3u) || !ok_ptr(ws) || !ok_status(dev_status))
+            return MOE_ERR_INVALID;
+    }
+    HeadCall c{*h, x, W, idx, distill ? logits : nullptr, temperature, loss, lse, g, ws, dev_status};
+    return cuda_status(launch_head(c, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_head_workspace_size(const moe_head* h, const moe_head_grad* g) {
+    return check_head(h, g) == MOE_OK ? head_workspace(*h, g) : 0;
+}
+
+moe_status moe_head_ce(const moe_head* h, const void* x, const void* W, const int64_t* target,
+                       float* loss, float* lse, const moe_head_grad* g, void* ws,
+                       int32_t* dev_status, moe_stream_t stream) {
+    return run_head(h, x, W, target, nullptr, false, 1.f, loss, lse, g, ws, dev_status, stream);
+}
+
+moe_status moe_head_distill(const moe_head* h, const void* x, const void* W, const int64_t* idx,
+                            const float* logits, float temperature, float* loss, float* lse,
+                            const moe_head_grad* g, void* ws, int32_t* dev_status,
+                            moe_stream_t stream) {
+    return run_head(h, x, W, idx, logits, true, temperature, loss, lse, g, ws, dev_status, stream);
+}
+
 moe_status moe_debug_bounded_wait(uint64_t limit_ns, int32_t* dev_status, moe_stream_t stream) {
     if (dev_status == nullptr || !ok_status(dev_status)) return MOE_ERR_INVALID;
     return cuda_status(launch_bounded_wait(limit_ns, dev_status, (cudaStream_t)stream));

@@ -29,7 +29,8 @@ ENTRY_POINTS = ("moe_status_string", "moe_workspace_size", "moe_route", "moe_per
                 "moe_expert_ffn_bwd_weights_gather", "moe_set_gemm_max_units",
                 "moe_expert_ffn_bwd_weights_workspace_size", "moe_layer_few",
                 "moe_layer_few_workspace_size", "moe_grad_norm", "moe_grad_clip",
-                "moe_grad_workspace_size")
+                "moe_grad_workspace_size", "moe_head_ce", "moe_head_distill",
+                "moe_head_workspace_size")
 
 
 class MoEError(RuntimeError):
@@ -51,6 +52,17 @@ class moe_layer_params(ctypes.Structure):
 class moe_grad(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("dtype", ctypes.c_int32)]
+
+
+class moe_head(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("piece", ctypes.c_int64), ("V", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("entries", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class moe_head_grad(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dW", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("mean", ctypes.c_int32), ("dW_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
 
 
 def make_shape(T: int, d: int, f: int, E: int, k: int, dtype, renorm: int) -> moe_shape:
@@ -121,6 +133,12 @@ def lib() -> ctypes.CDLL:
             L.moe_grad_norm.argtypes = [ctypes.c_int, ctypes.POINTER(moe_grad)] + [_P] * 4
             L.moe_grad_clip.argtypes = [ctypes.c_int, ctypes.POINTER(moe_grad),
                                         ctypes.c_float] + [_P] * 4
+            _HP, _GP = ctypes.POINTER(moe_head), ctypes.POINTER(moe_head_grad)
+            L.moe_head_workspace_size.restype = ctypes.c_size_t
+            L.moe_head_workspace_size.argtypes = [_HP, _GP]
+            L.moe_head_ce.argtypes = [_HP, _P, _P, _P, _P, _P, _GP, _P, _P, _P]
+            L.moe_head_distill.argtypes = [_HP, _P, _P, _P, _P, ctypes.c_float, _P, _P, _GP, _P,
+                                           _P, _P]
             for fn in ENTRY_POINTS[2:]:
                 if not fn.endswith("_workspace_size"):
                     getattr(L, fn).restype = ctypes.c_int
@@ -416,4 +434,49 @@ def moe_grad_clip(grads, max_norm: float, norm, ws, dev_status, stream=None):
     """grads: from make_grads."""
     _check("moe_grad_clip", lib().moe_grad_clip(
         len(grads), grads, float(max_norm), _ptr(norm, _F32), _ptr(ws), _ptr(dev_status, _I32),
+        _stream(stream)))
+
+
+HEAD_MAX_ENTRIES = 128  # MOE_HEAD_MAX_ENTRIES in include/moe.h
+
+
+def make_head(T, V, d, dtype, entries=1, piece=0) -> moe_head:
+    """dtype: torch dtype of x, W and dx (bfloat16 or float32)."""
+    return moe_head(int(T), int(piece), int(V), int(d), int(entries),
+                    MOE_BF16 if dtype == torch.bfloat16 else MOE_F32)
+
+
+def make_head_grad(dx, dW, dtype, weight=None, scale=1.0, mean=False,
+                   accumulate=False) -> moe_head_grad:
+    """The gradients moe_head_ce / moe_head_distill take (dx, dW: None where one is
+    not wanted; dW fp32 or of dtype).  It holds addresses only: keep the tensors
+    alive while it is used."""
+    one_device("make_head_grad", dx, dW, weight)
+    if dW is not None and dW.dtype not in (dtype, _F32):
+        raise MoEError("make_head_grad", MOE_ERR_INVALID, f"dW dtype {dW.dtype}")
+    wide = dW is None or dW.dtype == _F32
+    return moe_head_grad(_ptr(weight, _F32), _ptr(dx, dtype), _ptr(dW), float(scale),
+                         int(bool(mean)), MOE_F32 if wide else MOE_BF16, int(bool(accumulate)))
+
+
+def moe_head_workspace_size(h: moe_head, grad=None) -> int:
+    return int(lib().moe_head_workspace_size(
+        ctypes.byref(h), None if grad is None else ctypes.byref(grad)))
+
+
+def moe_head_ce(h, x, W, target, loss, lse, grad, ws, dev_status, stream=None):
+    """grad: from make_head_grad, or None for the losses alone."""
+    _check("moe_head_ce", lib().moe_head_ce(
+        ctypes.byref(h), _ptr(x, _act(h)), _ptr(W, _act(h)), _ptr(target, torch.int64),
+        _ptr(loss, _F32), _ptr(lse, _F32), None if grad is None else ctypes.byref(grad),
+        _ptr(ws), _ptr(dev_status, _I32), _stream(stream)))
+
+
+def moe_head_distill(h, x, W, idx, logits, temperature, loss, lse, grad, ws, dev_status,
+                     stream=None):
+    """grad: from make_head_grad, or None for the losses alone."""
+    _check("moe_head_distill", lib().moe_head_distill(
+        ctypes.byref(h), _ptr(x, _act(h)), _ptr(W, _act(h)), _ptr(idx, torch.int64),
+        _ptr(logits, _F32), float(temperature), _ptr(loss, _F32), _ptr(lse, _F32),
+        None if grad is None else ctypes.byref(grad), _ptr(ws), _ptr(dev_status, _I32),
         _stream(stream)))
