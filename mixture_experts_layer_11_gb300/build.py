@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["moe_api.cu", "route.cu", "dispatch.cu", "gemm_simt.cu", "gemm_tc.cu",
-           "few.cu", "grads.cu", "head.cu", "head_simt.cu"]
+           "few.cu", "grads.cu", "head.cu", "head_simt.cu", "head_tc.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "head.h"),
            os.path.join(ROOT, "include", "moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

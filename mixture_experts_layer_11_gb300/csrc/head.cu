@@ -24,15 +24,16 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kPieceBytes = int64_t(2) << 30;   // of E, where the caller sets no piece
-constexpr int kFewRows = 128;    // losses alone of up to this many rows: no gathering
 
 inline int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 struct Plan {
     int64_t T, piece, pieces, Tp, Vp;
-    int nblk, K, esize;
-    bool few, backward, wide;   // wide: dW is summed in an fp32 buffer of the workspace
-    size_t ctl, live, xc, sidx, q, lq, ent, start, lz, stats, lse2, P, dW32, total;
+    int nblk, nstat, K, esize;
+    // few: losses alone of up to kHeadFewRows rows, none gathered; single: as few rows in
+    // bf16; wide: dW is summed in an fp32 buffer of the workspace
+    bool few, single, backward, wide;
+    size_t ctl, live, xc, sidx, q, lq, ent, start, lz, stats, lse2, P, dW32, part, part_bytes, total;
 };
 
 Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
@@ -41,9 +42,18 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     p.esize = h.dtype == MOE_BF16 ? 2 : 4;
     p.K = h.entries;
     p.backward = g != nullptr;
-    p.few = !p.backward && h.T <= kFewRows;
+    p.few = !p.backward && h.T <= kHeadFewRows;
+    p.single = h.dtype == MOE_BF16 && h.T <= kHeadFewRows;
     p.Vp = up(h.V, 64);
     p.nblk = (h.V + kHeadBlock - 1) / kHeadBlock;
+    p.nstat = p.nblk;
+    int most_stat = p.nblk;   // a call with more tokens needs no less workspace
+    if (!p.backward && h.dtype == MOE_BF16) {
+        const int n = head_few_tile(h.V);
+        const int few = (h.V + n - 1) / n * (n > kHeadBlock ? 2 : 1);
+        if (p.few && n % kHeadBlock) p.nstat = few;
+        if (few > most_stat) most_stat = few;
+    }
     p.Tp = up(h.T > 0 ? h.T : 1, kHeadRows);
     int64_t piece = p.Tp;
     if (p.backward) {
@@ -64,7 +74,7 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     const size_t T = (size_t)(h.T > 0 ? h.T : 1), K = (size_t)p.K;
     p.ctl = take(256);
     p.lz = take(T * K * 4);
-    p.stats = take((size_t)p.nblk * piece * sizeof(float2));
+    p.stats = take((size_t)most_stat * piece * sizeof(float2));
     p.lse2 = take((size_t)piece * 4);
     if (distill) {
         p.sidx = take(T * K * 4);
@@ -79,6 +89,10 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     }
     if (p.backward) {
         p.P = take((size_t)piece * p.Vp * p.esize);
+        if (h.dtype == MOE_BF16) {
+            p.part_bytes = head_part_bytes(piece, h.V, h.d, p.single);
+            p.part = take(p.part_bytes);
+        }
         if (p.wide) p.dW32 = take((size_t)h.V * h.d * 4);
     }
     p.total = at;
@@ -237,8 +251,9 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
     if (r0 >= n) return;
     float m = -INFINITY, s = 0.f;
     if (r0 + lane < n) {
-        for (int b = w; b < h.nblk; b += 32) {
+        for (int b = w; b < h.nstat; b += 32) {
             const float2 v = h.stats[(int64_t)b * h.srows + r0 + lane];
+            if (v.y == 0.f) continue;   // no entries
             // (NaN: the comparison fails, and the sum takes it on)
             if (v.x > m) {
                 s = s * exp2f(m - v.x) + v.y;
@@ -394,6 +409,7 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
     h.K = s.entries;
     h.Vp = (int)p.Vp;
     h.nblk = p.nblk;
+    h.nstat = p.nstat;
     h.rows = (int)p.piece;
     h.srows = (int)p.piece;
     if (!p.few) {
@@ -405,7 +421,7 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         h.q = (const float*)(ws + p.q);
         h.lq = (const float*)(ws + p.lq);
         h.ent = (const int*)(ws + p.ent);
-        h.start = ws + p.start;
+        h.start = p.K > 1 ? ws + p.start : nullptr;
     } else {
         h.target = c.idx;
     }
@@ -429,6 +445,7 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
             h, c.idx, c.teacher, 1.f / c.temperature, (int*)(ws + p.sidx), (float*)(ws + p.q),
             (float*)(ws + p.lq), (int*)(ws + p.ent), ws + p.start);
     const void* xc = c.x;
+    float* part = (float*)(ws + p.part);
     if (!p.few) {
         head_scan_kernel<<<1, 1024, 0, st>>>(h, (int*)(ws + p.live), (int*)(ws + p.ctl));
         head_gather_kernel<<<(unsigned)(p.Tp / 8), 256, 0, st>>>(
@@ -442,7 +459,8 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         const int64_t left = p.Tp - h.p0;
         h.rows = (int)(left < p.piece ? left : p.piece);
         const uint8_t* xp = (const uint8_t*)xc + (size_t)h.p0 * s.d * p.esize;
-        e = launch_head_simt(h, bf16, xp, c.W, p.backward, st);
+        e = bf16 ? launch_head_tc(h, xp, c.W, p.backward, p.single, st)
+                 : launch_head_simt(h, xp, c.W, p.backward, st);
         if (e != cudaSuccess) break;
         head_loss_kernel<<<(unsigned)(h.rows / 32), 1024, 0, st>>>(h);
         e = cudaGetLastError();
@@ -451,11 +469,15 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         if (bf16) head_gradient_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(h);
         else head_gradient_kernel<float><<<grid, 256, 0, st>>>(h);
         e = cudaGetLastError();
-        if (e == cudaSuccess && want_dx) e = launch_head_simt_dx(h, bf16, c.W, HeadOut{g->dx, 0, 0}, st);
+        if (e == cudaSuccess && want_dx) {
+            const HeadOut o{g->dx, !bf16, 0};
+            e = bf16 ? launch_head_tc_dx(h, c.W, o, part, p.part_bytes, p.single, st)
+                     : launch_head_simt_dx(h, c.W, o, st);
+        }
         if (e == cudaSuccess && want_dW) {
             HeadOut o{p.wide ? (void*)(ws + p.dW32) : g->dW, p.wide || g->dW_dtype == MOE_F32,
                       g->accumulate || i > 0};
-            e = launch_head_simt_dw(h, bf16, xp, o, st);
+            e = bf16 ? launch_head_tc_dw(h, xp, o, part, p.part_bytes, st) : launch_head_simt_dw(h, xp, o, st);
         }
     }
     if (e == cudaSuccess && want_dW && p.wide) {

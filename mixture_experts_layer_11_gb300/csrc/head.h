@@ -28,6 +28,7 @@ struct HeadDev {
     int T, V, d, K;
     int Vp;                  // row length of P (V rounded up to 64)
     int nblk;                // blocks of kHeadBlock entries
+    int nstat;               // blocks the statistics are over (nblk, or of the few-row tiles)
     int p0, rows;            // first live row of the piece, its most rows
     int srows;               // row length of stats (rows, rounded up to kHeadRows)
     const int* n_live;       // null: rows are tokens, all T of them
@@ -39,7 +40,7 @@ struct HeadDev {
     const int* ent;          // entries present [T]
     const uint8_t* start;    // first entry of each block [T][nblk]
     float* lz;               // logits of the targets / entries [T][K]
-    float2* stats;           // [nblk][srows]: largest exponent - kHeadShift, sum
+    float2* stats;           // [nstat][srows]: largest exponent - kHeadShift, sum (0: no entries)
     float* lse2;             // [srows] log2 of the sum of exponentials
     void* P;                 // [rows][Vp]: exponentials, then gradients by the logits
     const float* weight;
@@ -72,14 +73,23 @@ __device__ __forceinline__ float head_scale(const HeadDev& h) {
 //   DW  dW (+)= scale * G^T xc
 struct HeadOut {
     void* out;               // dx [T,d] or dW [V,d]
-    int f32;                 // dW: fp32 (else the dtype)
+    int f32;                 // fp32 (else bf16)
     int accumulate;
 };
-cudaError_t launch_head_simt(const HeadDev& h, bool bf16, const void* xc, const void* W, bool keep,
-                             cudaStream_t st);
-cudaError_t launch_head_simt_dx(const HeadDev& h, bool bf16, const void* W, const HeadOut& o,
-                                cudaStream_t st);
-cudaError_t launch_head_simt_dw(const HeadDev& h, bool bf16, const void* xc, const HeadOut& o,
-                                cudaStream_t st);
+cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st);
+cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& o, cudaStream_t st);
+cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, cudaStream_t st);
+
+// The same on the tensor cores, bf16 (single: up to 128 rows; xc may be x itself,
+// where rows are tokens).  part: the cut tiles' sums.
+constexpr int kHeadFewRows = 128;
+int head_few_tile(int V);
+size_t head_part_bytes(int64_t rows, int V, int d, bool single);
+cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool keep, bool single,
+                           cudaStream_t st);
+cudaError_t launch_head_tc_dx(const HeadDev& h, const void* W, const HeadOut& o, float* part,
+                              size_t part_bytes, bool single, cudaStream_t st);
+cudaError_t launch_head_tc_dw(const HeadDev& h, const void* xc, const HeadOut& o, float* part,
+                              size_t part_bytes, cudaStream_t st);
 
 }  // namespace moe

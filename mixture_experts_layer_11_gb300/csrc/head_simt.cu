@@ -10,23 +10,13 @@ constexpr int LD = BM + 4;     // row of a K step in shared memory, 16-byte alig
 
 enum Mode { Z = 0, ZKEEP = 1, DX = 2, DW = 3 };
 
-template <typename T> __device__ __forceinline__ float4 load4(const T* p);
-template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
-    return *reinterpret_cast<const float4*>(p);
-}
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-
 // A 128 x 16 step of an operand, as two groups of four values a thread.  KC: the
 // reduction runs along memory (row-major [M][K]), else across it ([K][M]).  Rows
 // and columns past the edge are zero; a group of four never straddles an edge
 // but in the vocabulary (kmax or mmax not a multiple of 4), where it is masked.
-template <typename T, bool KC>
+template <bool KC>
 struct Loader {
-    const T* p;
+    const float* p;
     int64_t ld;
     int m0, mmax, kmax;
     float4 v[2];
@@ -37,7 +27,7 @@ struct Loader {
             const int m = m0 + (KC ? g >> 2 : (g & 31) * 4), k = k0 + (KC ? (g & 3) * 4 : g >> 5);
             v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (m < mmax && k < kmax) {
-                v[i] = load4<T>(p + (KC ? (int64_t)m * ld + k : (int64_t)k * ld + m));
+                v[i] = *reinterpret_cast<const float4*>(p + (KC ? (int64_t)m * ld + k : (int64_t)k * ld + m));
                 const int left = KC ? kmax - k : mmax - m;
                 if (left < 2) v[i].y = 0.f;
                 if (left < 3) v[i].z = 0.f;
@@ -73,13 +63,9 @@ __device__ __forceinline__ float half_sum(float v) {
     return v;
 }
 
-template <typename T> struct PType { using type = float; };
-template <> struct PType<__nv_bfloat16> { using type = __half; };
-
-// T: type of x, W and G.
-template <typename T, int MODE>
+template <int MODE>
 __global__ void __launch_bounds__(THREADS)
-    head_simt_kernel(const HeadDev h, const T* A, const T* B, const HeadOut o) {
+    head_simt_kernel(const HeadDev h, const float* A, const float* B, const HeadOut o) {
     constexpr bool A_KC = MODE != DW, B_KC = MODE <= ZKEEP;
     __shared__ __align__(16) float As[2][BK][LD], Bs[2][BK][LD];
     const int n = head_rows(h);
@@ -89,8 +75,8 @@ __global__ void __launch_bounds__(THREADS)
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
     if (m0 >= M) return;
-    Loader<T, A_KC> la{A, MODE <= ZKEEP ? h.d : h.Vp, m0, M, K};
-    Loader<T, B_KC> lb{B, h.d, n0, N, K};
+    Loader<A_KC> la{A, MODE <= ZKEEP ? h.d : h.Vp, m0, M, K};
+    Loader<B_KC> lb{B, h.d, n0, N, K};
 
     uint64_t acc[8][4];   // [row][pair of columns]
 #pragma unroll
@@ -160,12 +146,11 @@ __global__ void __launch_bounds__(THREADS)
             if (r >= n) continue;
             if (tx == 0) h.stats[(int64_t)blockIdx.y * h.srows + r] = make_float2(m, sum);
             if (MODE == ZKEEP) {
-                using P = typename PType<T>::type;
-                P* out = (P*)h.P + (int64_t)r * h.Vp;
+                float* out = (float*)h.P + (int64_t)r * h.Vp;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int col = n0 + (j >> 2) * 64 + tx * 4 + (j & 3);
-                    if (col < h.Vp) out[col] = (P)e[j];
+                    if (col < h.Vp) out[col] = e[j];
                 }
             }
             const int t = head_token(h, r);
@@ -190,48 +175,35 @@ __global__ void __launch_bounds__(THREADS)
                 const int col = n0 + (j >> 2) * 64 + tx * 4 + (j & 3);
                 if (col >= N) continue;
                 const int64_t at = row * N + col;
-                if (MODE == DW && o.f32) {
-                    float* out = (float*)o.out;
-                    out[at] = o.accumulate ? fmaf(scale, v[j], out[at]) : scale * v[j];
-                } else {
-                    ((T*)o.out)[at] = from_f32<T>(scale * v[j]);
-                }
+                float* out = (float*)o.out;
+                out[at] = o.accumulate ? fmaf(scale, v[j], out[at]) : scale * v[j];
             }
         }
     }
 }
 
-template <typename T, int MODE>
+template <int MODE>
 cudaError_t launch(const HeadDev& h, const void* A, const void* B, const HeadOut& o, int64_t M, int64_t N,
                    cudaStream_t st) {
     const dim3 grid((unsigned)((M + BM - 1) / BM), (unsigned)((N + BN - 1) / BN));
     if (grid.x == 0 || grid.y == 0) return cudaSuccess;
-    head_simt_kernel<T, MODE><<<grid, THREADS, 0, st>>>(h, (const T*)A, (const T*)B, o);
+    head_simt_kernel<MODE><<<grid, THREADS, 0, st>>>(h, (const float*)A, (const float*)B, o);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_head_simt(const HeadDev& h, bool bf16, const void* xc, const void* W, bool keep,
-                             cudaStream_t st) {
+cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st) {
     const HeadOut o{};
-    if (bf16)
-        return keep ? launch<__nv_bfloat16, ZKEEP>(h, xc, W, o, h.rows, h.V, st)
-                    : launch<__nv_bfloat16, Z>(h, xc, W, o, h.rows, h.V, st);
-    return keep ? launch<float, ZKEEP>(h, xc, W, o, h.rows, h.V, st)
-                : launch<float, Z>(h, xc, W, o, h.rows, h.V, st);
+    return keep ? launch<ZKEEP>(h, xc, W, o, h.rows, h.V, st) : launch<Z>(h, xc, W, o, h.rows, h.V, st);
 }
 
-cudaError_t launch_head_simt_dx(const HeadDev& h, bool bf16, const void* W, const HeadOut& o,
-                                cudaStream_t st) {
-    return bf16 ? launch<__nv_bfloat16, DX>(h, h.P, W, o, h.rows, h.d, st)
-                : launch<float, DX>(h, h.P, W, o, h.rows, h.d, st);
+cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& o, cudaStream_t st) {
+    return launch<DX>(h, h.P, W, o, h.rows, h.d, st);
 }
 
-cudaError_t launch_head_simt_dw(const HeadDev& h, bool bf16, const void* xc, const HeadOut& o,
-                                cudaStream_t st) {
-    return bf16 ? launch<__nv_bfloat16, DW>(h, h.P, xc, o, h.V, h.d, st)
-                : launch<float, DW>(h, h.P, xc, o, h.V, h.d, st);
+cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, cudaStream_t st) {
+    return launch<DW>(h, h.P, xc, o, h.V, h.d, st);
 }
 
 }  // namespace moe
