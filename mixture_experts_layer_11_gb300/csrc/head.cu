@@ -33,7 +33,7 @@ struct Plan {
     // few: losses alone of up to kHeadFewRows rows, none gathered; single: as few rows in
     // bf16; wide: dW is summed in an fp32 buffer of the workspace
     bool few, single, backward, wide;
-    size_t ctl, live, xc, sidx, q, lq, ent, start, lz, stats, lse2, P, dW32, part, part_bytes, total;
+    size_t ctl, live, pos, xc, sidx, q, lq, ent, start, lz, stats, lse2, P, dW32, part, part_bytes, total;
 };
 
 Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
@@ -49,9 +49,8 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     p.nstat = p.nblk;
     int most_stat = p.nblk;   // a call with more tokens needs no less workspace
     if (!p.backward && h.dtype == MOE_BF16) {
-        const int n = head_few_tile(h.V);
-        const int few = (h.V + n - 1) / n * (n > kHeadBlock ? 2 : 1);
-        if (p.few && n % kHeadBlock) p.nstat = few;
+        const int few = head_few_stats(h.V);
+        if (p.few) p.nstat = few;
         if (few > most_stat) most_stat = few;
     }
     p.Tp = up(h.T > 0 ? h.T : 1, kHeadRows);
@@ -85,14 +84,14 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     }
     if (!p.few) {
         p.live = take((size_t)p.Tp * 4);
+        p.pos = take((size_t)p.Tp * 4);
         p.xc = take((size_t)p.Tp * h.d * p.esize);
     }
     if (p.backward) {
         p.P = take((size_t)piece * p.Vp * p.esize);
-        if (h.dtype == MOE_BF16) {
-            p.part_bytes = head_part_bytes(piece, h.V, h.d, p.single);
-            p.part = take(p.part_bytes);
-        }
+        p.part_bytes = h.dtype == MOE_BF16 ? head_part_bytes(piece, h.V, h.d, p.single)
+                                           : head_simt_part_bytes(piece, h.V, h.d);
+        p.part = take(p.part_bytes);
         if (p.wide) p.dW32 = take((size_t)h.V * h.d * 4);
     }
     p.total = at;
@@ -112,6 +111,7 @@ __global__ void __launch_bounds__(128)
     constexpr int N = MOE_HEAD_MAX_ENTRIES / 32;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * 4 + w;
+    wait_front();
     if (t >= h.T) return;
     const int64_t at = (int64_t)t * h.K;
     float v[N], top = -INFINITY;
@@ -192,74 +192,123 @@ __device__ __forceinline__ bool token_live(const HeadDev& h, int t) {
     return y >= 0 && y < h.V;
 }
 
-// One block: the live tokens in order, and their count.
-__global__ void __launch_bounds__(1024) head_scan_kernel(const HeadDev h, int* live, int* n_live) {
-    __shared__ int part[32];
+// The live tokens' rows.  Up to kScanTokens tokens each block of head_gather_kernel
+// counts them all for itself (64 KB of targets from L2 for 8192 tokens: 2 us, against
+// a launch of one block that takes 5 us and its gap); more are counted once, by this
+// block.
+constexpr int kScanTokens = 16384;
+
+__global__ void __launch_bounds__(1024) head_scan_kernel(const HeadDev h, int* pos, int* n_live) {
+    __shared__ int part[2][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int base = 0;
-    for (int t0 = 0; t0 < h.T; t0 += 1024) {
+    wait_front();
+    for (int t0 = 0, it = 0; t0 < h.T; t0 += 1024, ++it) {
         const int t = t0 + threadIdx.x;
         const bool on = t < h.T && token_live(h, t);
-        if (h.target && t < h.T && h.target[t] >= h.V) report(h.status, MOE_ERR_INVALID);
         const unsigned mask = __ballot_sync(0xffffffffu, on);
-        if (lane == 0) part[w] = __popc(mask);
+        if (lane == 0) part[it & 1][w] = __popc(mask);
         __syncthreads();
-        int before = 0, all = 0;
-        for (int i = 0; i < 32; ++i) {
-            before += i < w ? part[i] : 0;
-            all += part[i];
-        }
-        if (on) live[base + before + __popc(mask & ((1u << lane) - 1))] = t;
-        base += all;
-        __syncthreads();
+        const int v = part[it & 1][lane];
+        const int before = __reduce_add_sync(0xffffffffu, lane < w ? v : 0);
+        if (t < h.T) pos[t] = on ? base + before + __popc(mask & ((1u << lane) - 1)) : -1;
+        base += __reduce_add_sync(0xffffffffu, v);
     }
     if (threadIdx.x == 0) *n_live = base;
 }
 
-// Warp i: row i of the gathered x (zeros behind the live rows, up to a whole tile),
-// and, if token i is ignored, its outputs.
-__global__ void __launch_bounds__(256)
-    head_gather_kernel(const HeadDev h, const uint4* x, uint4* xc, uint4* dx, int vecs, int64_t Tp) {
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (i >= Tp) return;
-    const int n = *h.n_live;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    if (i < n) {
-        const uint4* src = x + (int64_t)h.live[i] * vecs;
-        for (int v = lane; v < vecs; v += 32) xc[i * vecs + v] = src[v];
-    } else if (i < (int64_t)(n + kHeadRows - 1) / kHeadRows * kHeadRows) {
-        for (int v = lane; v < vecs; v += 32) xc[i * vecs + v] = zero;
-    }
-    if (i < h.T && !token_live(h, (int)i)) {
+// A warp a token: a live one's x goes to its row of xc, an ignored one's outputs are
+// zeros; and row i of xc behind the live ones, up to the end of a K block of 64 (of
+// the tensor cores' products, where it meets zeros of G), is zeros.
+template <bool COUNT>
+__global__ void __launch_bounds__(1024)
+    head_gather_kernel(const HeadDev h, const uint4* x, uint4* xc, uint4* dx, int vecs, int* live, const int* pos,
+                       int* n_live) {
+    __shared__ int part[2][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = blockIdx.x * 32, t = first + w;
+    wait_front();
+    const bool on = t < h.T && token_live(h, t);
+    int row = -1, n;
+    if (COUNT) {
+        int before = 0, all = 0;
+        for (int i = threadIdx.x; i < h.T; i += 1024) {
+            const int v = token_live(h, i);
+            all += v;
+            before += i < first ? v : 0;
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        before = __reduce_add_sync(0xffffffffu, before);
         if (lane == 0) {
-            h.loss[i] = 0.f;
-            if (h.lse) h.lse[i] = 0.f;
+            part[0][w] = all;
+            part[1][w] = before;
+        }
+        __syncthreads();
+        n = __reduce_add_sync(0xffffffffu, part[0][lane]);
+        before = __reduce_add_sync(0xffffffffu, part[1][lane]);
+        const int i = first + lane;
+        const unsigned mask = __ballot_sync(0xffffffffu, i < h.T && token_live(h, i));
+        if (on) row = before + __popc(mask & ((1u << w) - 1));
+        if (blockIdx.x == 0 && threadIdx.x == 0) *n_live = n;
+    } else {
+        n = *n_live;
+        if (on) row = pos[t];
+    }
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (on) {
+        const uint4* src = x + (int64_t)t * vecs;
+        uint4* dst = xc + (int64_t)row * vecs;
+        int v = lane;
+        for (; v + 96 < vecs; v += 128) {
+            const uint4 a = src[v], b = src[v + 32], c = src[v + 64], d = src[v + 96];
+            dst[v] = a;
+            dst[v + 32] = b;
+            dst[v + 64] = c;
+            dst[v + 96] = d;
+        }
+        for (; v < vecs; v += 32) dst[v] = src[v];
+        if (lane == 0) live[row] = t;
+    } else if (t < h.T) {
+        if (lane == 0) {
+            if (h.target && h.target[t] >= h.V) report(h.status, MOE_ERR_INVALID);
+            h.loss[t] = 0.f;
+            if (h.lse) h.lse[t] = 0.f;
         }
         if (dx)
-            for (int v = lane; v < vecs; v += 32) dx[i * vecs + v] = zero;
+            for (int v = lane; v < vecs; v += 32) dx[(int64_t)t * vecs + v] = zero;
     }
+    if (t >= n && t < (n + 63) / 64 * 64)
+        for (int v = lane; v < vecs; v += 32) xc[(int64_t)t * vecs + v] = zero;
 }
 
 // ---- statistics to losses ----------------------------------------------------------
 //
 // A block takes 32 rows; lane = row, a warp every 32nd vocabulary block.
+constexpr int kLossLoads = 8;   // in flight a thread
 __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
     __shared__ float ms[32][33], ss[32][33];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    wait_front();
     const int n = head_rows(h), r0 = blockIdx.x * 32;
     if (r0 >= n) return;
     float m = -INFINITY, s = 0.f;
     if (r0 + lane < n) {
-        for (int b = w; b < h.nstat; b += 32) {
-            const float2 v = h.stats[(int64_t)b * h.srows + r0 + lane];
-            if (v.y == 0.f) continue;   // no entries
-            // (NaN: the comparison fails, and the sum takes it on)
-            if (v.x > m) {
-                s = s * exp2f(m - v.x) + v.y;
-                m = v.x;
-            } else {
-                s += v.y * exp2f(v.x - m);
+        const float2* src = h.stats + r0 + lane;
+        for (int b = w; b < h.nstat; b += 32 * kLossLoads) {
+            float2 v[kLossLoads];
+#pragma unroll
+            for (int i = 0; i < kLossLoads; ++i)
+                v[i] = b + 32 * i < h.nstat ? src[(int64_t)(b + 32 * i) * h.srows] : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kLossLoads; ++i) {
+                if (v[i].y == 0.f) continue;   // no entries
+                // (NaN: the comparison fails, and the sum takes it on)
+                if (v[i].x > m) {
+                    s = s * exp2f(m - v[i].x) + v[i].y;
+                    m = v[i].x;
+                } else {
+                    s += v[i].y * exp2f(v[i].x - m);
+                }
             }
         }
     }
@@ -335,28 +384,43 @@ template <> struct Pair<float> {
     }
 };
 
-constexpr int kGradCols = 4096;   // columns of a row a block turns
+constexpr int kGradLoads = 4;     // of 16 bytes a thread, in flight at once
 
 template <typename T>
 __global__ void __launch_bounds__(256) head_gradient_kernel(const HeadDev h) {
-    const int r = blockIdx.x, c0 = blockIdx.y * kGradCols;
+    constexpr int N = Pair<T>::N, COLS = 256 * N * kGradLoads;   // columns of a row a block turns
+    wait_front();
     const int n = head_rows(h);
-    if (r >= (n + 63) / 64 * 64) return;
-    constexpr int N = Pair<T>::N;
+    // the last rows first: L2 still holds some of them
+    const int r = (n + 63) / 64 * 64 - 1 - (int)blockIdx.x, c0 = blockIdx.y * COLS;
+    if (r < 0) return;
     T* row = (T*)h.P + (int64_t)r * h.Vp;
-    const int c1 = c0 + kGradCols < h.Vp ? c0 + kGradCols : h.Vp;
+    const int c1 = c0 + COLS < h.Vp ? c0 + COLS : h.Vp;
+    const int first = c0 + threadIdx.x * N;
+    uint4 v[kGradLoads];
     if (r >= n) {   // the last K block's rows behind the live ones
-        for (int c = c0 + threadIdx.x * N; c < c1; c += 256 * N)
-            *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kGradLoads; ++i)
+            if (first + i * 256 * N < c1)
+                *reinterpret_cast<uint4*>(row + first + i * 256 * N) = make_uint4(0, 0, 0, 0);
         return;
+    }
+    float m[kGradLoads];
+#pragma unroll
+    for (int i = 0; i < kGradLoads; ++i) {
+        const int c = first + i * 256 * N;
+        if (c < c1) {
+            v[i] = *reinterpret_cast<const uint4*>(row + c);
+            m[i] = h.stats[(int64_t)(c / kHeadBlock) * h.srows + r].x;
+        }
     }
     const int t = head_token(h, r);
     const float lse2 = h.lse2[r];
     const float weight = h.weight ? h.weight[t] : 1.f;
-    for (int c = c0 + threadIdx.x * N; c < c1; c += 256 * N) {
-        const float m = h.stats[(int64_t)(c / kHeadBlock) * h.srows + r].x;
-        uint4* p = reinterpret_cast<uint4*>(row + c);
-        *p = Pair<T>::scale(*p, weight * exp2f(m - lse2), h.V - c);
+#pragma unroll
+    for (int i = 0; i < kGradLoads; ++i) {
+        const int c = first + i * 256 * N;
+        if (c < c1) *reinterpret_cast<uint4*>(row + c) = Pair<T>::scale(v[i], weight * exp2f(m[i] - lse2), h.V - c);
     }
     __syncthreads();
     // the targets' entries, from their own logits
@@ -376,6 +440,7 @@ __global__ void __launch_bounds__(256) head_gradient_kernel(const HeadDev h) {
 }
 
 __global__ void __launch_bounds__(256) head_round_kernel(const float4* in, uint2* out, int64_t n4) {
+    wait_front();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
         const float4 v = in[i];
         __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
@@ -440,20 +505,25 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
     h.lse = c.lse;
     h.status = c.status;
 
+    cudaError_t e = cudaSuccess;
     if (distill)
-        head_entries_kernel<<<(unsigned)((s.T + 3) / 4), 128, 0, st>>>(
-            h, c.idx, c.teacher, 1.f / c.temperature, (int*)(ws + p.sidx), (float*)(ws + p.q),
-            (float*)(ws + p.lq), (int*)(ws + p.ent), ws + p.start);
+        e = launch_early(head_entries_kernel, dim3((unsigned)((s.T + 3) / 4)), 128, 0, 1, st, h, c.idx, c.teacher,
+                         1.f / c.temperature, (int*)(ws + p.sidx), (float*)(ws + p.q), (float*)(ws + p.lq),
+                         (int*)(ws + p.ent), ws + p.start);
     const void* xc = c.x;
     float* part = (float*)(ws + p.part);
     if (!p.few) {
-        head_scan_kernel<<<1, 1024, 0, st>>>(h, (int*)(ws + p.live), (int*)(ws + p.ctl));
-        head_gather_kernel<<<(unsigned)(p.Tp / 8), 256, 0, st>>>(
-            h, (const uint4*)c.x, (uint4*)(ws + p.xc), want_dx ? (uint4*)g->dx : nullptr,
-            s.d * p.esize / 16, p.Tp);
+        int *live = (int*)(ws + p.live), *pos = (int*)(ws + p.pos), *n_live = (int*)(ws + p.ctl);
+        const bool count = s.T <= kScanTokens;
+        if (e == cudaSuccess && !count)
+            e = launch_early(head_scan_kernel, dim3(1), 1024, 0, 1, st, h, pos, n_live);
+        if (e == cudaSuccess)
+            e = launch_early(count ? head_gather_kernel<true> : head_gather_kernel<false>, dim3((unsigned)(p.Tp / 32)),
+                             1024, 0, 1, st, h, (const uint4*)c.x, (uint4*)(ws + p.xc),
+                             want_dx ? (uint4*)g->dx : (uint4*)nullptr, s.d * p.esize / 16, live, (const int*)pos,
+                             n_live);
         xc = ws + p.xc;
     }
-    cudaError_t e = cudaGetLastError();
     for (int64_t i = 0; i < p.pieces && e == cudaSuccess; ++i) {
         h.p0 = (int)(i * p.piece);
         const int64_t left = p.Tp - h.p0;
@@ -462,30 +532,30 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         e = bf16 ? launch_head_tc(h, xp, c.W, p.backward, p.single, st)
                  : launch_head_simt(h, xp, c.W, p.backward, st);
         if (e != cudaSuccess) break;
-        head_loss_kernel<<<(unsigned)(h.rows / 32), 1024, 0, st>>>(h);
-        e = cudaGetLastError();
+        // rows that there may be: no more than tokens
+        const int64_t rows = s.T - h.p0 < h.rows ? s.T - h.p0 : h.rows;
+        e = launch_early(head_loss_kernel, dim3((unsigned)((rows + 31) / 32)), 1024, 0, 1, st, h);
         if (!p.backward || e != cudaSuccess) continue;
-        const dim3 grid((unsigned)h.rows, (unsigned)((p.Vp + kGradCols - 1) / kGradCols));
-        if (bf16) head_gradient_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(h);
-        else head_gradient_kernel<float><<<grid, 256, 0, st>>>(h);
-        e = cudaGetLastError();
+        const int cols = 256 * (16 / p.esize) * kGradLoads;
+        e = launch_early(bf16 ? head_gradient_kernel<__nv_bfloat16> : head_gradient_kernel<float>,
+                         dim3((unsigned)up(rows, 64), (unsigned)((p.Vp + cols - 1) / cols)), 256, 0, 1, st, h);
         if (e == cudaSuccess && want_dx) {
             const HeadOut o{g->dx, !bf16, 0};
             e = bf16 ? launch_head_tc_dx(h, c.W, o, part, p.part_bytes, p.single, st)
-                     : launch_head_simt_dx(h, c.W, o, st);
+                     : launch_head_simt_dx(h, c.W, o, part, p.part_bytes, st);
         }
         if (e == cudaSuccess && want_dW) {
             HeadOut o{p.wide ? (void*)(ws + p.dW32) : g->dW, p.wide || g->dW_dtype == MOE_F32,
                       g->accumulate || i > 0};
-            e = bf16 ? launch_head_tc_dw(h, xp, o, part, p.part_bytes, st) : launch_head_simt_dw(h, xp, o, st);
+            e = bf16 ? launch_head_tc_dw(h, xp, o, part, p.part_bytes, st)
+                     : launch_head_simt_dw(h, xp, o, part, p.part_bytes, st);
         }
     }
     if (e == cudaSuccess && want_dW && p.wide) {
         const int64_t n4 = (int64_t)s.V * s.d / 4;
         const int64_t blocks = (n4 + 255) / 256;
-        head_round_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(
-            (const float4*)(ws + p.dW32), (uint2*)g->dW, n4);
-        e = cudaGetLastError();
+        e = launch_early(head_round_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, 1, st,
+                         (const float4*)(ws + p.dW32), (uint2*)g->dW, n4);
     }
     return e;
 }

@@ -28,7 +28,7 @@ struct HeadDev {
     int T, V, d, K;
     int Vp;                  // row length of P (V rounded up to 64)
     int nblk;                // blocks of kHeadBlock entries
-    int nstat;               // blocks the statistics are over (nblk, or of the few-row tiles)
+    int nstat;               // rows of stats: nblk, or two a CTA where a call has few rows
     int p0, rows;            // first live row of the piece, its most rows
     int srows;               // row length of stats (rows, rounded up to kHeadRows)
     const int* n_live;       // null: rows are tokens, all T of them
@@ -67,23 +67,127 @@ __device__ __forceinline__ float head_scale(const HeadDev& h) {
     return h.grad_scale / (float)(n > 0 ? n : 1);
 }
 
+// How the tiles of a reduction over kb blocks of 64 run on `units` CTAs (or pairs, or
+// blocks at once): tiles before `full` whole, the uneven last wave behind them (or
+// all, where there are few) in `parts` parts of kbp blocks, whose sums a second
+// launch joins in order.  Costs, in a block's time: a part's blocks and `each` more
+// (its start and end), and for cutting `once`, the joining launch, with a block for
+// `bytes` parts written and read.  Parts have at least `least` blocks.  The same
+// everywhere; called by whole warps.
+struct Split { int tiles, full, parts, kbp; };
+constexpr int kMostParts = 64;
+__device__ __forceinline__ Split split_tiles(int tiles, int kb, int units, int cap, int least, int each,
+                                             int once, int bytes) {
+    Split s{tiles, tiles, 1, kb};
+    const int rem = tiles % units, lane = threadIdx.x & 31;
+    if (rem == 0 || kb < 2 * least) return s;
+    unsigned best = 0xffffffffu;
+    for (int P = lane + 1; P <= kMostParts; P += 32) {
+        if (P > 1 && (P * least > kb || rem * P > cap)) continue;
+        const int kbp = (kb + P - 1) / P, parts = (kb + kbp - 1) / kbp;
+        unsigned cost = (unsigned)((rem * parts + units - 1) / units * (kbp + each));
+        if (parts > 1) cost += (unsigned)(once + rem * parts / bytes);
+        const unsigned key = (cost < (1u << 24) ? cost : (1u << 24) - 1) << 8 | (unsigned)P;
+        best = key < best ? key : best;
+    }
+    best = __reduce_min_sync(0xffffffffu, best);
+    const int P = (int)(best & 255u);
+    if (P > 1) {
+        s.full = tiles - rem;
+        s.kbp = (kb + P - 1) / P;
+        s.parts = (kb + s.kbp - 1) / s.kbp;
+    }
+    return s;
+}
+// The most parts that the workspace holds: four waves, and no more than split_tiles
+// can ask for.  No less for more tiles or blocks.
+inline size_t split_bound(int64_t tiles, int64_t kb, int units, int least) {
+    if (kb < 2 * least) return 0;
+    const int64_t rem = tiles < units ? tiles : units, most = kb / least < kMostParts ? kb / least : kMostParts;
+    return (size_t)(rem * most < 4 * (int64_t)units ? rem * most : 4 * (int64_t)units);
+}
+
+// The sum of `parts` rows of N values, `stride` values apart, by a block of 256
+// threads: in 1024 / N groups of threads, each every so manieth row, then the groups in
+// order.  Returns the first column of the calling thread's four sums, or -1 in the
+// threads that have none.
+constexpr int kJoinRows = 4;   // rows a block joins
+template <int N>
+__device__ __forceinline__ int join_row(const float* src, int64_t stride, int parts, float4* buf, float4& s) {
+    constexpr int Q = N / 4, G = 256 / Q;
+    const int q = threadIdx.x % Q, g = threadIdx.x / Q;
+    s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = g; k < parts; k += G) {
+        const float4 v = *reinterpret_cast<const float4*>(src + k * stride + q * 4);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    __syncthreads();   // buf is free again
+    buf[threadIdx.x] = s;
+    __syncthreads();
+    if (g) return -1;
+#pragma unroll
+    for (int i = 1; i < G; ++i) {
+        const float4 v = buf[i * Q + q];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    return q * 4;
+}
+
+// Kernels here begin while the one in front of them ends: nothing is touched before
+// wait_front(), and nothing is read through the non-coherent path.
+__device__ __forceinline__ void wait_front() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... A, typename... B>
+cudaError_t launch_early(void (*kern)(A...), dim3 grid, int block, size_t smem, int cluster, cudaStream_t st,
+                         const B&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // The three products of a call:
 //   Z   exponentials and statistics of xc W^T (KEEP: P is written too)
 //   DX  dx = scale * G W
 //   DW  dW (+)= scale * G^T xc
+// part: room for the sums of cut tiles.
 struct HeadOut {
     void* out;               // dx [T,d] or dW [V,d]
     int f32;                 // fp32 (else bf16)
     int accumulate;
 };
 cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st);
-cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& o, cudaStream_t st);
-cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, cudaStream_t st);
+cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& o, float* part, size_t part_bytes,
+                                cudaStream_t st);
+cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, float* part, size_t part_bytes,
+                                cudaStream_t st);
+size_t head_simt_part_bytes(int64_t rows, int V, int d);
 
 // The same on the tensor cores, bf16 (single: up to 128 rows; xc may be x itself,
-// where rows are tokens).  part: the cut tiles' sums.
+// where rows are tokens).
 constexpr int kHeadFewRows = 128;
 int head_few_tile(int V);
+int head_few_stats(int V);   // rows of statistics of a few-row call
 size_t head_part_bytes(int64_t rows, int V, int d, bool single);
 cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool keep, bool single,
                            cudaStream_t st);

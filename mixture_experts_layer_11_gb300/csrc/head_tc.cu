@@ -69,6 +69,7 @@ struct TcParams {
     HeadDev h;
     int tile_n;              // columns of a tile (Z, single CTAs: any multiple of 16; else 256)
     int a_rows;              // rows of A's box
+    int few;                 // losses alone of up to 128 rows: running statistics a CTA
     HeadOut o;
     float* part;             // [cap][TILE_M][BN] sums of cut tiles
     int cap;
@@ -76,35 +77,6 @@ struct TcParams {
     uint64_t limit_ns;
     int withhold_unit, withhold_kb;   // test hook: see launch_tc
 };
-
-// How the tiles of a reduction over kb blocks of 64 run on `units`: tiles before
-// `full` whole, those behind it in `parts` parts of kbp blocks.  A part costs its
-// blocks and about 4 more (its epilogue's end and the next part's start), cutting
-// about 12 for the launch that joins and an eighth of a block a part for its bytes
-// (256 KB written and read).  Called by whole warps; the same everywhere.
-struct Split { int tiles, full, parts, kbp; };
-__device__ __forceinline__ Split split_tiles(int tiles, int kb, int units, int cap) {
-    Split s{tiles, tiles, 1, kb};
-    const int rem = tiles % units, lane = threadIdx.x & 31;
-    if (rem == 0 || kb < 8) return s;
-    unsigned best = 0xffffffffu;
-    for (int P = lane + 1; P <= 64; P += 32) {
-        if (P > 1 && (P * 4 > kb || rem * P > cap)) continue;
-        const int kbp = (kb + P - 1) / P, parts = (kb + kbp - 1) / kbp;
-        unsigned cost = (unsigned)((rem * parts + units - 1) / units * (kbp + 4));
-        if (parts > 1) cost += 12 + (unsigned)(rem * parts) / 8;
-        const unsigned key = (cost < (1u << 24) ? cost : (1u << 24) - 1) << 8 | (unsigned)P;
-        best = key < best ? key : best;
-    }
-    best = __reduce_min_sync(0xffffffffu, best);
-    const int P = (int)(best & 255u);
-    if (P > 1) {
-        s.full = tiles - rem;
-        s.kbp = (kb + P - 1) / P;
-        s.parts = (kb + s.kbp - 1) / s.kbp;
-    }
-    return s;
-}
 
 // Tiles and K blocks of a mode's product.
 template <int MODE, bool PAIR>
@@ -118,7 +90,7 @@ __device__ __forceinline__ Split plan_tiles(const TcParams& p, int& kb) {
     if (MODE <= ZKEEP) return Split{MT * NT, MT * NT, 1, kb};
     // nothing to add: no tiles; without accumulation dW's zeros are written
     if (MODE == DW && n == 0) return Split{p.o.accumulate ? 0 : MT * NT, MT * NT, 1, 0};
-    return split_tiles(MT * NT, kb, p.units, p.cap);
+    return split_tiles(MT * NT, kb, p.units, p.cap, 4, 4, 12, PAIR ? 8 : 16);
 }
 
 struct Tile { int mt, nt, kb0, nkb, slot; };   // slot: of a part, else -1
@@ -154,10 +126,6 @@ __device__ __forceinline__ Tile get_tile(const C& c, const TcParams& p, int u) {
         t.nt = l / gm;
     }
     return t;
-}
-// statistics' block of a warp's columns where tiles are no whole blocks
-__device__ __forceinline__ int few_block(const TcParams& p, const Tile& t, int half) {
-    return t.nt * (p.tile_n > 128 ? 2 : 1) + half;
 }
 template <int MODE, typename C>
 __device__ __forceinline__ int unit_count(const C& c) {
@@ -304,6 +272,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_barrier_init();
     }
     if (warp == 1) tm_alloc<PAIR>(smem_u32(&c.tmem_base));
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&mapA);
+        tma_prefetch_map(&mapB);
+    }
+    wait_front();
     if (warp == 2) {
         int kb;
         const Split s = plan_tiles<MODE, PAIR>(p, kb);
@@ -324,8 +297,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_map(&mapA);
-            tma_prefetch_map(&mapB);
             int stage = 0, issued[STAGES];
             uint32_t phase = 0;
             bool ok = true;
@@ -430,6 +401,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint8_t* box = boxes + ew * BOX;
         const int n = head_rows(h);
         const float scale = MODE >= DX ? head_scale(h) : 1.f;
+        // a few-row call's tiles all have the same rows: their statistics run on
+        float few_m = -INFINITY, few_s = 0.f;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int u = unit0; u < units; u += nunits) {
@@ -485,8 +458,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int width = min(p.tile_n - half * 128, 128);
                 const int left = min(width, h.V - col0);   // the warp's columns (maybe none)
                 if (left <= 0) {
-                    if ((p.tile_n & 127) && half * 128 < p.tile_n && r < n)
-                        h.stats[(int64_t)few_block(p, t, half) * h.srows + r] = make_float2(-INFINITY, 0.f);
                     release();
                     continue;
                 }
@@ -540,11 +511,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                         v[ch][j] = a;
                         v[ch][j + 1] = b;
                     }
-                if (r < n) {
-                    float a, b;
-                    f2_unpack(f2_add(sum[0], sum[1]), a, b);
-                    const int blk = p.tile_n & 127 ? few_block(p, t, half) : col0 / kHeadBlock;
-                    h.stats[(int64_t)blk * h.srows + r] = make_float2(m, a + b);
+                float sa, sb;
+                f2_unpack(f2_add(sum[0], sum[1]), sa, sb);
+                sa += sb;
+                if (p.few) {
+                    // (NaN: the comparison fails, and the sum takes it on)
+                    if (m > few_m) {
+                        few_s = few_s == 0.f ? sa : few_s * ex2_approx(few_m - m) + sa;
+                        few_m = m;
+                    } else {
+                        few_s += sa * ex2_approx(m - few_m);
+                    }
+                } else if (r < n) {
+                    h.stats[(int64_t)(col0 / kHeadBlock) * h.srows + r] = make_float2(m, sa);
                 }
                 if (MODE == ZKEEP) {
 #pragma unroll
@@ -647,6 +626,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 release();
             }
         }
+        if (MODE == Z && p.few && q * 32 + lane < n)
+            h.stats[(int64_t)(blockIdx.x * 2 + half) * h.srows + q * 32 + lane] = make_float2(few_m, few_s);
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
@@ -660,12 +641,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-// The parts of cut tiles, added in order: a block takes eight rows of a tile, 64
-// threads a row.
+// The parts of cut tiles, added in order.
 template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ TcParams p) {
     constexpr int TM = Shape<PAIR>::TILE_M;
     __shared__ Split ss;
+    __shared__ float4 buf[256];
+    wait_front();
     if (threadIdx.x < 32) {
         int kb;
         const Split s = plan_tiles<MODE, PAIR>(p, kb);
@@ -678,23 +660,14 @@ __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ 
     struct { int tiles, full_tiles, parts, kbp, kb; } c{ss.tiles, ss.full, ss.parts, ss.kbp, 1};
     const Tile t = get_tile<MODE, PAIR>(c, p, ss.full + i);
     const int M = MODE == DW ? h.V : head_rows(h);
-    const int col = t.nt * BN + (threadIdx.x & 63) * 4;
-    if (col >= h.d) return;
     const float scale = head_scale(h);
-    for (int rr = blockIdx.y * 8 + (threadIdx.x >> 6); rr < blockIdx.y * 8 + 8; rr += 4) {
+    for (int rr = blockIdx.y * kJoinRows; rr < (int)(blockIdx.y + 1) * kJoinRows; ++rr) {
         const int r = t.mt * TM + rr;
         if (r >= M) return;
-        const float4* src = reinterpret_cast<const float4*>(p.part + ((int64_t)i * ss.parts * TM + rr) * BN) +
-                            (threadIdx.x & 63);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < ss.parts; ++k) {
-            const float4 v = src[(int64_t)k * TM * BN / 4];
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
+        float4 s;
+        const int cl = join_row<BN>(p.part + ((int64_t)i * ss.parts * TM + rr) * BN, (int64_t)TM * BN, ss.parts, buf, s);
+        const int col = t.nt * BN + cl;
+        if (cl < 0 || col >= h.d) continue;
         s.x *= scale;
         s.y *= scale;
         s.z *= scale;
@@ -803,21 +776,16 @@ cudaError_t launch_tc(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
     p.units = units;
     p.limit_ns = wait_limit_ns();
     withhold_hook(MODE == ZKEEP ? Z : MODE, p);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {2, 1, 1};
-    cfg.gridDim = dim3((unsigned)(units * Shape<PAIR>::CTAS));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes<PAIR>();
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kern, a, b, o, p);
+    e = launch_early(kern, dim3((unsigned)(units * Shape<PAIR>::CTAS)), THREADS, smem_bytes<PAIR>(),
+                     Shape<PAIR>::CTAS, st, a, b, o, p);
     if constexpr (MODE >= DX) {
         if (e != cudaSuccess || p.cap == 0) return e;
-        head_join_kernel<MODE, PAIR><<<dim3((unsigned)units, Shape<PAIR>::TILE_M / 8), 256, 0, st>>>(p);
-        e = cudaGetLastError();
+        // tiles: of all rows, where that is known to be less than a wave
+        const int64_t rem = tiles < units ? tiles : units;
+        const int64_t M = MODE == DW ? p.h.V : p.h.n_live ? p.h.rows : p.h.T;
+        const int rows = M < Shape<PAIR>::TILE_M ? (int)M : Shape<PAIR>::TILE_M;
+        e = launch_early(head_join_kernel<MODE, PAIR>, dim3((unsigned)rem, (rows + kJoinRows - 1) / kJoinRows), 256, 0,
+                         1, st, p);
     }
     return e;
 }
@@ -826,20 +794,13 @@ inline int64_t tiles_of(int64_t m, int tm, int64_t n, int tn) { return (m + tm -
 
 inline size_t tile_bytes(bool single) { return (size_t)(single ? BM : 2 * BM) * BN * 4; }
 
-// Bytes of parts of a product of `tiles` tiles over kb blocks: at most four waves of
-// them, and 64 parts of at least four blocks a tile (split_tiles).
-size_t part_need(int64_t tiles, int64_t kb, bool single) {
-    const int64_t units = device_sm_count() / (single ? 1 : 2);
-    const int64_t rem = tiles < units ? tiles : units, most = kb / 4 < 64 ? (kb / 4 > 1 ? kb / 4 : 1) : 64;
-    const int64_t n = rem * most < 4 * units ? rem * most : 4 * units;
-    return (size_t)n * tile_bytes(single);
-}
-
 }  // namespace
 
 size_t head_part_bytes(int64_t rows, int V, int d, bool single) {
-    const size_t a = part_need(tiles_of(rows, single ? BM : 2 * BM, d, BN), (V + BK - 1) / BK, single);
-    const size_t b = part_need(tiles_of(V, 2 * BM, d, BN), (rows + BK - 1) / BK, false);
+    const int sms = device_sm_count();
+    const size_t a = split_bound(tiles_of(rows, single ? BM : 2 * BM, d, BN), (V + BK - 1) / BK,
+                                 sms / (single ? 1 : 2), 4) * tile_bytes(single);
+    const size_t b = split_bound(tiles_of(V, 2 * BM, d, BN), (rows + BK - 1) / BK, sms / 2, 4) * tile_bytes(false);
     return a > b ? a : b;
 }
 
@@ -851,13 +812,19 @@ int head_few_tile(int V) {
     return n <= 32 ? 32 : (n + 15) / 16 * 16;
 }
 
+int head_few_stats(int V) {
+    const int n = head_few_tile(V), tiles = (V + n - 1) / n, sms = device_sm_count();
+    return 2 * (tiles < sms ? tiles : sms);
+}
+
 cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool keep, bool single,
                            cudaStream_t st) {
     TcParams p{};
     p.h = h;
     CUtensorMap a, b, o;
     const int64_t xrows = single && !h.n_live ? h.T : h.rows;
-    p.tile_n = single && !keep ? head_few_tile(h.V) : BN;
+    p.few = single && !keep;
+    p.tile_n = p.few ? head_few_tile(h.V) : BN;
     p.a_rows = single ? (int)((xrows < BM ? xrows : BM) + 7) / 8 * 8 : BM;
     if (!make_map(&a, xc, h.d, xrows, h.d, p.a_rows, kBf16) ||
         !make_map(&b, W, h.d, h.V, h.d, single ? p.tile_n : BM, kBf16))
@@ -865,7 +832,7 @@ cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool
     o = a;
     if (keep && !make_map(&o, h.P, h.Vp, h.srows, h.Vp, 32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
         return cudaErrorInvalidValue;
-    const int64_t tiles = tiles_of(h.rows, single ? BM : 2 * BM, h.V, p.tile_n);
+    const int64_t tiles = tiles_of(single ? BM : h.rows, single ? BM : 2 * BM, h.V, p.tile_n);
     if (single) return keep ? launch_tc<ZKEEP, false>(a, b, o, p, tiles, st) : launch_tc<Z, false>(a, b, o, p, tiles, st);
     return keep ? launch_tc<ZKEEP, true>(a, b, o, p, tiles, st) : launch_tc<Z, true>(a, b, o, p, tiles, st);
 }
@@ -882,7 +849,8 @@ cudaError_t launch_head_tc_dx(const HeadDev& h, const void* W, const HeadOut& ou
     CUtensorMap a, b;
     if (!make_map(&a, h.P, h.V, h.srows, h.Vp, BM, kBf16) || !make_map(&b, W, h.d, h.V, h.d, 64, kBf16))
         return cudaErrorInvalidValue;
-    return single ? launch_tc<DX, false>(a, b, a, p, 0, st) : launch_tc<DX, true>(a, b, a, p, 0, st);
+    const int64_t tiles = tiles_of(h.rows, single ? BM : 2 * BM, h.d, BN);
+    return single ? launch_tc<DX, false>(a, b, a, p, tiles, st) : launch_tc<DX, true>(a, b, a, p, tiles, st);
 }
 
 cudaError_t launch_head_tc_dw(const HeadDev& h, const void* xc, const HeadOut& out, float* part, size_t part_bytes,
@@ -898,7 +866,7 @@ cudaError_t launch_head_tc_dw(const HeadDev& h, const void* xc, const HeadOut& o
     if (!make_map(&a, h.P, h.V, h.srows, h.Vp, 64, kBf16) || !make_map(&b, xc, h.d, h.rows, h.d, 64, kBf16) ||
         !make_map(&o, out.out, h.d, h.V, h.d, 32, out.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kBf16))
         return cudaErrorInvalidValue;
-    return launch_tc<DW, true>(a, b, o, p, 0, st);
+    return launch_tc<DW, true>(a, b, o, p, tiles_of(h.V, 2 * BM, h.d, BN), st);
 }
 
 }  // namespace moe
