@@ -48,9 +48,10 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     p.nblk = (h.V + kHeadBlock - 1) / kHeadBlock;
     p.nstat = p.nblk;
     int most_stat = p.nblk;   // a call with more tokens needs no less workspace
-    if (!p.backward && h.dtype == MOE_BF16) {
-        const int few = head_few_stats(h.V);
-        if (p.few) p.nstat = few;
+    if (!p.backward) {
+        const bool bf16 = h.dtype == MOE_BF16;
+        const int few = bf16 ? head_few_stats(h.V) : (h.V + 63) / 64;
+        if (p.few && (bf16 || h.T <= head_simt_few_rows())) p.nstat = few;
         if (few > most_stat) most_stat = few;
     }
     p.Tp = up(h.T > 0 ? h.T : 1, kHeadRows);

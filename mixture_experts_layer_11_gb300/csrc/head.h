@@ -28,7 +28,7 @@ struct HeadDev {
     int T, V, d, K;
     int Vp;                  // row length of P (V rounded up to 64)
     int nblk;                // blocks of kHeadBlock entries
-    int nstat;               // rows of stats: nblk, or two a CTA where a call has few rows
+    int nstat;               // rows of stats: nblk, or for few rows two a CTA (fp32: blocks of 64)
     int p0, rows;            // first live row of the piece, its most rows
     int srows;               // row length of stats (rows, rounded up to kHeadRows)
     const int* n_live;       // null: rows are tokens, all T of them
@@ -107,36 +107,45 @@ inline size_t split_bound(int64_t tiles, int64_t kb, int units, int least) {
     return (size_t)(rem * most < 4 * (int64_t)units ? rem * most : 4 * (int64_t)units);
 }
 
-// The sum of `parts` rows of N values, `stride` values apart, by a block of 256
-// threads: in 1024 / N groups of threads, each every so manieth row, then the groups in
-// order.  Returns the first column of the calling thread's four sums, or -1 in the
-// threads that have none.
-constexpr int kJoinRows = 4;   // rows a block joins
+// The sums of `parts` rows of N values, `stride` values apart, for kJoinRows
+// neighbouring rows at once, by a block of 256 threads: in 1024 / N groups of threads,
+// each every so manieth part, then the groups in order.  Returns the first column of
+// the calling thread's four sums a row, or -1 in the threads that have none.  rows: of
+// the kJoinRows that exist.
+constexpr int kJoinRows = 4;
 template <int N>
-__device__ __forceinline__ int join_row(const float* src, int64_t stride, int parts, float4* buf, float4& s) {
+__device__ __forceinline__ int join_rows(const float* src, int64_t stride, int parts, int rows,
+                                         float4 (*buf)[256], float4 (&s)[kJoinRows]) {
     constexpr int Q = N / 4, G = 256 / Q;
     const int q = threadIdx.x % Q, g = threadIdx.x / Q;
-    s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int k = g; k < parts; k += G) {
-        const float4 v = *reinterpret_cast<const float4*>(src + k * stride + q * 4);
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            if (r >= rows) break;
+            const float4 v = *reinterpret_cast<const float4*>(src + k * stride + r * N + q * 4);
+            s[r].x += v.x;
+            s[r].y += v.y;
+            s[r].z += v.z;
+            s[r].w += v.w;
+        }
     }
-    __syncthreads();   // buf is free again
-    buf[threadIdx.x] = s;
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) buf[r][threadIdx.x] = s[r];
     __syncthreads();
     if (g) return -1;
 #pragma unroll
-    for (int i = 1; i < G; ++i) {
-        const float4 v = buf[i * Q + q];
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
-    }
+    for (int r = 0; r < kJoinRows; ++r)
+#pragma unroll
+        for (int i = 1; i < G; ++i) {
+            const float4 v = buf[r][i * Q + q];
+            s[r].x += v.x;
+            s[r].y += v.y;
+            s[r].z += v.z;
+            s[r].w += v.w;
+        }
     return q * 4;
 }
 
@@ -182,6 +191,7 @@ cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& 
 cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, float* part, size_t part_bytes,
                                 cudaStream_t st);
 size_t head_simt_part_bytes(int64_t rows, int V, int d);
+int head_simt_few_rows();
 
 // The same on the tensor cores, bf16 (single: up to 128 rows; xc may be x itself,
 // where rows are tokens).

@@ -1,10 +1,15 @@
 // head_simt.cu -- the three products of the losses over a vocabulary head in fp32,
 // on the CUDA cores: fp32 is not split for the tensor cores.
 //
-// 64 x 128 tiles, 128 threads, 8 x 8 sums a thread held as packed pairs (64 FMAs a
-// thread and K value for four 16-byte loads from shared memory), four blocks an SM.
-// The FMA pipe bounds: 152 SMs x 128 FMAs at about 1.9 GHz are 74 TFLOP/s.  Half
-// tiles of 128 x 128 cost half as many more loads from L2 and leave finer waves.
+// The FMA pipe bounds (152 SMs x 128 FMAs at about 1.9 GHz are 74 TFLOP/s), fed by
+// fma.rn.f32x2 from shared memory that cp.async fills three or four steps of 16 K
+// values ahead, in the order memory has them:
+//   Z     both operands run along K: a pair is two neighbouring K values, whose sums
+//         are added at the end (64 x 128 tiles of 256 threads, 4 x 8 sums each; for
+//         few rows 8 TM x 64 tiles of 64 threads, so that there are blocks enough to
+//         stream W)
+//   DX    G runs along K, W across: pairs are neighbouring columns, G's value doubled
+//   DW    both run across K         (64 x 128 tiles of 128 threads, 8 x 8 sums each)
 // DX and DW are cut along their reduction as the tensor cores' are (split_tiles).
 #include "head.h"
 
@@ -12,58 +17,68 @@ namespace moe {
 namespace {
 
 constexpr int BM = 64, BN = 128, BK = 16, THREADS = 128;
-constexpr int LDA = BM + 4, LDB = BN + 4;   // a K value's row in shared memory
+constexpr int STAGES = 3;
+constexpr int LDK = BK + 4;                 // a row of K values in shared memory
 constexpr int KB = 64;                      // K values the reduction is cut in multiples of
 constexpr int kBlocksPerSm = 4;
 
 enum Mode { Z = 0, ZKEEP = 1, DX = 2, DW = 3 };
 
-// A ROWS x 16 step of an operand.  KC: the reduction runs along memory ([M][K]), else
-// across it ([K][M]).  Rows and columns past the edge are zero: only the vocabulary
-// may end inside a group of four, and G is zero from there to its row's end.
-template <bool KC, int ROWS, int LD>
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
+    // off: 16 bytes of zeros (src is not read)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A step of an operand to shared memory.  KC: the reduction runs along memory
+// ([M][K]), kept as [ROWS][LDK]; else across it ([K][M]), kept as [BK][ROWS + 4].
+// Rows and columns past the edge are zero: only the vocabulary may end inside a group
+// of four, and G is zero from there to its row's end.
+template <bool KC, int ROWS, int NT>
 struct Loader {
-    static constexpr int N = ROWS * BK / 4 / THREADS;
-    const float* p;
-    int64_t ld;
-    int m0, mmax, kmax;
-    float4 v[N];
-    __device__ __forceinline__ void fetch(int k0, int tid) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int g = tid + i * THREADS;
-            const int m = m0 + (KC ? g >> 2 : g % (ROWS / 4) * 4);
-            const int k = k0 + (KC ? (g & 3) * 4 : g / (ROWS / 4));
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (m < mmax && k < kmax)
-                v[i] = *reinterpret_cast<const float4*>(p + (KC ? (int64_t)m * ld + k : (int64_t)k * ld + m));
-        }
+    static constexpr int LD = KC ? LDK : ROWS + 4;
+    static constexpr int SIZE = KC ? ROWS * LDK : BK * (ROWS + 4);
+    static constexpr int G = KC ? BK / 4 : ROWS / 4;       // groups of four in a row of memory
+    static constexpr int N = ROWS * BK / 4, COPIES = (N + NT - 1) / NT, SKIP = NT / G;
+    static_assert(NT % G == 0, "a thread's groups lie under one another");
+    const float* src;       // the thread's first group at K value 0
+    int64_t ld, skip;       // values from one K step's or row's memory to the next
+    int at, outer, edge, kl;   // place in shared memory; first row of memory, their end; K offset
+    bool inner;
+    __device__ __forceinline__ Loader(const float* p, int64_t ld_, int m0, int mmax, int tid) {
+        const int in = tid % G * 4, out = tid / G;
+        ld = ld_;
+        skip = SKIP * ld_;
+        at = out * LD + in;
+        src = p + (KC ? (int64_t)(m0 + out) * ld_ + in : (int64_t)out * ld_ + m0 + in);
+        outer = KC ? m0 + out : out;
+        edge = mmax;
+        kl = KC ? in : out;
+        inner = KC || m0 + in < mmax;
     }
-    __device__ __forceinline__ void store(float (&s)[BK][LD], int tid) const {
+    __device__ __forceinline__ void copy(float* s, int k0, int kmax) const {
+        const float* p = src + (KC ? k0 : k0 * ld);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int g = tid + i * THREADS;
-            if (KC) {
-                const int m = g >> 2, k = (g & 3) * 4;
-                s[k][m] = v[i].x;
-                s[k + 1][m] = v[i].y;
-                s[k + 2][m] = v[i].z;
-                s[k + 3][m] = v[i].w;
-            } else {
-                *reinterpret_cast<float4*>(&s[g / (ROWS / 4)][g % (ROWS / 4) * 4]) = v[i];
-            }
+        for (int i = 0; i < COPIES; ++i) {
+            if (N % NT && i == COPIES - 1 && at / LD + i * SKIP >= (KC ? ROWS : BK)) break;
+            const bool on = KC ? outer + i * SKIP < edge && k0 + kl < kmax : inner && k0 + kl + i * SKIP < kmax;
+            copy16(s + at + i * SKIP * LD, on ? p + i * skip : src, on);
         }
     }
 };
 
-__device__ __forceinline__ float half_max(float v) {   // over 16 lanes
+template <int W> __device__ __forceinline__ float lanes_max(float v) {   // over W lanes
 #pragma unroll
-    for (int o = 8; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = W / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-__device__ __forceinline__ float half_sum(float v) {
+template <int W> __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -77,25 +92,132 @@ struct SimtParams {
     int units;               // blocks that run at once
 };
 
+// ---- Z ---------------------------------------------------------------------------------
+//
+// TY x TX threads; thread (ty, tx) has rows ty + TY i and columns tx + TX j, so that
+// its 16-byte loads (rows of 80 bytes) meet no bank conflict.
+template <int TY, int TX, int TM, int TN, bool KEEP, int DEPTH, int BLOCKS>
+__global__ void __launch_bounds__(TY * TX, BLOCKS)
+    head_simt_z_kernel(const __grid_constant__ SimtParams p) {
+    constexpr int ROWS = TY * TM, COLS = TX * TN, NT = TY * TX;
+    using LA = Loader<true, ROWS, NT>;
+    using LB = Loader<true, COLS, NT>;
+    __shared__ __align__(16) float smem[DEPTH][LA::SIZE + LB::SIZE];
+    const HeadDev& h = p.h;
+    const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
+    wait_front();
+    const int n = head_rows(h);
+    const int MT = (n + ROWS - 1) / ROWS;   // rows first: W's tile is shared
+    const int mt = MT ? blockIdx.x % MT : 0, nt = MT ? blockIdx.x / MT : 0;
+    const int m0 = mt * ROWS, n0 = nt * COLS;
+    if (MT == 0 || n0 >= h.V) return;
+    const LA la(p.A, h.d, m0, n, tid);
+    const LB lb(p.B, h.d, n0, h.V, tid);
+    uint64_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = 0;
+    const int steps = (h.d + BK - 1) / BK;
+#pragma unroll
+    for (int s = 0; s < DEPTH - 1; ++s) {
+        if (s < steps) {
+            la.copy(smem[s], s * BK, h.d);
+            lb.copy(smem[s] + LA::SIZE, s * BK, h.d);
+        }
+        copies_commit();
+    }
+    for (int s = 0, cur = 0; s < steps; ++s) {
+        copies_wait<DEPTH - 2>();
+        __syncthreads();
+        const int next = cur == 0 ? DEPTH - 1 : cur - 1;   // (s + DEPTH - 1) % DEPTH
+        if (s + DEPTH - 1 < steps) {
+            la.copy(smem[next], (s + DEPTH - 1) * BK, h.d);
+            lb.copy(smem[next] + LA::SIZE, (s + DEPTH - 1) * BK, h.d);
+        }
+        copies_commit();
+        const float* A = smem[cur] + ty * LDK;
+        const float* B = smem[cur] + LA::SIZE + tx * LDK;
+#pragma unroll
+        for (int k = 0; k < BK; k += 4) {
+            ulonglong2 a[TM];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(A + i * TY * LDK + k);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(B + j * TX * LDK + k);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) acc[i][j] = f2_fma(a[i].x, b.x, acc[i][j]);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) acc[i][j] = f2_fma(a[i].y, b.y, acc[i][j]);
+            }
+        }
+        if (++cur == DEPTH) cur = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int r = m0 + ty + TY * i;
+        float v[TN], e[TN], m = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            float a, b;
+            f2_unpack(acc[i][j], a, b);
+            v[j] = a + b;
+            if (n0 + tx + TX * j < h.V) m = fmaxf(m, v[j]);
+        }
+        m = lanes_max<TX>(m) * h.c - kHeadShift;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            e[j] = n0 + tx + TX * j < h.V ? exp2f(fmaf(v[j], h.c, -m)) : 0.f;
+            sum += e[j];
+        }
+        sum = lanes_sum<TX>(sum);
+        if (r >= n) continue;
+        if (tx == 0) h.stats[(int64_t)nt * h.srows + r] = make_float2(m, sum);
+        if (KEEP) {
+            float* out = (float*)h.P + (int64_t)r * h.Vp + n0;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                if (n0 + tx + TX * j < h.Vp) out[tx + TX * j] = e[j];
+        }
+        // the targets' logits
+        const int t = head_token(h, r);
+        int a = 0, b = 1;
+        if (h.start) {
+            const int blk = n0 / kHeadBlock;
+            a = h.start[(int64_t)t * h.nblk + blk];
+            b = blk + 1 < h.nblk ? h.start[(int64_t)t * h.nblk + blk + 1] : h.ent[t];
+        }
+        for (; a < b; ++a) {
+            const int64_t rel = (h.target ? h.target[t] : h.sidx[(int64_t)t * h.K + a]) - n0;
+            if (rel < 0 || rel >= COLS || rel % TX != tx) continue;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                if (tx + TX * j == (int)rel) h.lz[(int64_t)t * h.K + a] = v[j];
+        }
+    }
+}
+
+// ---- DX, DW ------------------------------------------------------------------------------
+
 template <int MODE> struct Shape { int M, N, K, MT, NT; };
 template <int MODE> __device__ __forceinline__ Shape<MODE> shape_of(const HeadDev& h) {
     const int n = head_rows(h);
     Shape<MODE> s;
     s.M = MODE == DW ? h.V : n;
-    s.N = MODE <= ZKEEP ? h.V : h.d;
-    s.K = MODE <= ZKEEP ? h.d : MODE == DX ? h.V : n;
+    s.N = h.d;
+    s.K = MODE == DX ? h.V : n;
     s.MT = (s.M + BM - 1) / BM;
     s.NT = (s.N + BN - 1) / BN;
     return s;
 }
 template <int MODE> __device__ __forceinline__ Split plan_tiles(const SimtParams& p, const Shape<MODE>& s) {
     const int tiles = s.MT * s.NT, kb = (s.K + KB - 1) / KB;
-    if (MODE <= ZKEEP) return Split{tiles, tiles, 1, kb};
     if (MODE == DW && s.K == 0) return Split{p.o.accumulate ? 0 : tiles, tiles, 1, 0};
     return split_tiles(tiles, kb, p.units, p.cap, 1, 1, 1, 1024);
 }
 // Tiles that share the larger operand follow each other: W's columns over the rows
-// (Z, DX), G's columns over the width (DW).
+// (DX), G's columns over the width (DW).
 template <int MODE> __device__ __forceinline__ void tile_at(const Shape<MODE>& s, int i, int& mt, int& nt) {
     if (MODE == DW) {
         mt = i / s.NT;
@@ -117,8 +239,9 @@ __device__ __forceinline__ void write4(const HeadOut& o, float* out, float4 v) {
 
 template <int MODE>
 __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const __grid_constant__ SimtParams p) {
-    constexpr bool A_KC = MODE != DW, B_KC = MODE <= ZKEEP;
-    __shared__ __align__(16) float As[2][BK][LDA], Bs[2][BK][LDB];
+    using LA = Loader<MODE == DX, BM, THREADS>;
+    using LB = Loader<false, BN, THREADS>;
+    __shared__ __align__(16) float smem[STAGES][LA::SIZE + LB::SIZE];
     __shared__ Split plan;
     const HeadDev& h = p.h;
     wait_front();
@@ -144,8 +267,8 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const 
     int mt, nt;
     tile_at<MODE>(sh, tile, mt, nt);
     const int m0 = mt * BM, n0 = nt * BN;
-    Loader<A_KC, BM, LDA> la{p.A, MODE <= ZKEEP ? h.d : h.Vp, m0, sh.M, k1};
-    Loader<B_KC, BN, LDB> lb{p.B, h.d, n0, sh.N, k1};
+    const LA la(p.A, h.Vp, m0, sh.M, tid);
+    const LB lb(p.B, h.d, n0, sh.N, tid);
 
     uint64_t acc[8][4];   // [row][pair of columns]
 #pragma unroll
@@ -153,101 +276,76 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const 
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0;
     const int steps = (k1 - k0 + BK - 1) / BK;
-    if (steps > 0) {
-        la.fetch(k0, tid);
-        lb.fetch(k0, tid);
-        la.store(As[0], tid);
-        lb.store(Bs[0], tid);
-    }
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        const int cur = s & 1;
-        if (s + 1 < steps) {
-            la.fetch(k0 + (s + 1) * BK, tid);
-            lb.fetch(k0 + (s + 1) * BK, tid);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+        if (s < steps) {
+            la.copy(smem[s], k0 + s * BK, k1);
+            lb.copy(smem[s] + LA::SIZE, k0 + s * BK, k1);
         }
+        copies_commit();
+    }
+    for (int s = 0, cur = 0; s < steps; ++s) {
+        copies_wait<STAGES - 2>();
+        __syncthreads();
+        const int next = cur == 0 ? STAGES - 1 : cur - 1;
+        if (s + STAGES - 1 < steps) {
+            la.copy(smem[next], k0 + (s + STAGES - 1) * BK, k1);
+            lb.copy(smem[next] + LA::SIZE, k0 + (s + STAGES - 1) * BK, k1);
+        }
+        copies_commit();
+        const float* A = smem[cur];
+        const float* B = smem[cur] + LA::SIZE + tx * 4;
 #pragma unroll
-        for (int k = 0; k < BK; ++k) {
-            const float4 a0 = *reinterpret_cast<const float4*>(&As[cur][k][ty * 4]);
-            const float4 a1 = *reinterpret_cast<const float4*>(&As[cur][k][32 + ty * 4]);
-            const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&Bs[cur][k][tx * 4]);
-            const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(&Bs[cur][k][64 + tx * 4]);
-            const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            const uint64_t b[4] = {b0.x, b0.y, b1.x, b1.y};
+        for (int k4 = 0; k4 < BK; k4 += 4) {
+            float4 ak[8];   // DX: the rows' four K values
+            if (MODE == DX) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint64_t ai = f2_pack(a[i], a[i]);
+                for (int i = 0; i < 8; ++i) ak[i] = *reinterpret_cast<const float4*>(A + (ty + 8 * i) * LDK + k4);
+            }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = f2_fma(ai, b[j], acc[i][j]);
+            for (int kk = 0; kk < 4; ++kk) {
+                const int k = k4 + kk;
+                float a[8];
+                if (MODE == DX) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) a[i] = kk == 0 ? ak[i].x : kk == 1 ? ak[i].y : kk == 2 ? ak[i].z : ak[i].w;
+                } else {
+                    const float4 a0 = *reinterpret_cast<const float4*>(A + k * LA::LD + ty * 8);
+                    const float4 a1 = *reinterpret_cast<const float4*>(A + k * LA::LD + ty * 8 + 4);
+                    a[0] = a0.x, a[1] = a0.y, a[2] = a0.z, a[3] = a0.w;
+                    a[4] = a1.x, a[5] = a1.y, a[6] = a1.z, a[7] = a1.w;
+                }
+                const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(B + k * LB::LD);
+                const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(B + k * LB::LD + 64);
+                const uint64_t b[4] = {b0.x, b0.y, b1.x, b1.y};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t ai = f2_pack(a[i], a[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = f2_fma(ai, b[j], acc[i][j]);
+                }
             }
         }
-        if (s + 1 < steps) {
-            la.store(As[cur ^ 1], tid);
-            lb.store(Bs[cur ^ 1], tid);
-        }
-        __syncthreads();
+        if (++cur == STAGES) cur = 0;
     }
 
-    const float scale = MODE >= DX ? head_scale(h) : 1.f;
+    const float scale = head_scale(h);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int rl = (i >> 2) * 32 + ty * 4 + (i & 3), r = m0 + rl;
+        const int rl = MODE == DX ? ty + 8 * i : ty * 8 + i, r = m0 + rl;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) f2_unpack(acc[i][j], v[2 * j], v[2 * j + 1]);
-        if (MODE <= ZKEEP) {
-            // the row's 128 columns lie in 16 threads, eight each
-            float m = -INFINITY;
+        if (r >= sh.M) continue;
+        float* out = slot >= 0 ? p.part + ((int64_t)slot * BM + rl) * BN
+                               : (float*)p.o.out + (int64_t)(MODE == DX ? head_token(h, r) : r) * h.d + n0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int col = n0 + (j >> 2) * 64 + tx * 4 + (j & 3);
-                if (col < h.V) m = fmaxf(m, v[j]);
-            }
-            m = half_max(m) * h.c - kHeadShift;
-            float sum = 0.f, e[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int col = n0 + (j >> 2) * 64 + tx * 4 + (j & 3);
-                e[j] = col < h.V ? exp2f(fmaf(v[j], h.c, -m)) : 0.f;
-                sum += e[j];
-            }
-            sum = half_sum(sum);
-            if (r >= sh.M) continue;
-            if (tx == 0) h.stats[(int64_t)nt * h.srows + r] = make_float2(m, sum);
-            if (MODE == ZKEEP) {
-                float* out = (float*)h.P + (int64_t)r * h.Vp + n0;
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj)
-                    if (n0 + jj * 64 < h.Vp)
-                        *reinterpret_cast<float4*>(out + jj * 64 + tx * 4) =
-                            make_float4(e[4 * jj], e[4 * jj + 1], e[4 * jj + 2], e[4 * jj + 3]);
-            }
-            const int t = head_token(h, r);
-            int a = 0, b = 1;
-            if (h.start) {
-                a = h.start[(int64_t)t * h.nblk + nt];
-                b = nt + 1 < h.nblk ? h.start[(int64_t)t * h.nblk + nt + 1] : h.ent[t];
-            }
-            for (; a < b; ++a) {
-                const int64_t k = h.target ? h.target[t] : h.sidx[(int64_t)t * h.K + a];
-                const int64_t rel = k - n0;
-                if (rel < 0 || rel >= BN || ((rel & 63) >> 2) != tx) continue;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if ((j >> 2) * 64 + tx * 4 + (j & 3) == (int)rel) h.lz[(int64_t)t * h.K + a] = v[j];
-            }
-        } else {
-            if (r >= sh.M) continue;
-            float* out = slot >= 0 ? p.part + ((int64_t)slot * BM + rl) * BN
-                                   : (float*)p.o.out + (int64_t)(MODE == DX ? head_token(h, r) : r) * h.d + n0;
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                const int c = jj * 64 + tx * 4;
-                if (n0 + c >= sh.N) continue;
-                const float4 w = make_float4(v[4 * jj], v[4 * jj + 1], v[4 * jj + 2], v[4 * jj + 3]);
-                if (slot >= 0) *reinterpret_cast<float4*>(out + c) = w;
-                else write4<MODE>(p.o, out + c, make_float4(w.x * scale, w.y * scale, w.z * scale, w.w * scale));
-            }
+        for (int jj = 0; jj < 2; ++jj) {
+            const int c = jj * 64 + tx * 4;
+            if (n0 + c >= sh.N) continue;
+            const float4 w = make_float4(v[4 * jj], v[4 * jj + 1], v[4 * jj + 2], v[4 * jj + 3]);
+            if (slot >= 0) *reinterpret_cast<float4*>(out + c) = w;
+            else write4<MODE>(p.o, out + c, make_float4(w.x * scale, w.y * scale, w.z * scale, w.w * scale));
         }
     }
 }
@@ -256,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const 
 template <int MODE>
 __global__ void __launch_bounds__(256) head_simt_join_kernel(const __grid_constant__ SimtParams p) {
     __shared__ Split plan;
-    __shared__ float4 buf[256];
+    __shared__ float4 buf[kJoinRows][256];
     const HeadDev& h = p.h;
     wait_front();
     const Shape<MODE> sh = shape_of<MODE>(h);
@@ -270,40 +368,47 @@ __global__ void __launch_bounds__(256) head_simt_join_kernel(const __grid_consta
     int mt, nt;
     tile_at<MODE>(sh, plan.full + i, mt, nt);
     const float scale = head_scale(h);
-    for (int rl = blockIdx.y * kJoinRows; rl < (int)(blockIdx.y + 1) * kJoinRows; ++rl) {
-        const int r = mt * BM + rl;
-        if (r >= sh.M) return;
-        float4 s;
-        const int c = join_row<BN>(p.part + ((int64_t)i * plan.parts * BM + rl) * BN, (int64_t)BM * BN, plan.parts,
-                                   buf, s);
-        if (c < 0 || nt * BN + c >= sh.N) continue;
-        float* out = (float*)p.o.out + (int64_t)(MODE == DX ? head_token(h, r) : r) * h.d + nt * BN + c;
-        write4<MODE>(p.o, out, make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale));
+    const int rl = blockIdx.y * kJoinRows, r0 = mt * BM + rl, rows = sh.M - r0;
+    if (rows <= 0) return;
+    float4 s[kJoinRows];
+    const int c = join_rows<BN>(p.part + ((int64_t)i * plan.parts * BM + rl) * BN, (int64_t)BM * BN, plan.parts, rows,
+                                buf, s);
+    if (c < 0 || nt * BN + c >= sh.N) return;
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+        if (r >= rows) break;
+        float* out =
+            (float*)p.o.out + (int64_t)(MODE == DX ? head_token(h, r0 + r) : r0 + r) * h.d + nt * BN + c;
+        write4<MODE>(p.o, out, make_float4(s[r].x * scale, s[r].y * scale, s[r].z * scale, s[r].w * scale));
     }
 }
 
 int simt_units() { return kBlocksPerSm * device_sm_count(); }
 
 template <int MODE>
-cudaError_t launch(SimtParams& p, int64_t M, int64_t N, int64_t K, size_t part_bytes, cudaStream_t st) {
+cudaError_t launch(SimtParams& p, int64_t M, int64_t N, size_t part_bytes, cudaStream_t st) {
     const int64_t tiles = (M + BM - 1) / BM * ((N + BN - 1) / BN);
     if (tiles == 0) return cudaSuccess;
     p.units = simt_units();
     p.cap = (int)(part_bytes / (BM * BN * 4));
-    // (a device count below M or K leaves fewer tiles, but perhaps more parts: their
-    // most is what the workspace holds)
-    const int64_t units = MODE <= ZKEEP ? tiles : tiles + p.cap;
-    cudaError_t e = launch_early(head_simt_kernel<MODE>, dim3((unsigned)units), THREADS, 0, 1, st, p);
-    if constexpr (MODE >= DX) {
-        if (e != cudaSuccess || p.cap == 0) return e;
-        const int64_t rem = tiles < p.units ? tiles : p.units, rows = M < BM ? M : BM;
-        e = launch_early(head_simt_join_kernel<MODE>,
-                         dim3((unsigned)rem, (unsigned)((rows + kJoinRows - 1) / kJoinRows)), 256, 0, 1, st, p);
-    }
-    return e;
+    // (fewer live rows leave fewer tiles, but perhaps more parts: at most what the
+    // workspace holds)
+    cudaError_t e = launch_early(head_simt_kernel<MODE>, dim3((unsigned)(tiles + p.cap)), THREADS, 0, 1, st, p);
+    if (e != cudaSuccess || p.cap == 0) return e;
+    const int64_t rem = tiles < p.units ? tiles : p.units, rows = M < BM ? M : BM;
+    return launch_early(head_simt_join_kernel<MODE>, dim3((unsigned)rem, (unsigned)((rows + kJoinRows - 1) / kJoinRows)),
+                        256, 0, 1, st, p);
+}
+
+template <int TM> cudaError_t launch_few(const SimtParams& p, cudaStream_t st) {
+    return launch_early(head_simt_z_kernel<8, 16, TM, 4, false, 4, 1>, dim3((unsigned)((p.h.V + 63) / 64)), 128, 0, 1, st, p);
 }
 
 }  // namespace
+
+// The most rows of a call without gradients that take narrow tiles (its statistics are
+// over blocks of 64): 33 rows of 32000 entries, d = 768, 130 us in 64 x 128 tiles.
+int head_simt_few_rows() { return 64; }
 
 size_t head_simt_part_bytes(int64_t rows, int V, int d) {
     const int64_t nt = (d + BN - 1) / BN;
@@ -313,20 +418,33 @@ size_t head_simt_part_bytes(int64_t rows, int V, int d) {
 }
 
 cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st) {
-    SimtParams p{h, HeadOut{}, (const float*)xc, (const float*)W, nullptr, 0, 0};
-    return keep ? launch<ZKEEP>(p, h.rows, h.V, h.d, 0, st) : launch<Z>(p, h.rows, h.V, h.d, 0, st);
+    const SimtParams p{h, HeadOut{}, (const float*)xc, (const float*)W, nullptr, 0, 0};
+    if (h.nstat > h.nblk) {
+        switch ((h.T + 7) / 8) {
+            case 1: return launch_few<1>(p, st);
+            case 2: return launch_few<2>(p, st);
+            case 3: return launch_few<3>(p, st);
+            case 4: return launch_few<4>(p, st);
+            case 5: return launch_few<5>(p, st);
+            case 6: return launch_few<6>(p, st);
+            default: return launch_few<8>(p, st);
+        }
+    }
+    const int64_t blocks = (int64_t)((h.rows + 63) / 64) * ((h.V + 127) / 128);
+    return launch_early(keep ? head_simt_z_kernel<8, 16, 8, 8, true, STAGES, 2> : head_simt_z_kernel<8, 16, 8, 8, false, STAGES, 2>,
+                        dim3((unsigned)blocks), 128, 0, 1, st, p);
 }
 
 cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& o, float* part, size_t part_bytes,
                                 cudaStream_t st) {
     SimtParams p{h, o, (const float*)h.P, (const float*)W, part, 0, 0};
-    return launch<DX>(p, h.rows, h.d, h.V, part_bytes, st);
+    return launch<DX>(p, h.rows, h.d, part_bytes, st);
 }
 
 cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, float* part, size_t part_bytes,
                                 cudaStream_t st) {
     SimtParams p{h, o, (const float*)h.P, (const float*)xc, part, 0, 0};
-    return launch<DW>(p, h.V, h.d, h.rows, part_bytes, st);
+    return launch<DW>(p, h.V, h.d, part_bytes, st);
 }
 
 }  // namespace moe

@@ -646,7 +646,7 @@ template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ TcParams p) {
     constexpr int TM = Shape<PAIR>::TILE_M;
     __shared__ Split ss;
-    __shared__ float4 buf[256];
+    __shared__ float4 buf[kJoinRows][256];
     wait_front();
     if (threadIdx.x < 32) {
         int kb;
@@ -661,18 +661,22 @@ __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ 
     const Tile t = get_tile<MODE, PAIR>(c, p, ss.full + i);
     const int M = MODE == DW ? h.V : head_rows(h);
     const float scale = head_scale(h);
-    for (int rr = blockIdx.y * kJoinRows; rr < (int)(blockIdx.y + 1) * kJoinRows; ++rr) {
-        const int r = t.mt * TM + rr;
-        if (r >= M) return;
-        float4 s;
-        const int cl = join_row<BN>(p.part + ((int64_t)i * ss.parts * TM + rr) * BN, (int64_t)TM * BN, ss.parts, buf, s);
-        const int col = t.nt * BN + cl;
-        if (cl < 0 || col >= h.d) continue;
+    const int rl = blockIdx.y * kJoinRows, r0 = t.mt * TM + rl, rows = M - r0;
+    if (rows <= 0) return;
+    float4 sums[kJoinRows];
+    const int cl = join_rows<BN>(p.part + ((int64_t)i * ss.parts * TM + rl) * BN, (int64_t)TM * BN, ss.parts, rows, buf,
+                                 sums);
+    const int col = t.nt * BN + cl;
+    if (cl < 0 || col >= h.d) return;
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+        if (r >= rows) break;
+        float4 s = sums[r];
         s.x *= scale;
         s.y *= scale;
         s.z *= scale;
         s.w *= scale;
-        const int64_t at = (int64_t)(MODE == DX ? head_token(h, r) : r) * h.d + col;
+        const int64_t at = (int64_t)(MODE == DX ? head_token(h, r0 + r) : r0 + r) * h.d + col;
         if (MODE == DW && p.o.f32) {
             float4* o = reinterpret_cast<float4*>((float*)p.o.out + at);
             if (p.o.accumulate) {
