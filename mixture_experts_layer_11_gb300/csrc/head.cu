@@ -33,7 +33,7 @@ struct Plan {
     // few: losses alone of up to kHeadFewRows rows, none gathered; single: as few rows in
     // bf16; wide: dW is summed in an fp32 buffer of the workspace
     bool few, single, backward, wide;
-    size_t ctl, live, pos, xc, sidx, q, lq, ent, start, lz, stats, lse2, P, dW32, part, part_bytes, total;
+    size_t ctl, live, pos, xc, sidx, q, lq, ent, start, lz, stats, row, P, dW32, part, part_bytes, total;
 };
 
 Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
@@ -75,7 +75,7 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     p.ctl = take(256);
     p.lz = take(T * K * 4);
     p.stats = take((size_t)most_stat * piece * sizeof(float2));
-    p.lse2 = take((size_t)piece * 4);
+    p.row = take((size_t)piece * sizeof(float4));
     if (distill) {
         p.sidx = take(T * K * 4);
         p.q = take(T * K * 4);
@@ -90,7 +90,7 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     }
     if (p.backward) {
         p.P = take((size_t)piece * p.Vp * p.esize);
-        p.part_bytes = h.dtype == MOE_BF16 ? head_part_bytes(piece, h.V, h.d, p.single)
+        p.part_bytes = h.dtype == MOE_BF16 ? head_part_bytes(piece, h.V, h.d)
                                            : head_simt_part_bytes(piece, h.V, h.d);
         p.part = take(p.part_bytes);
         if (p.wide) p.dW32 = take((size_t)h.V * h.d * 4);
@@ -339,13 +339,36 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
         return;
     }
     const int64_t at = (int64_t)t * h.K;
-    float loss = 0.f;
+    const float weight = h.row && h.weight ? h.weight[t] : 1.f;
+    float loss = 0.f, g = 0.f;
+    int k = -1;
     if (h.target) {
-        loss = (lse2 - h.lz[at] * h.c) * kLn2;
+        const float z = h.lz[at] * h.c;
+        loss = (lse2 - z) * kLn2;
+        k = (int)h.target[t];
+        g = weight * (exp2f(z - lse2) - 1.f);
     } else {
         const int e = h.ent[t];
-        for (int j = lane; j < e; j += 32)
-            loss += h.q[at + j] * (h.lq[at + j] + (lse2 - h.lz[at + j] * h.c) * kLn2);
+        float gs[MOE_HEAD_MAX_ENTRIES / 32];
+#pragma unroll
+        for (int i = 0; i < MOE_HEAD_MAX_ENTRIES / 32; ++i) {
+            const int j = i * 32 + lane;
+            if (j >= e) break;
+            const float z = h.lz[at + j] * h.c;
+            float q = h.q[at + j];
+            loss += q * (h.lq[at + j] + (lse2 - z) * kLn2);
+            if (h.row) {   // an index that is there more than once has the sum of all
+                const int me = h.sidx[at + j];
+                for (int u = j - 1; u >= 0 && h.sidx[at + u] == me; --u) q += h.q[at + u];
+                for (int u = j + 1; u < e && h.sidx[at + u] == me; ++u) q += h.q[at + u];
+                gs[i] = weight * (exp2f(z - lse2) - q);
+            }
+        }
+        if (h.row) {   // the entries' values of G, in place of their logits
+#pragma unroll
+            for (int i = 0; i < MOE_HEAD_MAX_ENTRIES / 32; ++i)
+                if (i * 32 + lane < e) h.lz[at + i * 32 + lane] = gs[i];
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
         loss *= h.loss_scale;
@@ -354,7 +377,7 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
         if (!isfinite(loss) || !isfinite(lse2)) report(h.status, MOE_ERR_NONFINITE);
         h.loss[t] = loss;
         if (h.lse) h.lse[t] = lse2 * kLn2;
-        h.lse2[r] = lse2;
+        if (h.row) h.row[r] = make_float4(lse2, weight, __int_as_float(k), g);
     }
 }
 
@@ -385,58 +408,65 @@ template <> struct Pair<float> {
     }
 };
 
-constexpr int kGradLoads = 4;     // of 16 bytes a thread, in flight at once
+// A warp takes kGradCols columns of a row, eight loads of 16 bytes a lane in flight.
+constexpr int kGradWarps = 8, kGradCols = 2048;
 
 template <typename T>
-__global__ void __launch_bounds__(256) head_gradient_kernel(const HeadDev h) {
-    constexpr int N = Pair<T>::N, COLS = 256 * N * kGradLoads;   // columns of a row a block turns
+__global__ void __launch_bounds__(32 * kGradWarps) head_gradient_kernel(const __grid_constant__ HeadDev h) {
+    constexpr int N = Pair<T>::N, LOADS = 8, PART = 32 * N * LOADS;   // columns of 8 loads
     wait_front();
-    const int n = head_rows(h);
+    const int lane = threadIdx.x & 31;
+    const int n = head_rows(h), nck = (h.Vp + kGradCols - 1) / kGradCols;
+    const int64_t it = (int64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5);
     // the last rows first: L2 still holds some of them
-    const int r = (n + 63) / 64 * 64 - 1 - (int)blockIdx.x, c0 = blockIdx.y * COLS;
+    const int r = (n + 63) / 64 * 64 - 1 - (int)(it / nck), c0 = (int)(it % nck) * kGradCols;
     if (r < 0) return;
+    const bool on = r < n;   // else a row of the last K block, behind the live ones: zeros
     T* row = (T*)h.P + (int64_t)r * h.Vp;
-    const int c1 = c0 + COLS < h.Vp ? c0 + COLS : h.Vp;
-    const int first = c0 + threadIdx.x * N;
-    uint4 v[kGradLoads];
-    if (r >= n) {   // the last K block's rows behind the live ones
-#pragma unroll
-        for (int i = 0; i < kGradLoads; ++i)
-            if (first + i * 256 * N < c1)
-                *reinterpret_cast<uint4*>(row + first + i * 256 * N) = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    float m[kGradLoads];
-#pragma unroll
-    for (int i = 0; i < kGradLoads; ++i) {
-        const int c = first + i * 256 * N;
-        if (c < c1) {
-            v[i] = *reinterpret_cast<const uint4*>(row + c);
-            m[i] = h.stats[(int64_t)(c / kHeadBlock) * h.srows + r].x;
+    float4 info = make_float4(0.f, 0.f, 0.f, 0.f);
+    int a = 0, b = 0;
+    int64_t at = 0;
+    if (on) info = h.row[r];
+    if (on && !h.target) {   // the entries in these columns
+        const int t = head_token(h, r);
+        at = (int64_t)t * h.K;
+        b = h.ent[t];
+        if (h.start) {
+            const uint8_t* st = h.start + (int64_t)t * h.nblk;
+            a = st[c0 / kHeadBlock];
+            if (c0 + kGradCols < h.V) b = st[(c0 + kGradCols) / kHeadBlock];
         }
     }
-    const int t = head_token(h, r);
-    const float lse2 = h.lse2[r];
-    const float weight = h.weight ? h.weight[t] : 1.f;
+#pragma unroll 1
+    for (int c1 = c0; c1 < c0 + kGradCols; c1 += PART) {
+        uint4 v[LOADS];
+        float m[LOADS];
+        const int c = c1 + lane * N;
 #pragma unroll
-    for (int i = 0; i < kGradLoads; ++i) {
-        const int c = first + i * 256 * N;
-        if (c < c1) *reinterpret_cast<uint4*>(row + c) = Pair<T>::scale(v[i], weight * exp2f(m[i] - lse2), h.V - c);
-    }
-    __syncthreads();
-    // the targets' entries, from their own logits
-    const int64_t at = (int64_t)t * h.K;
-    const int e = h.target ? 1 : h.ent[t];
-    for (int j = threadIdx.x; j < e; j += 256) {
-        const int k = h.target ? (int)h.target[t] : h.sidx[at + j];
-        if (k < c0 || k >= c1) continue;
-        float q = 1.f;
-        if (!h.target) {
-            if (j > 0 && h.sidx[at + j - 1] == k) continue;   // the first of equals writes
-            q = h.q[at + j];
-            for (int i = j + 1; i < e && h.sidx[at + i] == k; ++i) q += h.q[at + i];
+        for (int i = 0; i < LOADS; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            m[i] = 0.f;
+            if (on && c + i * 32 * N < h.Vp) {
+                v[i] = *reinterpret_cast<const uint4*>(row + c + i * 32 * N);
+                m[i] = h.stats[(int64_t)((c + i * 32 * N) / kHeadBlock) * h.srows + r].x;
+            }
         }
-        row[k] = from_f32<T>(weight * (exp2f(fmaf(h.lz[at + j], h.c, -lse2)) - q));
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (c + i * 32 * N < h.Vp)
+                *reinterpret_cast<uint4*>(row + c + i * 32 * N) =
+                    Pair<T>::scale(v[i], info.y * exp2f(m[i] - info.x), h.V - c - i * 32 * N);
+    }
+    __syncwarp();
+    // the targets' own values
+    if (h.target) {
+        const int k = __float_as_int(info.z);
+        if (on && lane == 0 && k >= c0 && k < c0 + kGradCols) row[k] = from_f32<T>(info.w);
+    } else {
+        for (int j = a + lane; j < b; j += 32) {
+            const int k = h.sidx[at + j];
+            if (k >= c0 && k < c0 + kGradCols) row[k] = from_f32<T>(h.lz[at + j]);
+        }
     }
 }
 
@@ -493,7 +523,7 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
     }
     h.lz = (float*)(ws + p.lz);
     h.stats = (float2*)(ws + p.stats);
-    h.lse2 = (float*)(ws + p.lse2);
+    if (g) h.row = (float4*)(ws + p.row);
     h.P = ws + p.P;
     h.c = kLog2e / c.temperature;
     h.loss_scale = c.temperature * c.temperature;
@@ -537,20 +567,16 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         const int64_t rows = s.T - h.p0 < h.rows ? s.T - h.p0 : h.rows;
         e = launch_early(head_loss_kernel, dim3((unsigned)((rows + 31) / 32)), 1024, 0, 1, st, h);
         if (!p.backward || e != cudaSuccess) continue;
-        const int cols = 256 * (16 / p.esize) * kGradLoads;
+        const int64_t items = up(rows, 64) * (up(p.Vp, kGradCols) / kGradCols);
         e = launch_early(bf16 ? head_gradient_kernel<__nv_bfloat16> : head_gradient_kernel<float>,
-                         dim3((unsigned)up(rows, 64), (unsigned)((p.Vp + cols - 1) / cols)), 256, 0, 1, st, h);
-        if (e == cudaSuccess && want_dx) {
-            const HeadOut o{g->dx, !bf16, 0};
-            e = bf16 ? launch_head_tc_dx(h, c.W, o, part, p.part_bytes, p.single, st)
-                     : launch_head_simt_dx(h, c.W, o, part, p.part_bytes, st);
-        }
-        if (e == cudaSuccess && want_dW) {
-            HeadOut o{p.wide ? (void*)(ws + p.dW32) : g->dW, p.wide || g->dW_dtype == MOE_F32,
-                      g->accumulate || i > 0};
-            e = bf16 ? launch_head_tc_dw(h, xp, o, part, p.part_bytes, st)
-                     : launch_head_simt_dw(h, xp, o, part, p.part_bytes, st);
-        }
+                         dim3((unsigned)((items + kGradWarps - 1) / kGradWarps)), 32 * kGradWarps, 0, 1, st, h);
+        if (e != cudaSuccess) break;
+        const HeadOut dx{want_dx ? g->dx : nullptr, !bf16, 0};
+        const HeadOut dW{want_dW ? p.wide ? (void*)(ws + p.dW32) : g->dW : nullptr,
+                         p.wide || g->dW_dtype == MOE_F32, g->accumulate || i > 0};
+        if (!want_dx && !want_dW) continue;
+        e = bf16 ? launch_head_tc_grad(h, xp, c.W, dx, dW, part, p.piece, st)
+                 : launch_head_simt_grad(h, xp, c.W, dx, dW, part, p.piece, st);
     }
     if (e == cudaSuccess && want_dW && p.wide) {
         const int64_t n4 = (int64_t)s.V * s.d / 4;

@@ -41,7 +41,8 @@ struct HeadDev {
     const uint8_t* start;    // first entry of each block [T][nblk]
     float* lz;               // logits of the targets / entries [T][K]
     float2* stats;           // [nstat][srows]: largest exponent - kHeadShift, sum (0: no entries)
-    float* lse2;             // [srows] log2 of the sum of exponentials
+    float4* row;             // [srows], with gradients: log2 of the sum of exponentials,
+                             // weight, and the target with its value of G (CE)
     void* P;                 // [rows][Vp]: exponentials, then gradients by the logits
     const float* weight;
     float c;                 // log2(e) / temperature
@@ -181,29 +182,25 @@ cudaError_t launch_early(void (*kern)(A...), dim3 grid, int block, size_t smem, 
 //   DW  dW (+)= scale * G^T xc
 // part: room for the sums of cut tiles.
 struct HeadOut {
-    void* out;               // dx [T,d] or dW [V,d]
+    void* out;               // dx [T,d] or dW [V,d]; null: not wanted
     int f32;                 // fp32 (else bf16)
     int accumulate;
 };
 cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st);
-cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& o, float* part, size_t part_bytes,
-                                cudaStream_t st);
-cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, float* part, size_t part_bytes,
-                                cudaStream_t st);
+cudaError_t launch_head_simt_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
+                                  const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st);
 size_t head_simt_part_bytes(int64_t rows, int V, int d);
 int head_simt_few_rows();
 
 // The same on the tensor cores, bf16 (single: up to 128 rows; xc may be x itself,
-// where rows are tokens).
+// where rows are tokens).  part_rows: those that head_part_bytes was asked for.
 constexpr int kHeadFewRows = 128;
 int head_few_tile(int V);
 int head_few_stats(int V);   // rows of statistics of a few-row call
-size_t head_part_bytes(int64_t rows, int V, int d, bool single);
+size_t head_part_bytes(int64_t rows, int V, int d);
 cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool keep, bool single,
                            cudaStream_t st);
-cudaError_t launch_head_tc_dx(const HeadDev& h, const void* W, const HeadOut& o, float* part,
-                              size_t part_bytes, bool single, cudaStream_t st);
-cudaError_t launch_head_tc_dw(const HeadDev& h, const void* xc, const HeadOut& o, float* part,
-                              size_t part_bytes, cudaStream_t st);
+cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
+                                const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st);
 
 }  // namespace moe

@@ -84,12 +84,13 @@ template <int W> __device__ __forceinline__ float lanes_sum(float v) {
 
 struct SimtParams {
     HeadDev h;
-    HeadOut o;
-    const float* A;
-    const float* B;
-    float* part;             // [cap][BM][BN] sums of cut tiles
-    int cap;
+    HeadOut dx, dW;          // out null: not wanted
+    const float* xc;
+    const float* W;
+    float* part;             // [capx + capw][BM][BN] sums of cut tiles, DX's first
+    int capx, capw;
     int units;               // blocks that run at once
+    int ux;                  // blocks of DX's (the first)
 };
 
 // ---- Z ---------------------------------------------------------------------------------
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(TY * TX, BLOCKS)
     const int mt = MT ? blockIdx.x % MT : 0, nt = MT ? blockIdx.x / MT : 0;
     const int m0 = mt * ROWS, n0 = nt * COLS;
     if (MT == 0 || n0 >= h.V) return;
-    const LA la(p.A, h.d, m0, n, tid);
-    const LB lb(p.B, h.d, n0, h.V, tid);
+    const LA la(p.xc, h.d, m0, n, tid);
+    const LB lb(p.W, h.d, n0, h.V, tid);
     uint64_t acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -213,8 +214,8 @@ template <int MODE> __device__ __forceinline__ Shape<MODE> shape_of(const HeadDe
 }
 template <int MODE> __device__ __forceinline__ Split plan_tiles(const SimtParams& p, const Shape<MODE>& s) {
     const int tiles = s.MT * s.NT, kb = (s.K + KB - 1) / KB;
-    if (MODE == DW && s.K == 0) return Split{p.o.accumulate ? 0 : tiles, tiles, 1, 0};
-    return split_tiles(tiles, kb, p.units, p.cap, 1, 1, 1, 1024);
+    if (MODE == DW && s.K == 0) return Split{p.dW.accumulate ? 0 : tiles, tiles, 1, 0};
+    return split_tiles(tiles, kb, p.units, MODE == DX ? p.capx : p.capw, 1, 1, 1, 1024);
 }
 // Tiles that share the larger operand follow each other: W's columns over the rows
 // (DX), G's columns over the width (DW).
@@ -237,14 +238,19 @@ __device__ __forceinline__ void write4(const HeadOut& o, float* out, float4 v) {
     *reinterpret_cast<float4*>(out) = v;
 }
 
+template <int MODE> struct Loaders {
+    using A = Loader<MODE == DX, BM, THREADS>;
+    using B = Loader<false, BN, THREADS>;
+    static constexpr int SIZE = A::SIZE + B::SIZE;
+};
+
 template <int MODE>
-__global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const __grid_constant__ SimtParams p) {
-    using LA = Loader<MODE == DX, BM, THREADS>;
-    using LB = Loader<false, BN, THREADS>;
-    __shared__ __align__(16) float smem[STAGES][LA::SIZE + LB::SIZE];
-    __shared__ Split plan;
+__device__ __forceinline__ void product(const SimtParams& p, int u, float* smem_raw, Split& plan) {
+    using LA = typename Loaders<MODE>::A;
+    using LB = typename Loaders<MODE>::B;
+    float(*smem)[Loaders<MODE>::SIZE] = reinterpret_cast<float(*)[Loaders<MODE>::SIZE]>(smem_raw);
     const HeadDev& h = p.h;
-    wait_front();
+    const HeadOut& o = MODE == DX ? p.dx : p.dW;
     const Shape<MODE> sh = shape_of<MODE>(h);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     if (tid < 32) {
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const 
         if (tid == 0) plan = s;
     }
     __syncthreads();
-    const int u = blockIdx.x, rem = plan.tiles - min(plan.full, plan.tiles);
+    const int rem = plan.tiles - min(plan.full, plan.tiles);
     int tile = u, k0 = 0, k1 = sh.K, slot = -1;
     if (plan.parts > 1 && u >= plan.full) {
         const int v = u - plan.full, part = v / rem;
@@ -260,15 +266,15 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const 
         tile = plan.full + v % rem;
         k0 = part * plan.kbp * KB;
         k1 = min(k1, k0 + plan.kbp * KB);
-        slot = (tile - plan.full) * plan.parts + part;
+        slot = (MODE == DX ? 0 : p.capx) + (tile - plan.full) * plan.parts + part;
     } else if (u >= plan.tiles) {
         return;
     }
     int mt, nt;
     tile_at<MODE>(sh, tile, mt, nt);
     const int m0 = mt * BM, n0 = nt * BN;
-    const LA la(p.A, h.Vp, m0, sh.M, tid);
-    const LB lb(p.B, h.d, n0, sh.N, tid);
+    const LA la((const float*)h.P, h.Vp, m0, sh.M, tid);
+    const LB lb(MODE == DX ? p.W : p.xc, h.d, n0, sh.N, tid);
 
     uint64_t acc[8][4];   // [row][pair of columns]
 #pragma unroll
@@ -338,32 +344,40 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_kernel(const 
         for (int j = 0; j < 4; ++j) f2_unpack(acc[i][j], v[2 * j], v[2 * j + 1]);
         if (r >= sh.M) continue;
         float* out = slot >= 0 ? p.part + ((int64_t)slot * BM + rl) * BN
-                               : (float*)p.o.out + (int64_t)(MODE == DX ? head_token(h, r) : r) * h.d + n0;
+                               : (float*)o.out + (int64_t)(MODE == DX ? head_token(h, r) : r) * h.d + n0;
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
             const int c = jj * 64 + tx * 4;
             if (n0 + c >= sh.N) continue;
             const float4 w = make_float4(v[4 * jj], v[4 * jj + 1], v[4 * jj + 2], v[4 * jj + 3]);
             if (slot >= 0) *reinterpret_cast<float4*>(out + c) = w;
-            else write4<MODE>(p.o, out + c, make_float4(w.x * scale, w.y * scale, w.z * scale, w.w * scale));
+            else write4<MODE>(o, out + c, make_float4(w.x * scale, w.y * scale, w.z * scale, w.w * scale));
         }
     }
 }
 
+// DX's blocks, then DW's.
+__global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_grad_kernel(const __grid_constant__ SimtParams p) {
+    constexpr int SIZE = Loaders<DX>::SIZE > Loaders<DW>::SIZE ? Loaders<DX>::SIZE : Loaders<DW>::SIZE;
+    __shared__ __align__(16) float smem[STAGES * SIZE];
+    __shared__ Split plan;
+    wait_front();
+    if ((int)blockIdx.x < p.ux) product<DX>(p, blockIdx.x, smem, plan);
+    else product<DW>(p, blockIdx.x - p.ux, smem, plan);
+}
+
 // The parts of cut tiles, added in order.
 template <int MODE>
-__global__ void __launch_bounds__(256) head_simt_join_kernel(const __grid_constant__ SimtParams p) {
-    __shared__ Split plan;
-    __shared__ float4 buf[kJoinRows][256];
+__device__ __forceinline__ void join(const SimtParams& p, int i, Split& plan, float4 (*buf)[256]) {
     const HeadDev& h = p.h;
-    wait_front();
+    const HeadOut& o = MODE == DX ? p.dx : p.dW;
     const Shape<MODE> sh = shape_of<MODE>(h);
+    if (i >= sh.MT * sh.NT % p.units) return;
     if (threadIdx.x < 32) {
         const Split s = plan_tiles<MODE>(p, sh);
         if (threadIdx.x == 0) plan = s;
     }
     __syncthreads();
-    const int i = blockIdx.x;
     if (plan.parts <= 1 || plan.full + i >= plan.tiles) return;
     int mt, nt;
     tile_at<MODE>(sh, plan.full + i, mt, nt);
@@ -371,54 +385,54 @@ __global__ void __launch_bounds__(256) head_simt_join_kernel(const __grid_consta
     const int rl = blockIdx.y * kJoinRows, r0 = mt * BM + rl, rows = sh.M - r0;
     if (rows <= 0) return;
     float4 s[kJoinRows];
-    const int c = join_rows<BN>(p.part + ((int64_t)i * plan.parts * BM + rl) * BN, (int64_t)BM * BN, plan.parts, rows,
-                                buf, s);
+    const int64_t slot = (MODE == DX ? 0 : p.capx) + (int64_t)i * plan.parts;
+    const int c = join_rows<BN>(p.part + (slot * BM + rl) * BN, (int64_t)BM * BN, plan.parts, rows, buf, s);
     if (c < 0 || nt * BN + c >= sh.N) return;
 #pragma unroll
     for (int r = 0; r < kJoinRows; ++r) {
         if (r >= rows) break;
-        float* out =
-            (float*)p.o.out + (int64_t)(MODE == DX ? head_token(h, r0 + r) : r0 + r) * h.d + nt * BN + c;
-        write4<MODE>(p.o, out, make_float4(s[r].x * scale, s[r].y * scale, s[r].z * scale, s[r].w * scale));
+        float* out = (float*)o.out + (int64_t)(MODE == DX ? head_token(h, r0 + r) : r0 + r) * h.d + nt * BN + c;
+        write4<MODE>(o, out, make_float4(s[r].x * scale, s[r].y * scale, s[r].z * scale, s[r].w * scale));
     }
+}
+__global__ void __launch_bounds__(256) head_simt_join_kernel(const __grid_constant__ SimtParams p, int nx) {
+    __shared__ Split plan;
+    __shared__ float4 buf[kJoinRows][256];
+    wait_front();
+    if ((int)blockIdx.x < nx) join<DX>(p, blockIdx.x, plan, buf);
+    else join<DW>(p, blockIdx.x - nx, plan, buf);
 }
 
 int simt_units() { return kBlocksPerSm * device_sm_count(); }
-
-template <int MODE>
-cudaError_t launch(SimtParams& p, int64_t M, int64_t N, size_t part_bytes, cudaStream_t st) {
-    const int64_t tiles = (M + BM - 1) / BM * ((N + BN - 1) / BN);
-    if (tiles == 0) return cudaSuccess;
-    p.units = simt_units();
-    p.cap = (int)(part_bytes / (BM * BN * 4));
-    // (fewer live rows leave fewer tiles, but perhaps more parts: at most what the
-    // workspace holds)
-    cudaError_t e = launch_early(head_simt_kernel<MODE>, dim3((unsigned)(tiles + p.cap)), THREADS, 0, 1, st, p);
-    if (e != cudaSuccess || p.cap == 0) return e;
-    const int64_t rem = tiles < p.units ? tiles : p.units, rows = M < BM ? M : BM;
-    return launch_early(head_simt_join_kernel<MODE>, dim3((unsigned)rem, (unsigned)((rows + kJoinRows - 1) / kJoinRows)),
-                        256, 0, 1, st, p);
-}
 
 template <int TM> cudaError_t launch_few(const SimtParams& p, cudaStream_t st) {
     return launch_early(head_simt_z_kernel<8, 16, TM, 4, false, 4, 1>, dim3((unsigned)((p.h.V + 63) / 64)), 128, 0, 1, st, p);
 }
 
+int64_t tiles_of(int64_t m, int64_t n) { return (m + BM - 1) / BM * ((n + BN - 1) / BN); }
+int64_t parts_dx(int64_t rows, int V, int d) {
+    return (int64_t)split_bound(tiles_of(rows, d), (V + KB - 1) / KB, simt_units(), 1);
+}
+int64_t parts_dw(int64_t rows, int V, int d) {
+    return (int64_t)split_bound(tiles_of(V, d), (rows + KB - 1) / KB, simt_units(), 1);
+}
+
 }  // namespace
 
 // The most rows of a call without gradients that take narrow tiles (its statistics are
-// over blocks of 64): 33 rows of 32000 entries, d = 768, 130 us in 64 x 128 tiles.
+// over blocks of 64): 33 rows of 32000 entries, d = 768, 130 us in 64 x 128 tiles, 62
+// in narrow ones.
 int head_simt_few_rows() { return 64; }
 
 size_t head_simt_part_bytes(int64_t rows, int V, int d) {
-    const int64_t nt = (d + BN - 1) / BN;
-    const size_t a = split_bound((rows + BM - 1) / BM * nt, (V + KB - 1) / KB, simt_units(), 1);
-    const size_t b = split_bound((V + BM - 1) / BM * nt, (rows + KB - 1) / KB, simt_units(), 1);
-    return (a > b ? a : b) * BM * BN * 4;
+    return (size_t)(parts_dx(rows, V, d) + parts_dw(rows, V, d)) * BM * BN * 4;
 }
 
 cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st) {
-    const SimtParams p{h, HeadOut{}, (const float*)xc, (const float*)W, nullptr, 0, 0};
+    SimtParams p{};
+    p.h = h;
+    p.xc = (const float*)xc;
+    p.W = (const float*)W;
     if (h.nstat > h.nblk) {
         switch ((h.T + 7) / 8) {
             case 1: return launch_few<1>(p, st);
@@ -435,16 +449,32 @@ cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bo
                         dim3((unsigned)blocks), 128, 0, 1, st, p);
 }
 
-cudaError_t launch_head_simt_dx(const HeadDev& h, const void* W, const HeadOut& o, float* part, size_t part_bytes,
-                                cudaStream_t st) {
-    SimtParams p{h, o, (const float*)h.P, (const float*)W, part, 0, 0};
-    return launch<DX>(p, h.rows, h.d, part_bytes, st);
-}
-
-cudaError_t launch_head_simt_dw(const HeadDev& h, const void* xc, const HeadOut& o, float* part, size_t part_bytes,
-                                cudaStream_t st) {
-    SimtParams p{h, o, (const float*)h.P, (const float*)xc, part, 0, 0};
-    return launch<DW>(p, h.V, h.d, part_bytes, st);
+cudaError_t launch_head_simt_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
+                                  const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st) {
+    SimtParams p{};
+    p.h = h;
+    p.dx = dx;
+    p.dW = dW;
+    p.xc = (const float*)xc;
+    p.W = (const float*)W;
+    p.part = part;
+    p.capx = (int)parts_dx(part_rows, h.V, h.d);
+    p.capw = (int)parts_dw(part_rows, h.V, h.d);
+    p.units = simt_units();
+    // (fewer live rows leave fewer tiles, but perhaps more parts: at most what the
+    // workspace holds)
+    const int64_t rows = h.T - h.p0 < h.rows ? h.T - h.p0 : h.rows;
+    const int64_t tx = dx.out ? tiles_of(rows, h.d) : 0, tw = dW.out ? tiles_of(h.V, h.d) : 0;
+    p.ux = (int)(tx ? tx + p.capx : 0);
+    const int64_t blocks = p.ux + (tw ? tw + p.capw : 0);
+    if (blocks == 0) return cudaSuccess;
+    cudaError_t e = launch_early(head_simt_grad_kernel, dim3((unsigned)blocks), THREADS, 0, 1, st, p);
+    if (e != cudaSuccess) return e;
+    const int nx = p.capx ? (int)(tx < p.units ? tx : p.units) : 0, nw = p.capw ? (int)(tw % p.units) : 0;
+    if (nx + nw == 0) return cudaSuccess;
+    const int most = nw || rows > BM ? BM : (int)rows;
+    return launch_early(head_simt_join_kernel, dim3((unsigned)(nx + nw), (unsigned)((most + kJoinRows - 1) / kJoinRows)),
+                        256, 0, 1, st, p, nx);
 }
 
 }  // namespace moe

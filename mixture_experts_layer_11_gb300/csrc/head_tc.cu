@@ -4,19 +4,19 @@
 //   Z, ZKEEP  tiles of xc W^T whose epilogue leaves a row's largest logit and sum of
 //             exponentials a 128 columns, its targets' logits and (ZKEEP) the
 //             exponentials as fp16
-//   DX        dx = scale G W       reduction over the vocabulary
-//   DW        dW (+)= scale G^T xc reduction over the live tokens
+//   GRAD      dx = scale G W (DX: a reduction over the vocabulary) and
+//             dW (+)= scale G^T xc (DW: over the live rows), one launch for both
 //
 // CTA = 10 warps: warp 0 issues the TMA loads into a ring of stages of 64 K values,
 // one thread of warp 1 the MMAs into one of two TMEM accumulators of 256 columns,
 // eight warps drain the other one: warp w the lanes of quarter w % 4 and 128
 // columns.  PAIR: clusters of two CTAs, tiles of 256 x 256 (cta_group::2, each CTA
 // holds its 128 rows of A and 128 columns of B, 32 KB a stage, six stages); else
-// one CTA, 128 rows (48 KB, four stages), for calls of up to 128 tokens, where W's
-// bytes bound and half a pair's rows would be empty.
+// one CTA, 128 rows (48 KB, four stages), for Z of calls of up to 128 tokens, where
+// W's bytes bound and half a pair's rows would be empty.
 //
-// A persistent grid walks the tiles.  What is left of the last, uneven wave (or
-// everything, with few tiles) is cut along the reduction into parts whose sums go
+// A persistent grid walks the tiles.  What is left of a product's last, uneven wave
+// (or everything, with few tiles) is cut along the reduction into parts whose sums go
 // to the workspace in fp32 and are added in order by head_join_kernel.  The number
 // of live tokens, and with it tiles and parts, is read on the device.
 //
@@ -41,7 +41,7 @@ constexpr int BOX = 32 * 128;                // an epilogue warp's staged box: 3
 constexpr int TMEM_COLS = 512;
 constexpr int GROUP_Z = 16, GROUP_DX = 8;    // row tiles that share a column tile's operand
 
-enum Mode { Z = 0, ZKEEP = 1, DX = 2, DW = 3 };
+enum Mode { Z = 0, ZKEEP = 1, GRAD = 2, DX = 3, DW = 4 };   // GRAD: both of the others
 
 template <bool PAIR> struct Shape {
     static constexpr int CTAS = PAIR ? 2 : 1;
@@ -53,11 +53,21 @@ template <bool PAIR> struct Shape {
     static constexpr int STAGES = PAIR ? 6 : 4;
 };
 
+// A product's tiles, their split, K blocks and units.
+struct Product {
+    Split s;
+    int MT, NT, kb;
+    __device__ __forceinline__ int units() const { return s.full + (s.tiles - s.full) * s.parts; }
+};
+struct Plan { Product x, w; };   // Z's or DX's; DW's
+
+template <bool B> struct Flag { static constexpr bool value = B; };
+
 template <int STAGES> struct Ctrl {
     uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
-    int tiles, full_tiles, parts, kbp, kb;
+    Plan plan;
 };
 
 template <bool PAIR> constexpr size_t smem_bytes() {
@@ -70,66 +80,86 @@ struct TcParams {
     int tile_n;              // columns of a tile (Z, single CTAs: any multiple of 16; else 256)
     int a_rows;              // rows of A's box
     int few;                 // losses alone of up to 128 rows: running statistics a CTA
-    HeadOut o;
-    float* part;             // [cap][TILE_M][BN] sums of cut tiles
-    int cap;
+    HeadOut dx, dW;          // out null: not wanted
+    float* part;             // [capx + capw][256][BN] sums of cut tiles, DX's first
+    int capx, capw;
     int units;               // CTAs or pairs of the launch
     uint64_t limit_ns;
     int withhold_unit, withhold_kb;   // test hook: see launch_tc
 };
 
-// Tiles and K blocks of a mode's product.
-template <int MODE, bool PAIR>
-__device__ __forceinline__ Split plan_tiles(const TcParams& p, int& kb) {
+// (called by whole warps)
+template <int MODE, bool PAIR> __device__ __forceinline__ Plan make_plan(const TcParams& p) {
     constexpr int TM = Shape<PAIR>::TILE_M;
     const HeadDev& h = p.h;
     const int n = head_rows(h);
-    const int MT = ((MODE == DW ? h.V : n) + TM - 1) / TM;
-    const int NT = ((MODE <= ZKEEP ? h.V : h.d) + p.tile_n - 1) / p.tile_n;
-    kb = ((MODE <= ZKEEP ? h.d : MODE == DX ? h.V : n) + BK - 1) / BK;
-    if (MODE <= ZKEEP) return Split{MT * NT, MT * NT, 1, kb};
-    // nothing to add: no tiles; without accumulation dW's zeros are written
-    if (MODE == DW && n == 0) return Split{p.o.accumulate ? 0 : MT * NT, MT * NT, 1, 0};
-    return split_tiles(MT * NT, kb, p.units, p.cap, 4, 4, 12, PAIR ? 8 : 16);
+    Plan q{};
+    q.x.MT = (n + TM - 1) / TM;
+    if (MODE <= ZKEEP) {
+        q.x.NT = (h.V + p.tile_n - 1) / p.tile_n;
+        q.x.kb = (h.d + BK - 1) / BK;
+        q.x.s = Split{q.x.MT * q.x.NT, q.x.MT * q.x.NT, 1, q.x.kb};
+        return q;
+    }
+    q.x.NT = q.w.NT = (h.d + BN - 1) / BN;
+    q.x.kb = (h.V + BK - 1) / BK;
+    q.w.MT = (h.V + TM - 1) / TM;
+    q.w.kb = (n + BK - 1) / BK;
+    if (p.dx.out) q.x.s = split_tiles(q.x.MT * q.x.NT, q.x.kb, p.units, p.capx, 4, 4, 12, 8);
+    if (p.dW.out) {
+        const int tiles = q.w.MT * q.w.NT;
+        if (n > 0) q.w.s = split_tiles(tiles, q.w.kb, p.units, p.capw, 4, 4, 12, 8);
+        else if (!p.dW.accumulate) q.w.s = Split{tiles, tiles, 1, 0};   // zeros
+    }
+    return q;
 }
 
-struct Tile { int mt, nt, kb0, nkb, slot; };   // slot: of a part, else -1
+struct Tile { int mt, nt, kb0, nkb, slot; bool dw; };   // slot: of a part, else -1
 
-template <int MODE, bool PAIR, typename C>
-__device__ __forceinline__ Tile get_tile(const C& c, const TcParams& p, int u) {
-    constexpr int TM = Shape<PAIR>::TILE_M;
+// Where tile i of a product lies: GROUP row tiles share a column tile's operand; DW's
+// columns follow each other (they share G's).
+template <int GROUP> __device__ __forceinline__ void place(const Product& a, int i, Tile& t) {
+    if (GROUP == 0) {
+        t.mt = i / a.NT;
+        t.nt = i % a.NT;
+        return;
+    }
+    constexpr int G = GROUP > 0 ? GROUP : 1;
+    const int g = i / (G * a.NT), l = i - g * G * a.NT, gm = min(G, a.MT - g * G);
+    t.mt = g * G + l % gm;
+    t.nt = l / gm;
+}
+
+template <int GROUP> __device__ __forceinline__ Tile product_tile(const Product& a, int u, int slot0) {
     Tile t;
-    int i = u;
     t.kb0 = 0;
-    t.nkb = c.kb;
+    t.nkb = a.kb;
     t.slot = -1;
-    if (MODE >= DX && u >= c.full_tiles && c.parts > 1) {
+    int i = u;
+    if (u >= a.s.full && a.s.parts > 1) {
         // part after part: the parts of the same K range run at the same time
-        const int rem = c.tiles - c.full_tiles, v = u - c.full_tiles;
-        const int part = v / rem;
-        i = c.full_tiles + v % rem;
-        t.kb0 = part * c.kbp;
-        t.nkb = min(c.kbp, c.kb - t.kb0);
-        t.slot = (i - c.full_tiles) * c.parts + part;
+        const int rem = a.s.tiles - a.s.full, v = u - a.s.full, part = v / rem;
+        i = a.s.full + v % rem;
+        t.kb0 = part * a.s.kbp;
+        t.nkb = min(a.s.kbp, a.kb - t.kb0);
+        t.slot = slot0 + (i - a.s.full) * a.s.parts + part;
     }
-    const int n = head_rows(p.h);
-    const int NT = ((MODE <= ZKEEP ? p.h.V : p.h.d) + p.tile_n - 1) / p.tile_n;
-    if (MODE == DW) {
-        t.mt = i / NT;
-        t.nt = i % NT;
-    } else {
-        constexpr int G = MODE == DX ? GROUP_DX : GROUP_Z;
-        const int MT = (n + TM - 1) / TM;
-        const int g = i / (G * NT), l = i - g * G * NT;
-        const int gm = min(G, MT - g * G);
-        t.mt = g * G + l % gm;
-        t.nt = l / gm;
-    }
+    place<GROUP>(a, i, t);
     return t;
 }
-template <int MODE, typename C>
-__device__ __forceinline__ int unit_count(const C& c) {
-    return c.full_tiles + (c.tiles - c.full_tiles) * c.parts;
+template <int MODE> __device__ __forceinline__ Tile get_tile(const Plan& q, const TcParams& p, int u) {
+    Tile t;
+    if (MODE <= ZKEEP) {
+        t = product_tile<GROUP_Z>(q.x, u, 0);
+        t.dw = false;
+        return t;
+    }
+    const int ux = MODE == DW ? 0 : q.x.units();
+    t.dw = MODE == DW || (MODE == GRAD && u >= ux);
+    const bool dw = t.dw;
+    t = dw ? product_tile<0>(q.w, u - ux, p.capx) : product_tile<GROUP_DX>(q.x, u, 0);
+    t.dw = dw;
+    return t;
 }
 
 template <typename C> __device__ __forceinline__ void raise_abort(C& c, const TcParams& p) {
@@ -244,10 +274,12 @@ __device__ __forceinline__ uint32_t bf2_bits(float a, float b) {
 template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     head_tc_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                   const __grid_constant__ CUtensorMap mapC, const __grid_constant__ CUtensorMap mapD,
                    const __grid_constant__ CUtensorMap mapO, const __grid_constant__ TcParams p) {
+    // Z: A xc, B W, O P.  GRAD: A G, B W (DX); C G, D xc, O dW (DW).
     using S = Shape<PAIR>;
     constexpr int STAGES = S::STAGES;
-    constexpr bool A_MN = MODE == DW, B_MN = MODE >= DX;
+    auto is_dw = [](const Tile& t) { return MODE == DW || (MODE == GRAD && t.dw); };
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -278,22 +310,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     wait_front();
     if (warp == 2) {
-        int kb;
-        const Split s = plan_tiles<MODE, PAIR>(p, kb);
-        if (lane == 0) {
-            c.tiles = s.tiles;
-            c.full_tiles = s.full < s.tiles ? s.full : s.tiles;
-            c.parts = s.parts;
-            c.kbp = s.kbp;
-            c.kb = kb;
-        }
+        const Plan q = make_plan<MODE, PAIR>(p);
+        if (lane == 0) c.plan = q;
     }
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = c.tmem_base;
-    const int units = unit_count<MODE>(c);
+    const Plan& plan = c.plan;
+    const int units = plan.x.units() + plan.w.units();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -301,48 +327,50 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int s = 0; s < STAGES; ++s) issued[s] = -1;
-            const uint32_t bytes =
-                (uint32_t)(A_MN ? S::A_BYTES : p.a_rows * BK * 2) +
-                (uint32_t)(B_MN || PAIR ? S::B_BYTES : p.tile_n * BK * 2);
+            // the stages' bytes: whole boxes, also where they lie past an edge
+            const uint32_t bytes = MODE >= GRAD || PAIR ? (uint32_t)S::STAGE
+                                                        : (uint32_t)((p.a_rows + p.tile_n) * BK * 2);
             for (int u = unit0; u < units && ok; u += nunits) {
-                const Tile t = get_tile<MODE, PAIR>(c, p, u);
+                const Tile t = get_tile<MODE>(plan, p, u);
                 const int m0 = t.mt * S::TILE_M + rank * BM;
                 const int n0 = t.nt * p.tile_n + rank * S::BN_CTA;
-                for (int k = 0; k < t.nkb; ++k) {
-                    if (leader && u == p.withhold_unit && k == p.withhold_kb) {
-                        ok = false;
-                        break;
-                    }
-                    if (!mbar_wait_bounded(smem_u32(&c.empty[stage]), phase ^ 1, p.limit_ns, &c.abort_flag)) {
-                        raise_abort(c, p);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sA = smem_u32(base + stage * S::STAGE), sB = sA + S::A_BYTES;
-                    const uint32_t fb = smem_u32(&c.full[stage]);
-                    const uint32_t bar = PAIR ? mapa(fb, 0) : fb;
-                    if (PAIR && !leader) arrive_expect_cluster(bar, bytes);
-                    else mbar_arrive_expect_tx(fb, bytes);
-                    auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
-                        if (PAIR) tma_load_pair(dst, m, bar, c0, c1);
-                        else tma_load_2d(dst, m, fb, c0, c1);
-                    };
-                    const int k0 = (t.kb0 + k) * BK;
-                    if (!A_MN) {
-                        load(sA, &mapA, k0, m0);
-                    } else {
+                auto fill = [&](auto dw) {
+                    constexpr bool DWT = decltype(dw)::value;
+                    for (int k = 0; k < t.nkb; ++k) {
+                        const int k0 = (t.kb0 + k) * BK;
+                        if (leader && u == p.withhold_unit && k == p.withhold_kb) return false;
+                        if (!mbar_wait_bounded(smem_u32(&c.empty[stage]), phase ^ 1, p.limit_ns, &c.abort_flag)) {
+                            raise_abort(c, p);
+                            return false;
+                        }
+                        const uint32_t sA = smem_u32(base + stage * S::STAGE), sB = sA + S::A_BYTES;
+                        const uint32_t fb = smem_u32(&c.full[stage]);
+                        const uint32_t bar = PAIR ? mapa(fb, 0) : fb;
+                        if (PAIR && !leader) arrive_expect_cluster(bar, bytes);
+                        else mbar_arrive_expect_tx(fb, bytes);
+                        auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
+                            if (PAIR) tma_load_pair(dst, m, bar, c0, c1);
+                            else tma_load_2d(dst, m, fb, c0, c1);
+                        };
+                        if (MODE < GRAD) {
+                            load(sA, &mapA, k0, m0);
+                            load(sB, &mapB, k0, n0);
+                        } else if (!DWT) {
+                            load(sA, &mapA, k0, m0);
 #pragma unroll
-                        for (int i = 0; i < BM / 64; ++i) load(sA + i * SLAB, &mapA, m0 + i * 64, k0);
-                    }
-                    if (!B_MN) {
-                        load(sB, &mapB, k0, n0);
-                    } else {
+                            for (int i = 0; i < S::BN_CTA / 64; ++i) load(sB + i * SLAB, &mapB, n0 + i * 64, k0);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < S::BN_CTA / 64; ++i) load(sB + i * SLAB, &mapB, n0 + i * 64, k0);
+                            for (int i = 0; i < BM / 64; ++i) load(sA + i * SLAB, &mapC, m0 + i * 64, k0);
+#pragma unroll
+                            for (int i = 0; i < S::BN_CTA / 64; ++i) load(sB + i * SLAB, &mapD, n0 + i * 64, k0);
+                        }
+                        issued[stage] = (int)phase;
+                        if (++stage == STAGES) { stage = 0; phase ^= 1; }
                     }
-                    issued[stage] = (int)phase;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
-                }
+                    return true;
+                };
+                ok = is_dw(t) ? fill(Flag<true>{}) : fill(Flag<false>{});
             }
             if (!ok && leader)   // the copies that this CTA's barriers still count
                 for (int s = 0; s < STAGES; ++s)
@@ -353,38 +381,46 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         if (leader) {
             if (lane == 0) {
-                const uint32_t idesc = idesc_bf16_f32(S::TILE_M, 0, A_MN, B_MN) | (uint32_t)(p.tile_n >> 3) << 17;
-                const uint32_t s0 = smem_u32(base);
-                // a stage or a K step moves only the start address (16-byte units)
-                const uint64_t ad0 = smem_desc_sw128(s0, A_MN ? SLAB : 16, 1024);
-                const uint64_t bd0 = smem_desc_sw128(s0 + S::A_BYTES, B_MN ? SLAB : 16, 1024);
-                constexpr uint32_t A_STEP = (A_MN ? 2048 : 32) >> 4, B_STEP = (B_MN ? 2048 : 32) >> 4;
+                // a stage or a K step moves only the start address (16-byte units);
+                // operands along K ("k") or across it ("n")
+                const uint32_t s0 = smem_u32(base), width = (uint32_t)(p.tile_n >> 3) << 17;
+                const uint64_t ak = smem_desc_sw128(s0, 16, 1024), an = smem_desc_sw128(s0, SLAB, 1024);
+                const uint64_t bk = smem_desc_sw128(s0 + S::A_BYTES, 16, 1024);
+                const uint64_t bn = smem_desc_sw128(s0 + S::A_BYTES, SLAB, 1024);
+                constexpr uint32_t STEP_K = 32 >> 4, STEP_N = 2048 >> 4;
                 int stage = 0, acc = 0;
                 uint32_t phase = 0, acc_phase = 0;
                 bool ok = true;
                 for (int u = unit0; u < units && ok; u += nunits) {
-                    const Tile t = get_tile<MODE, PAIR>(c, p, u);
+                    const Tile t = get_tile<MODE>(plan, p, u);
                     if (t.nkb == 0) continue;
                     if (!mbar_wait_bounded(smem_u32(&c.tempty[acc]), acc_phase ^ 1, p.limit_ns, &c.abort_flag)) {
                         raise_abort(c, p);
                         break;
                     }
                     tc_fence_after();
-                    for (int k = 0; k < t.nkb; ++k) {
-                        if (!mbar_wait_bounded(smem_u32(&c.full[stage]), phase, p.limit_ns, &c.abort_flag)) {
-                            raise_abort(c, p);
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t so = (uint64_t)(stage * (S::STAGE >> 4));
+                    // (a loop for each product: what is issued a stage is constant)
+                    auto issue = [&](auto dw) {
+                        constexpr bool a_n = decltype(dw)::value, b_n = MODE >= GRAD;
+                        const uint32_t idesc = idesc_bf16_f32(S::TILE_M, 0, a_n, b_n) | width;
+                        const uint64_t ad0 = a_n ? an : ak, bd0 = b_n ? bn : bk;
+                        for (int k = 0; k < t.nkb; ++k) {
+                            if (!mbar_wait_bounded(smem_u32(&c.full[stage]), phase, p.limit_ns, &c.abort_flag)) {
+                                raise_abort(c, p);
+                                return false;
+                            }
+                            tc_fence_after();
+                            const uint64_t so = (uint64_t)(stage * (S::STAGE >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            mma<PAIR>(tmem + acc * BN, ad0 + so + kk * A_STEP, bd0 + so + kk * B_STEP, idesc,
-                                      (k | kk) != 0);
-                        commit<PAIR>(smem_u32(&c.empty[stage]));
-                        if (++stage == STAGES) { stage = 0; phase ^= 1; }
-                    }
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                mma<PAIR>(tmem + acc * BN, ad0 + so + kk * (a_n ? STEP_N : STEP_K),
+                                          bd0 + so + kk * (b_n ? STEP_N : STEP_K), idesc, (k | kk) != 0);
+                            commit<PAIR>(smem_u32(&c.empty[stage]));
+                            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                        }
+                        return true;
+                    };
+                    ok = is_dw(t) ? issue(Flag<true>{}) : issue(Flag<false>{});
                     if (!ok) break;
                     commit<PAIR>(smem_u32(&c.tfull[acc]));
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
@@ -400,19 +436,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int ew = warp - 2, q = warp & 3, half = ew >> 2;
         uint8_t* box = boxes + ew * BOX;
         const int n = head_rows(h);
-        const float scale = MODE >= DX ? head_scale(h) : 1.f;
+        const float scale = MODE >= GRAD ? head_scale(h) : 1.f;
         // a few-row call's tiles all have the same rows: their statistics run on
         float few_m = -INFINITY, few_s = 0.f;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int u = unit0; u < units; u += nunits) {
-            const Tile t = get_tile<MODE, PAIR>(c, p, u);
+            const Tile t = get_tile<MODE>(plan, p, u);
+            const bool dw = is_dw(t);
             const int r0 = t.mt * S::TILE_M + rank * BM + q * 32, r = r0 + lane;
             const int col0 = t.nt * p.tile_n + half * 128;   // of the warp's columns
             const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + half * 128);
             // what the epilogue reads of the row, in front of the wait
             int tok = 0, e0 = 0, e1 = 0, tgt = -1;
-            if (MODE != DW && r < n) tok = head_token(h, r);
+            if (!dw && r < n) tok = head_token(h, r);
             if (MODE <= ZKEEP && r < n) {
                 if (h.target) {
                     const int64_t y = h.target[tok];
@@ -547,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             } else {
-                const int rows = (MODE == DW ? h.V : n) - r0;      // valid rows of the warp's 32
+                const int rows = (dw ? h.V : n) - r0;      // valid rows of the warp's 32
 #pragma unroll 1
                 for (int ch = 0; ch < 4; ++ch) {
                     const int col = col0 + ch * 32;
@@ -573,7 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (rows <= 0) break;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] *= scale;
-                    if (MODE == DW && p.o.f32) {
+                    if (dw && p.dW.f32) {
                         if (lane == 0) bulk_wait_read();
                         __syncwarp();
 #pragma unroll
@@ -583,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            if (p.o.accumulate) add_box(&mapO, smem_u32(box), col, r0);
+                            if (p.dW.accumulate) add_box(&mapO, smem_u32(box), col, r0);
                             else store_box(&mapO, smem_u32(box), col, r0);
                             bulk_commit();
                         }
@@ -592,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     // bf16: 64 columns make a box
                     const int part = (ch & 1) * 4;
                     if (part == 0) {
-                        if (MODE == DW && lane == 0) bulk_wait_read();
+                        if (lane == 0) bulk_wait_read();
                         __syncwarp();
                     }
 #pragma unroll
@@ -602,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                        bf2_bits(v[8 * j + 4], v[8 * j + 5]), bf2_bits(v[8 * j + 6], v[8 * j + 7]));
                     if (part == 0 && col + 32 < h.d) continue;
                     const int cb = col - part * 8;   // first column of the box
-                    if (MODE == DW) {
+                    if (dw) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -617,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const int rr = i * 4 + (lane >> 3), j = lane & 7;
                             const int to = __shfl_sync(0xffffffffu, tok, rr);
                             if (rr < rows && cb + j * 8 < h.d)
-                                *reinterpret_cast<uint4*>((__nv_bfloat16*)p.o.out + (int64_t)to * h.d + cb + j * 8) =
+                                *reinterpret_cast<uint4*>((__nv_bfloat16*)p.dx.out + (int64_t)to * h.d + cb + j * 8) =
                                     *reinterpret_cast<const uint4*>(box + box_at(rr, j));
                         }
                         __syncwarp();
@@ -641,31 +678,34 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-// The parts of cut tiles, added in order.
-template <int MODE, bool PAIR>
-__global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ TcParams p) {
-    constexpr int TM = Shape<PAIR>::TILE_M;
-    __shared__ Split ss;
+// The parts of cut tiles, added in order: blocks of kJoinRows rows of a tile; the
+// first `nx` tiles are DX's.
+__global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ TcParams p, int nx) {
+    constexpr int TM = 2 * BM;
+    __shared__ Plan plan;
     __shared__ float4 buf[kJoinRows][256];
     wait_front();
+    const HeadDev& h = p.h;
+    const bool dw = (int)blockIdx.x >= nx;
+    const int i = dw ? blockIdx.x - nx : blockIdx.x;   // tile behind the whole ones
+    const int M = dw ? h.V : head_rows(h);
+    if (i >= (M + TM - 1) / TM * ((h.d + BN - 1) / BN) % p.units) return;
     if (threadIdx.x < 32) {
-        int kb;
-        const Split s = plan_tiles<MODE, PAIR>(p, kb);
-        if (threadIdx.x == 0) ss = s;
+        const Plan q = make_plan<GRAD, true>(p);
+        if (threadIdx.x == 0) plan = q;
     }
     __syncthreads();
-    const HeadDev& h = p.h;
-    const int i = blockIdx.x;                       // tile behind the whole ones
-    if (ss.parts <= 1 || ss.full + i >= ss.tiles) return;
-    struct { int tiles, full_tiles, parts, kbp, kb; } c{ss.tiles, ss.full, ss.parts, ss.kbp, 1};
-    const Tile t = get_tile<MODE, PAIR>(c, p, ss.full + i);
-    const int M = MODE == DW ? h.V : head_rows(h);
+    const Product& a = dw ? plan.w : plan.x;
+    if (a.s.parts <= 1 || a.s.full + i >= a.s.tiles) return;
+    Tile t;
+    if (dw) place<0>(a, a.s.full + i, t);
+    else place<GROUP_DX>(a, a.s.full + i, t);
     const float scale = head_scale(h);
     const int rl = blockIdx.y * kJoinRows, r0 = t.mt * TM + rl, rows = M - r0;
     if (rows <= 0) return;
     float4 sums[kJoinRows];
-    const int cl = join_rows<BN>(p.part + ((int64_t)i * ss.parts * TM + rl) * BN, (int64_t)TM * BN, ss.parts, rows, buf,
-                                 sums);
+    const int64_t slot = (dw ? p.capx : 0) + (int64_t)i * a.s.parts;
+    const int cl = join_rows<BN>(p.part + (slot * TM + rl) * BN, (int64_t)TM * BN, a.s.parts, rows, buf, sums);
     const int col = t.nt * BN + cl;
     if (cl < 0 || col >= h.d) return;
 #pragma unroll
@@ -676,16 +716,17 @@ __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ 
         s.y *= scale;
         s.z *= scale;
         s.w *= scale;
-        const int64_t at = (int64_t)(MODE == DX ? head_token(h, r0 + r) : r0 + r) * h.d + col;
-        if (MODE == DW && p.o.f32) {
-            float4* o = reinterpret_cast<float4*>((float*)p.o.out + at);
-            if (p.o.accumulate) {
+        const int64_t at = (int64_t)(dw ? r0 + r : head_token(h, r0 + r)) * h.d + col;
+        if (dw && p.dW.f32) {
+            float4* o = reinterpret_cast<float4*>((float*)p.dW.out + at);
+            if (p.dW.accumulate) {
                 const float4 b = *o;
                 s = make_float4(s.x + b.x, s.y + b.y, s.z + b.z, s.w + b.w);
             }
             *o = s;
         } else {
-            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o.out + at) = make_uint2(bf2_bits(s.x, s.y), bf2_bits(s.z, s.w));
+            *reinterpret_cast<uint2*>((__nv_bfloat16*)(dw ? p.dW.out : p.dx.out) + at) =
+                make_uint2(bf2_bits(s.x, s.y), bf2_bits(s.z, s.w));
         }
     }
 }
@@ -757,7 +798,7 @@ template <int MODE, bool PAIR> cudaError_t resident(int* units) {
     return cudaSuccess;
 }
 
-// Test hook MOE_DEBUG_HEAD_WITHHOLD=mode:unit:kb (0 Z, 2 DX, 3 DW): that unit's
+// Test hook MOE_DEBUG_HEAD_WITHHOLD=mode:unit:kb (0 Z, 2 DX or DW): that unit's
 // producer issues nothing from K block kb on, so that the waits on it run out.
 void withhold_hook(int mode, TcParams& p) {
     p.withhold_unit = p.withhold_kb = -1;
@@ -769,43 +810,34 @@ void withhold_hook(int mode, TcParams& p) {
 }
 
 template <int MODE, bool PAIR>
-cudaError_t launch_tc(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, TcParams& p,
-                      int64_t tiles, cudaStream_t st) {
-    auto kern = head_tc_kernel<MODE, PAIR>;
+cudaError_t launch_tc(const CUtensorMap (&m)[5], TcParams& p, int64_t tiles, cudaStream_t st) {
     int units = 0;
     cudaError_t e = resident<MODE, PAIR>(&units);
     if (e != cudaSuccess) return e;
-    // (tiles that are cut need every unit)
+    // (GRAD's tiles are cut for every unit)
     if (MODE <= ZKEEP && tiles < units) units = (int)(tiles > 0 ? tiles : 1);
     p.units = units;
     p.limit_ns = wait_limit_ns();
-    withhold_hook(MODE == ZKEEP ? Z : MODE, p);
-    e = launch_early(kern, dim3((unsigned)(units * Shape<PAIR>::CTAS)), THREADS, smem_bytes<PAIR>(),
-                     Shape<PAIR>::CTAS, st, a, b, o, p);
-    if constexpr (MODE >= DX) {
-        if (e != cudaSuccess || p.cap == 0) return e;
-        // tiles: of all rows, where that is known to be less than a wave
-        const int64_t rem = tiles < units ? tiles : units;
-        const int64_t M = MODE == DW ? p.h.V : p.h.n_live ? p.h.rows : p.h.T;
-        const int rows = M < Shape<PAIR>::TILE_M ? (int)M : Shape<PAIR>::TILE_M;
-        e = launch_early(head_join_kernel<MODE, PAIR>, dim3((unsigned)rem, (rows + kJoinRows - 1) / kJoinRows), 256, 0,
-                         1, st, p);
-    }
-    return e;
+    withhold_hook(MODE <= ZKEEP ? Z : GRAD, p);
+    return launch_early(head_tc_kernel<MODE, PAIR>, dim3((unsigned)(units * Shape<PAIR>::CTAS)), THREADS,
+                        smem_bytes<PAIR>(), Shape<PAIR>::CTAS, st, m[0], m[1], m[2], m[3], m[4], p);
 }
 
 inline int64_t tiles_of(int64_t m, int tm, int64_t n, int tn) { return (m + tm - 1) / tm * ((n + tn - 1) / tn); }
 
-inline size_t tile_bytes(bool single) { return (size_t)(single ? BM : 2 * BM) * BN * 4; }
+constexpr size_t kTileBytes = (size_t)2 * BM * BN * 4;
+
+int64_t parts_dx(int64_t rows, int V, int d) {
+    return (int64_t)split_bound(tiles_of(rows, 2 * BM, d, BN), (V + BK - 1) / BK, device_sm_count() / 2, 4);
+}
+int64_t parts_dw(int64_t rows, int V, int d) {
+    return (int64_t)split_bound(tiles_of(V, 2 * BM, d, BN), (rows + BK - 1) / BK, device_sm_count() / 2, 4);
+}
 
 }  // namespace
 
-size_t head_part_bytes(int64_t rows, int V, int d, bool single) {
-    const int sms = device_sm_count();
-    const size_t a = split_bound(tiles_of(rows, single ? BM : 2 * BM, d, BN), (V + BK - 1) / BK,
-                                 sms / (single ? 1 : 2), 4) * tile_bytes(single);
-    const size_t b = split_bound(tiles_of(V, 2 * BM, d, BN), (rows + BK - 1) / BK, sms / 2, 4) * tile_bytes(false);
-    return a > b ? a : b;
+size_t head_part_bytes(int64_t rows, int V, int d) {
+    return (size_t)(parts_dx(rows, V, d) + parts_dw(rows, V, d)) * kTileBytes;
 }
 
 // Columns of a tile where W's bytes bound: about equal tiles for whole waves of CTAs.
@@ -825,52 +857,66 @@ cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool
                            cudaStream_t st) {
     TcParams p{};
     p.h = h;
-    CUtensorMap a, b, o;
+    CUtensorMap m[5];
     const int64_t xrows = single && !h.n_live ? h.T : h.rows;
     p.few = single && !keep;
     p.tile_n = p.few ? head_few_tile(h.V) : BN;
     p.a_rows = single ? (int)((xrows < BM ? xrows : BM) + 7) / 8 * 8 : BM;
-    if (!make_map(&a, xc, h.d, xrows, h.d, p.a_rows, kBf16) ||
-        !make_map(&b, W, h.d, h.V, h.d, single ? p.tile_n : BM, kBf16))
+    if (!make_map(&m[0], xc, h.d, xrows, h.d, p.a_rows, kBf16) ||
+        !make_map(&m[1], W, h.d, h.V, h.d, single ? p.tile_n : BM, kBf16))
         return cudaErrorInvalidValue;
-    o = a;
-    if (keep && !make_map(&o, h.P, h.Vp, h.srows, h.Vp, 32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
+    m[2] = m[3] = m[4] = m[0];
+    if (keep && !make_map(&m[4], h.P, h.Vp, h.srows, h.Vp, 32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
         return cudaErrorInvalidValue;
     const int64_t tiles = tiles_of(single ? BM : h.rows, single ? BM : 2 * BM, h.V, p.tile_n);
-    if (single) return keep ? launch_tc<ZKEEP, false>(a, b, o, p, tiles, st) : launch_tc<Z, false>(a, b, o, p, tiles, st);
-    return keep ? launch_tc<ZKEEP, true>(a, b, o, p, tiles, st) : launch_tc<Z, true>(a, b, o, p, tiles, st);
+    if (single) return keep ? launch_tc<ZKEEP, false>(m, p, tiles, st) : launch_tc<Z, false>(m, p, tiles, st);
+    return keep ? launch_tc<ZKEEP, true>(m, p, tiles, st) : launch_tc<Z, true>(m, p, tiles, st);
 }
 
-cudaError_t launch_head_tc_dx(const HeadDev& h, const void* W, const HeadOut& out, float* part, size_t part_bytes,
-                              bool single, cudaStream_t st) {
+cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
+                                const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st) {
     TcParams p{};
     p.h = h;
-    p.o = out;
+    p.dx = dx;
+    p.dW = dW;
     p.tile_n = BN;
     p.a_rows = BM;
     p.part = part;
-    p.cap = (int)(part_bytes / tile_bytes(single));
-    CUtensorMap a, b;
-    if (!make_map(&a, h.P, h.V, h.srows, h.Vp, BM, kBf16) || !make_map(&b, W, h.d, h.V, h.d, 64, kBf16))
+    p.capx = (int)parts_dx(part_rows, h.V, h.d);
+    p.capw = (int)parts_dw(part_rows, h.V, h.d);
+    // rows that are never made need not be read
+    const int64_t made = ((h.T - h.p0 < h.rows ? h.T - h.p0 : h.rows) + 63) / 64 * 64;
+    CUtensorMap m[5];
+    if (!make_map(&m[0], h.P, h.V, made, h.Vp, BM, kBf16) || !make_map(&m[1], W, h.d, h.V, h.d, 64, kBf16) ||
+        !make_map(&m[2], h.P, h.V, made, h.Vp, 64, kBf16) || !make_map(&m[3], xc, h.d, made, h.d, 64, kBf16))
         return cudaErrorInvalidValue;
-    const int64_t tiles = tiles_of(h.rows, single ? BM : 2 * BM, h.d, BN);
-    return single ? launch_tc<DX, false>(a, b, a, p, tiles, st) : launch_tc<DX, true>(a, b, a, p, tiles, st);
-}
-
-cudaError_t launch_head_tc_dw(const HeadDev& h, const void* xc, const HeadOut& out, float* part, size_t part_bytes,
-                              cudaStream_t st) {
-    TcParams p{};
-    p.h = h;
-    p.o = out;
-    p.tile_n = BN;
-    p.a_rows = BM;
-    p.part = part;
-    p.cap = (int)(part_bytes / tile_bytes(false));
-    CUtensorMap a, b, o;
-    if (!make_map(&a, h.P, h.V, h.srows, h.Vp, 64, kBf16) || !make_map(&b, xc, h.d, h.rows, h.d, 64, kBf16) ||
-        !make_map(&o, out.out, h.d, h.V, h.d, 32, out.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kBf16))
+    m[4] = m[0];
+    if (dW.out && !make_map(&m[4], dW.out, h.d, h.V, h.d, 32, dW.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kBf16))
         return cudaErrorInvalidValue;
-    return launch_tc<DW, true>(a, b, o, p, tiles_of(h.V, 2 * BM, h.d, BN), st);
+    // at most: DX's tiles of all rows, where that is less than a wave; DW's are known
+    const int64_t tx = dx.out ? tiles_of(made, 2 * BM, h.d, BN) : 0, tw = dW.out ? tiles_of(h.V, 2 * BM, h.d, BN) : 0;
+    // Short products in one launch (33 tokens of 32000 entries, d = 2048: 3 us less);
+    // long ones in two, each of which begins with all pairs in step, so that tiles that
+    // share an operand find it in L2 (4096 tokens of 131072 entries, d = 4096: 3% less)
+    const bool apart = tx * ((h.V + BK - 1) / BK) + tw * (made / BK) > 512 * (int64_t)(device_sm_count() / 2);
+    cudaError_t e;
+    if (apart && tx && tw) {
+        p.dW.out = nullptr;
+        e = launch_tc<DX, true>(m, p, 0, st);
+        if (e != cudaSuccess) return e;
+        p.dW = dW;
+        p.dx.out = nullptr;
+        e = launch_tc<DW, true>(m, p, 0, st);
+        p.dx = dx;
+    } else {
+        e = launch_tc<GRAD, true>(m, p, 0, st);
+    }
+    if (e != cudaSuccess) return e;
+    const int nx = p.capx ? (int)(tx < p.units ? tx : p.units) : 0, nw = p.capw ? (int)(tw % p.units) : 0;
+    if (nx + nw == 0) return cudaSuccess;
+    const int64_t most = nw || made > 2 * BM ? 2 * BM : made;
+    return launch_early(head_join_kernel, dim3((unsigned)(nx + nw), (unsigned)((most + kJoinRows - 1) / kJoinRows)),
+                        256, 0, 1, st, p, nx);
 }
 
 }  // namespace moe
