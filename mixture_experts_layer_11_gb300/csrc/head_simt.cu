@@ -444,9 +444,13 @@ cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bo
             default: return launch_few<8>(p, st);
         }
     }
-    const int64_t blocks = (int64_t)((h.rows + 63) / 64) * ((h.V + 127) / 128);
+    const int64_t rows = h.T - h.p0 < h.rows ? h.T - h.p0 : h.rows, cols = (h.V + 127) / 128;
+    // tiles of 16 rows where those of 64 would leave SMs idle
+    if ((rows + 63) / 64 * cols < device_sm_count())
+        return launch_early(keep ? head_simt_z_kernel<4, 32, 4, 4, true, 4, 1> : head_simt_z_kernel<4, 32, 4, 4, false, 4, 1>,
+                            dim3((unsigned)((rows + 15) / 16 * cols)), 128, 0, 1, st, p);
     return launch_early(keep ? head_simt_z_kernel<8, 16, 8, 8, true, STAGES, 2> : head_simt_z_kernel<8, 16, 8, 8, false, STAGES, 2>,
-                        dim3((unsigned)blocks), 128, 0, 1, st, p);
+                        dim3((unsigned)((rows + 63) / 64 * cols)), 128, 0, 1, st, p);
 }
 
 cudaError_t launch_head_simt_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
