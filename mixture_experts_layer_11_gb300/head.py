@@ -56,6 +56,8 @@ class HeadLoss:
         ops.one_device("HeadLoss", W, dW)
         V, d = W.shape
         dev = W.device
+        if not W.is_contiguous():
+            raise ops.MoEError("HeadLoss", ops.MOE_ERR_INVALID, "W is not contiguous")
         self.T, self.W, self.entries = T, W, entries
         self.head = ops.make_head(T, V, d, W.dtype, entries, piece)
         self.grad = None
@@ -75,13 +77,16 @@ class HeadLoss:
         self.lse = torch.empty(T, dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._device = self.loss.device.index
+        self._results = (self.loss, self.lse, self.dx, self.dW)
+        self._size = (T, d)
+        self._W = W.data_ptr()
+        self._losses = (self.loss.data_ptr(), self.lse.data_ptr())
         self._owned = (self.ws.data_ptr(), self.status.data_ptr())
 
     def score(self, x, target):
         """x [t,d] of W's type, t <= T; target [t] int64, below 0 for none.  Returns
         (loss, lse), fp32 [t]: loss = lse - logit of the target = -log p(target)."""
-        loss, lse, _, _ = self._call(x, target, None, 1.0, None)
-        return loss, lse
+        return self._call(x, target, None, 1.0, None)[:2]
 
     def cross_entropy(self, x, target, weight=None, scale: float = 1.0, mean: bool = False,
                       accumulate: bool = False):
@@ -125,32 +130,38 @@ class HeadLoss:
                                f"{name} on {t.device}, the head on cuda:{self._device}")
 
     def _call(self, x, idx, logits, temperature, grad):
-        if x.dim() != 2 or x.shape[1] != self.W.shape[1] or x.shape[0] > self.T:
-            raise ValueError(f"x is {tuple(x.shape)}, expected [t, {self.W.shape[1]}] with t <= {self.T}")
-        t = x.shape[0]
-        if idx.shape[0] != t or (logits is None and idx.dim() != 1):
-            raise ValueError(f"targets are {tuple(idx.shape)} for {t} tokens")
-        for name, tensor in (("x", x), ("targets", idx), ("logits", logits)):
-            if tensor is not None:
-                self._on_device(name, tensor)
+        size, d = x.shape, self._size[1]
+        if size != self._size and (len(size) != 2 or size[1] != d or size[0] > self.T):
+            raise ValueError(f"x is {tuple(size)}, expected [t, {d}] with t <= {self.T}")
+        t, lists = size[0], idx.shape
+        if lists[0] != t or (logits is None and len(lists) != 1):
+            raise ValueError(f"targets are {tuple(lists)} for {t} tokens")
+        self._on_device("x", x)
+        self._on_device("targets", idx)
         h = self.head
-        h.T, h.entries = t, 1 if logits is None else idx.shape[1]
-        loss, lse = self.loss[:t], self.lse[:t]
+        h.T = t
+        if logits is None:
+            h.entries = 1
+        else:
+            self._on_device("logits", logits)
+            h.entries = lists[1]
         if torch.cuda.current_device() == self._device:
-            self._launch(x, idx, logits, temperature, loss, lse, grad)
+            self._launch(x, idx, logits, temperature, grad)
         else:
             with torch.cuda.device(self._device):
-                self._launch(x, idx, logits, temperature, loss, lse, grad)
-        if grad is None:
-            return loss, lse, None, None
-        return loss, lse, None if self.dx is None else self.dx[:t], self.dW
+                self._launch(x, idx, logits, temperature, grad)
+        loss, lse, dx, dW = self._results
+        if t != self.T:
+            loss, lse = loss[:t], lse[:t]
+            dx = None if dx is None else dx[:t]
+        return (loss, lse, None, None) if grad is None else (loss, lse, dx, dW)
 
-    def _launch(self, x, idx, logits, temperature, loss, lse, grad):
+    def _launch(self, x, idx, logits, temperature, grad):
         stream = ops.raw_stream(self._device)
         if logits is None:
-            ops.moe_head_ce(self.head, x, self.W, idx, loss, lse, grad, *self._owned, stream=stream)
+            ops.moe_head_ce(self.head, x, self._W, idx, *self._losses, grad, *self._owned, stream=stream)
         else:
-            ops.moe_head_distill(self.head, x, self.W, idx, logits, temperature, loss, lse, grad,
+            ops.moe_head_distill(self.head, x, self._W, idx, logits, temperature, *self._losses, grad,
                                  *self._owned, stream=stream)
 
     def check_status(self):
