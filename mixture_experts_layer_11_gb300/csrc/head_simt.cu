@@ -38,10 +38,10 @@ template <int N> __device__ __forceinline__ void copies_wait() {
 // ([M][K]), kept as [ROWS][LDK]; else across it ([K][M]), kept as [BK][ROWS + 4].
 // Rows and columns past the edge are zero: only the vocabulary may end inside a group
 // of four, and G is zero from there to its row's end.
-template <bool KC, int ROWS, int NT>
+template <bool KC, int ROWS, int NT, int BK = 16>
 struct Loader {
-    static constexpr int LD = KC ? LDK : ROWS + 4;
-    static constexpr int SIZE = KC ? ROWS * LDK : BK * (ROWS + 4);
+    static constexpr int LD = KC ? (BK + 4) : ROWS + 4;
+    static constexpr int SIZE = KC ? ROWS * (BK + 4) : BK * (ROWS + 4);
     static constexpr int G = KC ? BK / 4 : ROWS / 4;       // groups of four in a row of memory
     static constexpr int N = ROWS * BK / 4, COPIES = (N + NT - 1) / NT, SKIP = NT / G;
     static_assert(NT % G == 0, "a thread's groups lie under one another");
@@ -97,12 +97,12 @@ struct SimtParams {
 //
 // TY x TX threads; thread (ty, tx) has rows ty + TY i and columns tx + TX j, so that
 // its 16-byte loads (rows of 80 bytes) meet no bank conflict.
-template <int TY, int TX, int TM, int TN, bool KEEP, int DEPTH, int BLOCKS>
+template <int TY, int TX, int TM, int TN, bool KEEP, int DEPTH, int BLOCKS, int BK = 16>
 __global__ void __launch_bounds__(TY * TX, BLOCKS)
     head_simt_z_kernel(const __grid_constant__ SimtParams p) {
     constexpr int ROWS = TY * TM, COLS = TX * TN, NT = TY * TX;
-    using LA = Loader<true, ROWS, NT>;
-    using LB = Loader<true, COLS, NT>;
+    using LA = Loader<true, ROWS, NT, BK>;
+    using LB = Loader<true, COLS, NT, BK>;
     __shared__ __align__(16) float smem[DEPTH][LA::SIZE + LB::SIZE];
     const HeadDev& h = p.h;
     const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
@@ -137,16 +137,16 @@ __global__ void __launch_bounds__(TY * TX, BLOCKS)
             lb.copy(smem[next] + LA::SIZE, (s + DEPTH - 1) * BK, h.d);
         }
         copies_commit();
-        const float* A = smem[cur] + ty * LDK;
-        const float* B = smem[cur] + LA::SIZE + tx * LDK;
+        const float* A = smem[cur] + ty * (BK + 4);
+        const float* B = smem[cur] + LA::SIZE + tx * (BK + 4);
 #pragma unroll
         for (int k = 0; k < BK; k += 4) {
             ulonglong2 a[TM];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(A + i * TY * LDK + k);
+            for (int i = 0; i < TM; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(A + i * TY * (BK + 4) + k);
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(B + j * TX * LDK + k);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(B + j * TX * (BK + 4) + k);
 #pragma unroll
                 for (int i = 0; i < TM; ++i) acc[i][j] = f2_fma(a[i].x, b.x, acc[i][j]);
 #pragma unroll
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(256) head_simt_join_kernel(const __grid_consta
 int simt_units() { return kBlocksPerSm * device_sm_count(); }
 
 template <int TM> cudaError_t launch_few(const SimtParams& p, cudaStream_t st) {
-    return launch_early(head_simt_z_kernel<8, 16, TM, 4, false, 4, 1>, dim3((unsigned)((p.h.V + 63) / 64)), 128, 0, 1, st, p);
+    return launch_early(head_simt_z_kernel<8, 16, TM, 4, false, 3, 1, 32>, dim3((unsigned)((p.h.V + 63) / 64)), 128, 0, 1, st, p);
 }
 
 int64_t tiles_of(int64_t m, int64_t n) { return (m + BM - 1) / BM * ((n + BN - 1) / BN); }
