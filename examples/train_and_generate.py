@@ -5,9 +5,14 @@ all five gradients clipped with ``GradClip``, a plain SGD step on fp32 master
 weights.  Serving: ``FewTokenPass`` on the trained bf16 weights, its decode step
 captured once in a CUDA graph and replayed for every new token.
 
-    python examples/train_and_generate.py [--steps 60] [--tokens 16]
+With --vocab N, a layer and a vocabulary head of N entries are then trained by
+distillation from a teacher's eight best tokens (``HeadLoss``, whose dx is the layer's
+dy), and the trained pair scores the teacher's best tokens.
+
+    python examples/train_and_generate.py [--steps 60] [--tokens 16] [--vocab 1000]
 """
 import argparse
+import math
 import os
 import sys
 
@@ -17,6 +22,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from mixture_experts_layer_11_gb300.decode import FewTokenPass  # noqa: E402
 from mixture_experts_layer_11_gb300.grads import GradClip  # noqa: E402
+from mixture_experts_layer_11_gb300.head import HeadLoss  # noqa: E402
 from mixture_experts_layer_11_gb300.layer import LayerPass  # noqa: E402
 
 T, D, F, E, K = 4096, 256, 512, 8, 2     # tokens a batch, widths, experts, experts a token
@@ -58,6 +64,45 @@ def train(steps, max_norm=1.0, rate=0.5):
     layer.check_status()
     clip.check_status()
     return params, [float(v) for v in losses]
+
+
+def train_tokens(steps, vocab, entries=8, max_norm=1.0, rate=0.5):
+    """Layer and head trained on a teacher's best tokens.  Returns the losses, and what
+    the last step worked on: (y, W, idx, logits) and its gradients (dx, dW)."""
+    teacher = [w.to(BF16) for w in weights(1)]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    teacher_head = torch.randn(vocab, D, generator=g, device="cuda").to(BF16)
+    master = weights(2) + [torch.randn(vocab, D, generator=g, device="cuda") * D ** -0.5]
+    params = [w.to(BF16) for w in master]
+    layer = LayerPass(T, D, F, E, K, BF16, renorm=1)
+    target = LayerPass(T, D, F, E, K, BF16, renorm=1)
+    W = params[5]
+    head = HeadLoss(T, W, entries=entries, dW=torch.empty(vocab, D, device="cuda"))
+    grads = [layer.dWg, layer.dW1, layer.db1, layer.dW2, layer.db2, head.dW]
+    clip = GradClip(grads)
+    losses, last = [], None
+    for step in range(steps):
+        x = torch.randn(T, D, device="cuda").to(BF16)
+        logits, idx = (target.forward(x, *teacher).float() @ teacher_head.float().T).topk(entries)
+        y = layer.forward(x, *params[:5])
+        loss, _, dx, dW = head.distill(y, idx, logits.contiguous(), temperature=2.0, mean=True)
+        losses.append(loss.mean())
+        if step == steps - 1:
+            last = [v.clone() for v in (y, W, idx, logits, dx, dW)]
+        layer.backward(dx, x, params[0], params[1], params[3])
+        clip.clip(max_norm)
+        for m, p, q in zip(master, params, grads):
+            m.sub_(q, alpha=rate)
+            p.copy_(m)
+        if step % 10 == 0 or step == steps - 1:
+            print(f"step {step:3d}  divergence from the teacher {losses[-1].item():.4f}")
+    scores = HeadLoss(T, W, backward=False)
+    score, _ = scores.score(layer.forward(x, *params[:5]), idx[:, 0].contiguous())
+    print(f"the teacher's best token: {score.mean().item():.3f} nats (even odds {math.log(vocab):.3f})")
+    for part in (layer, clip, head, scores):
+        part.check_status()
+    return [float(v) for v in losses], last[:4], last[4:]
 
 
 def generate(params, sequences, tokens):
@@ -104,12 +149,15 @@ def main(argv=None):
     a.add_argument("--steps", type=int, default=60)
     a.add_argument("--tokens", type=int, default=16)
     a.add_argument("--sequences", type=int, default=5)
+    a.add_argument("--vocab", type=int, default=0)
     a = a.parse_args(argv)
     torch.manual_seed(0)
     params, losses = train(a.steps)
     states = generate(params, a.sequences, a.tokens)
     off = check(params, states)
     print(f"{a.tokens} tokens for {a.sequences} sequences; decode and batch differ by {off:.1e} of the largest value")
+    if a.vocab:
+        train_tokens(a.steps, a.vocab)
     return losses, states, off
 
 

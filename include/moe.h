@@ -462,7 +462,8 @@ MOE_API moe_status moe_grad_clip(int n, const moe_grad* g, float max_norm, float
  * with an online log-sum-exp, whose logits are that training's largest buffer).
  * The logits are never kept: each product's tile of them goes straight into the
  * rows' running maxima and sums.  The gradients hold one 16-bit number (fp32: one
- * of 32 bits) a logit for `piece` tokens at a time.
+ * of 32 bits) a logit for `piece` tokens at a time.  Tokens without a target cost
+ * nothing: the others are gathered first.
  *
  * With z = x W^T / temperature, lse = log(sum_v exp(z_v)), p = exp(z - lse), a
  * token's loss and its gradient by the logits (before weight and scale) are
@@ -479,9 +480,12 @@ MOE_API moe_status moe_grad_clip(int n, const moe_grad* g, float max_norm, float
 #define MOE_HEAD_MAX_ENTRIES 128
 
 typedef struct {
-    int64_t T;        /* tokens of this call, 0 <= T < 2^31 */
-    int64_t piece;    /* tokens of which the gradients hold the probabilities at a time;
-                         rounded up to a multiple of 256; 0: as many as 2 GiB hold */
+    int64_t T;        /* tokens of this call, 0 <= T <= 2^30 */
+    int64_t piece;    /* live tokens of which the gradients hold the probabilities at a
+                         time (more tokens take several rounds, dW then summed in fp32);
+                         rounded up to a multiple of 256, at most 2^20; 0: as many as
+                         2 GiB hold, at most 65536.  Calls without gradients keep no
+                         probabilities and choose for themselves */
     int32_t V;        /* vocabulary, 1 <= V <= 2^22 */
     int32_t d;        /* width, d % 8 == 0, d <= 2^20 */
     int32_t entries;  /* moe_head_distill: entries of a token's list, 1 to
@@ -509,17 +513,21 @@ MOE_API size_t moe_head_workspace_size(const moe_head* h, const moe_head_grad* g
 
 /*   x       [T,d] dtype       W  [V,d] dtype
  *   target  [T] int64
+ *   (outputs and ws overlap neither the inputs nor one another)
  *   loss    [T] fp32, out     lse  [T] fp32, out, or NULL
  *   g       gradients, or NULL: the losses alone (scores of given tokens)
  *   ws      workspace (contents need no initialisation, garbage after)
  *   dev_status  MOE_ERR_NONFINITE on a loss that is not finite, MOE_ERR_INVALID
  *           on an index of V or more, MOE_ERR_TIMEOUT
+ * The launches may overlap the end of the kernel before them in the stream; they touch
+ * memory only when that kernel has completed.
  * Precision: products are summed in fp32 (bf16: by the tensor cores, which drop
- * what is below the accumulator's last bit), softmax statistics, losses and the
- * entries' own logits are fp32.  bf16 gradients: weight[t] G is rounded to bf16
- * once, before the products with W and x; scale and the mean are applied to their
- * fp32 sums; dx and dW are rounded once.  Deterministic: the same inputs give the
- * same bits on the same GPU.  Can be captured in a CUDA graph. */
+ * what is below the accumulator's last bit: 4e-6 of a logit at d = 4096, 2e-6 of a
+ * loss), softmax statistics, losses and the entries' own logits are fp32.  bf16
+ * gradients: weight[t] G is rounded to bf16 once, before the products with W and x;
+ * scale and the mean are applied to their fp32 sums; dx and dW are rounded once.
+ * Deterministic: the same inputs give the same bits on the same GPU.  Can be
+ * captured in a CUDA graph. */
 MOE_API moe_status moe_head_ce(const moe_head* h, const void* x, const void* W,
                                const int64_t* target, float* loss, float* lse,
                                const moe_head_grad* g, void* ws, int32_t* dev_status,
@@ -527,7 +535,7 @@ MOE_API moe_status moe_head_ce(const moe_head* h, const void* x, const void* W,
 
 /*   idx     [T,entries] int64, logits [T,entries] fp32: the teacher's entries, in
  *           any order
- *   temperature  > 0, finite
+ *   temperature  1e-4 to 1e4
  *   others as moe_head_ce (lse is that of z = x W^T / temperature). */
 MOE_API moe_status moe_head_distill(const moe_head* h, const void* x, const void* W,
                                     const int64_t* idx, const float* logits,

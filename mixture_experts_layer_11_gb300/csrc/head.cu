@@ -24,6 +24,9 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kPieceBytes = int64_t(2) << 30;   // of E, where the caller sets no piece
+constexpr int64_t kStatBytes = int64_t(256) << 20;  // of statistics, in a call without gradients
+constexpr int64_t kPieceRows = 65536;               // ... and the most rows, for the gathered x
+constexpr int64_t kMostPiece = 1 << 20;             // that a caller may ask for
 
 inline int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
@@ -55,13 +58,13 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
         if (few > most_stat) most_stat = few;
     }
     p.Tp = up(h.T > 0 ? h.T : 1, kHeadRows);
-    int64_t piece = p.Tp;
-    if (p.backward) {
-        int64_t most = h.piece;
-        if (most == 0) most = kPieceBytes / (p.Vp * p.esize) / kHeadRows * kHeadRows;
-        most = up(most > 0 ? most : 1, kHeadRows);
-        if (most < piece) piece = most;
-    }
+    int64_t most = p.backward ? kPieceBytes / (p.Vp * p.esize) : kStatBytes / (8 * (int64_t)p.nblk);
+    if (most > kPieceRows) most = kPieceRows;
+    if (p.backward && h.piece > 0) most = h.piece < kMostPiece ? h.piece : kMostPiece;
+    // whole tiles: rounded up where asked for, down where the workspace is bounded
+    most = p.backward && h.piece > 0 ? up(most, kHeadRows) : most / kHeadRows * kHeadRows;
+    if (most < kHeadRows) most = kHeadRows;
+    const int64_t piece = most < p.Tp ? most : p.Tp;
     p.piece = piece;
     p.pieces = h.T > 0 ? (h.T + piece - 1) / piece : 0;
     p.wide = p.backward && p.pieces > 1 && g->dW_dtype != MOE_F32;
@@ -86,7 +89,7 @@ Plan make_plan(const moe_head& h, const moe_head_grad* g, bool distill) {
     if (!p.few) {
         p.live = take((size_t)p.Tp * 4);
         p.pos = take((size_t)p.Tp * 4);
-        p.xc = take((size_t)p.Tp * h.d * p.esize);
+        p.xc = take((size_t)piece * h.d * p.esize);
     }
     if (p.backward) {
         p.P = take((size_t)piece * p.Vp * p.esize);
@@ -218,9 +221,10 @@ __global__ void __launch_bounds__(1024) head_scan_kernel(const HeadDev h, int* p
     if (threadIdx.x == 0) *n_live = base;
 }
 
-// A warp a token: a live one's x goes to its row of xc, an ignored one's outputs are
-// zeros; and row i of xc behind the live ones, up to the end of a K block of 64 (of
-// the tensor cores' products, where it meets zeros of G), is zeros.
+// A warp a token: the x of one that is live in this piece goes to its row of xc, an
+// ignored one's outputs are zeros (written with the first piece); and row i of xc behind
+// the live ones, up to the end of a K block of 64 (of the tensor cores' products, where
+// it meets zeros of G), is zeros.
 template <bool COUNT>
 __global__ void __launch_bounds__(1024)
     head_gather_kernel(const HeadDev h, const uint4* x, uint4* xc, uint4* dx, int vecs, int* live, const int* pos,
@@ -258,8 +262,9 @@ __global__ void __launch_bounds__(1024)
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if (on) {
         const uint4* src = x + (int64_t)t * vecs;
-        uint4* dst = xc + (int64_t)row * vecs;
-        int v = lane;
+        const int to = row - h.p0;
+        uint4* dst = xc + (int64_t)to * vecs;
+        int v = to >= 0 && to < h.rows ? lane : vecs;
         for (; v + 96 < vecs; v += 128) {
             const uint4 a = src[v], b = src[v + 32], c = src[v + 64], d = src[v + 96];
             dst[v] = a;
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(1024)
         }
         for (; v < vecs; v += 32) dst[v] = src[v];
         if (lane == 0) live[row] = t;
-    } else if (t < h.T) {
+    } else if (t < h.T && h.p0 == 0) {
         if (lane == 0) {
             if (h.target && h.target[t] >= h.V) report(h.status, MOE_ERR_INVALID);
             h.loss[t] = 0.f;
@@ -278,8 +283,8 @@ __global__ void __launch_bounds__(1024)
         if (dx)
             for (int v = lane; v < vecs; v += 32) dx[(int64_t)t * vecs + v] = zero;
     }
-    if (t >= n && t < (n + 63) / 64 * 64)
-        for (int v = lane; v < vecs; v += 32) xc[(int64_t)t * vecs + v] = zero;
+    if (t >= n && t < (n + 63) / 64 * 64 && t >= h.p0 && t < h.p0 + h.rows)
+        for (int v = lane; v < vecs; v += 32) xc[(int64_t)(t - h.p0) * vecs + v] = zero;
 }
 
 // ---- statistics to losses ----------------------------------------------------------
@@ -541,27 +546,24 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         e = launch_early(head_entries_kernel, dim3((unsigned)((s.T + 3) / 4)), 128, 0, 1, st, h, c.idx, c.teacher,
                          1.f / c.temperature, (int*)(ws + p.sidx), (float*)(ws + p.q), (float*)(ws + p.lq),
                          (int*)(ws + p.ent), ws + p.start);
-    const void* xc = c.x;
+    const void* xc = p.few ? c.x : ws + p.xc;
     float* part = (float*)(ws + p.part);
-    if (!p.few) {
-        int *live = (int*)(ws + p.live), *pos = (int*)(ws + p.pos), *n_live = (int*)(ws + p.ctl);
-        const bool count = s.T <= kScanTokens;
-        if (e == cudaSuccess && !count)
-            e = launch_early(head_scan_kernel, dim3(1), 1024, 0, 1, st, h, pos, n_live);
-        if (e == cudaSuccess)
-            e = launch_early(count ? head_gather_kernel<true> : head_gather_kernel<false>, dim3((unsigned)(p.Tp / 32)),
-                             1024, 0, 1, st, h, (const uint4*)c.x, (uint4*)(ws + p.xc),
-                             want_dx ? (uint4*)g->dx : (uint4*)nullptr, s.d * p.esize / 16, live, (const int*)pos,
-                             n_live);
-        xc = ws + p.xc;
-    }
+    int *live = (int*)(ws + p.live), *pos = (int*)(ws + p.pos), *n_live = (int*)(ws + p.ctl);
+    const bool count = s.T <= kScanTokens;
+    if (e == cudaSuccess && !p.few && !count)
+        e = launch_early(head_scan_kernel, dim3(1), 1024, 0, 1, st, h, pos, n_live);
     for (int64_t i = 0; i < p.pieces && e == cudaSuccess; ++i) {
         h.p0 = (int)(i * p.piece);
         const int64_t left = p.Tp - h.p0;
         h.rows = (int)(left < p.piece ? left : p.piece);
-        const uint8_t* xp = (const uint8_t*)xc + (size_t)h.p0 * s.d * p.esize;
-        e = bf16 ? launch_head_tc(h, xp, c.W, p.backward, p.single, st)
-                 : launch_head_simt(h, xp, c.W, p.backward, st);
+        if (!p.few)
+            e = launch_early(count ? head_gather_kernel<true> : head_gather_kernel<false>, dim3((unsigned)(p.Tp / 32)),
+                             1024, 0, 1, st, h, (const uint4*)c.x, (uint4*)(ws + p.xc),
+                             want_dx ? (uint4*)g->dx : (uint4*)nullptr, s.d * p.esize / 16, live, (const int*)pos,
+                             n_live);
+        if (e != cudaSuccess) break;
+        e = bf16 ? launch_head_tc(h, xc, c.W, p.backward, p.single, st)
+                 : launch_head_simt(h, xc, c.W, p.backward, st);
         if (e != cudaSuccess) break;
         // rows that there may be: no more than tokens
         const int64_t rows = s.T - h.p0 < h.rows ? s.T - h.p0 : h.rows;
@@ -575,8 +577,8 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         const HeadOut dW{want_dW ? p.wide ? (void*)(ws + p.dW32) : g->dW : nullptr,
                          p.wide || g->dW_dtype == MOE_F32, g->accumulate || i > 0};
         if (!want_dx && !want_dW) continue;
-        e = bf16 ? launch_head_tc_grad(h, xp, c.W, dx, dW, part, p.piece, st)
-                 : launch_head_simt_grad(h, xp, c.W, dx, dW, part, p.piece, st);
+        e = bf16 ? launch_head_tc_grad(h, xc, c.W, dx, dW, part, p.piece, st)
+                 : launch_head_simt_grad(h, xc, c.W, dx, dW, part, p.piece, st);
     }
     if (e == cudaSuccess && want_dW && p.wide) {
         const int64_t n4 = (int64_t)s.V * s.d / 4;

@@ -708,7 +708,7 @@ moe_status check_head(const moe_head* h, const moe_head_grad* g) {
             return MOE_ERR_INVALID;
         if (g->accumulate && g->dW_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
     }
-    if (h->T >= (int64_t(1) << 31) || h->piece >= (int64_t(1) << 31) || h->V > (1 << 22) ||
+    if (h->T > (int64_t(1) << 30) || h->piece > (int64_t(1) << 30) || h->V > (1 << 22) ||
         h->d % 8 || h->d > (1 << 20) || h->entries > MOE_HEAD_MAX_ENTRIES)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
@@ -720,7 +720,7 @@ moe_status run_head(const moe_head* h, const void* x, const void* W, const int64
     moe_status r = check_head(h, g);
     if (r != MOE_OK) return r;
     if (!distill && h->entries != 1) return MOE_ERR_INVALID;
-    if (!(temperature > 0.f) || temperature > 3.0e38f) return MOE_ERR_INVALID;
+    if (!(temperature >= 1e-4f && temperature <= 1e4f)) return MOE_ERR_INVALID;
     if (g && (!ok_opt(g->dW) || !ok_opt(g->dx) || ((uintptr_t)g->weight & 3u)))
         return MOE_ERR_INVALID;
     if (h->T > 0) {

@@ -29,7 +29,7 @@ class HeadLoss:
     ops.HEAD_MAX_ENTRIES); backward False for scores alone.  With backward: want_dx,
     want_dW which gradients; dW [V,d] the buffer for the head's (W's type or fp32),
     None for one of W's type made here; piece the tokens whose probabilities are held
-    at a time (0: as many as 2 GiB hold).
+    at a time (0: as many as 2 GiB hold); more are worked on in rounds.
 
     The results, the workspace and the status word are this object's, on the head's
     device, whichever is current: calls of one object run in order on one stream

@@ -43,6 +43,21 @@ def test_cross_entropy(T, d, V, dtype):
     head.check_status()
 
 
+@pytest.mark.parametrize("kind", ["ce", "distill"])
+@pytest.mark.parametrize("T,d,V", [(4100, 2056, 10007), (4096, 1024, 20000), (5000, 520, 30001)])
+def test_long_calls(T, d, V, kind):
+    # whole waves of tiles and cut ones behind them; the two gradients in a launch each
+    x, W, target = make(T, d, V, BF16, seed=d)
+    head = HeadLoss(T, W, entries=5)
+    if kind == "ce":
+        target[::9] = -1
+        check(head, x, target, mean=True)
+    else:
+        idx, logits = make_entries(T, 5, V, target, distinct=False)
+        check(head, x, idx=idx, logits=logits, temperature=1.5, weight=torch.rand(T, device="cuda"), mean=True)
+    head.check_status()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,d,V", SIZES + [(200, 64, 40000)])
 def test_score(T, d, V, dtype):

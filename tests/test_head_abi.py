@@ -43,8 +43,8 @@ def test_refuses_invalid_shapes(lib, bad):
     assert ops.moe_head_workspace_size(h) == 0
 
 
-@pytest.mark.parametrize("bad", [dict(T=1 << 31), dict(V=(1 << 22) + 1), dict(d=12), dict(d=(1 << 20) + 8),
-                                 dict(entries=129), dict(piece=1 << 31)])
+@pytest.mark.parametrize("bad", [dict(T=(1 << 30) + 1), dict(V=(1 << 22) + 1), dict(d=12), dict(d=(1 << 20) + 8),
+                                 dict(entries=129), dict(piece=(1 << 30) + 1)])
 def test_refuses_unsupported_shapes(lib, bad):
     h = _head(**bad)
     assert _distill(lib, h) == ops.MOE_ERR_UNSUPPORTED
@@ -62,7 +62,8 @@ def test_refuses_bad_pointers(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [dict(logits=None), dict(logits=18), dict(temperature=0.0), dict(temperature=-1.0),
-                                 dict(temperature=float("nan")), dict(temperature=float("inf"))])
+                                 dict(temperature=float("nan")), dict(temperature=float("inf")),
+                                 dict(temperature=9e-5), dict(temperature=1.1e4)])
 def test_distill_refuses(lib, bad):
     assert _distill(lib, _head(entries=4), **bad) == ops.MOE_ERR_INVALID
 
