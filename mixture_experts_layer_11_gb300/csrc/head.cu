@@ -417,10 +417,12 @@ template <> struct Pair<float> {
 constexpr int kGradWarps = 8, kGradCols = 2048;
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kGradWarps) head_gradient_kernel(const __grid_constant__ HeadDev h) {
+__global__ void __launch_bounds__(32 * kGradWarps)
+    head_gradient_kernel(const __grid_constant__ HeadDev h, const __grid_constant__ SplitRule rule) {
     constexpr int N = Pair<T>::N, LOADS = 8, PART = 32 * N * LOADS;   // columns of 8 loads
     wait_front();
     const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && threadIdx.x < 32) make_splits(h, rule);   // for the products that come next
     const int n = head_rows(h), nck = (h.Vp + kGradCols - 1) / kGradCols;
     const int64_t it = (int64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5);
     // the last rows first: L2 still holds some of them
@@ -530,6 +532,7 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
     h.stats = (float2*)(ws + p.stats);
     if (g) h.row = (float4*)(ws + p.row);
     h.P = ws + p.P;
+    h.splits = (Split*)(ws + p.ctl + 64);
     h.c = kLog2e / c.temperature;
     h.loss_scale = c.temperature * c.temperature;
     if (g) {
@@ -569,16 +572,23 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
         const int64_t rows = s.T - h.p0 < h.rows ? s.T - h.p0 : h.rows;
         e = launch_early(head_loss_kernel, dim3((unsigned)((rows + 31) / 32)), 1024, 0, 1, st, h);
         if (!p.backward || e != cudaSuccess) continue;
-        const int64_t items = up(rows, 64) * (up(p.Vp, kGradCols) / kGradCols);
-        e = launch_early(bf16 ? head_gradient_kernel<__nv_bfloat16> : head_gradient_kernel<float>,
-                         dim3((unsigned)((items + kGradWarps - 1) / kGradWarps)), 32 * kGradWarps, 0, 1, st, h);
-        if (e != cudaSuccess) break;
+        if (!want_dx && !want_dW) continue;
         const HeadOut dx{want_dx ? g->dx : nullptr, !bf16, 0};
         const HeadOut dW{want_dW ? p.wide ? (void*)(ws + p.dW32) : g->dW : nullptr,
                          p.wide || g->dW_dtype == MOE_F32, g->accumulate || i > 0};
-        if (!want_dx && !want_dW) continue;
-        e = bf16 ? launch_head_tc_grad(h, xc, c.W, dx, dW, part, p.piece, st)
-                 : launch_head_simt_grad(h, xc, c.W, dx, dW, part, p.piece, st);
+        SplitRule rule;
+        if (bf16) e = head_tc_rule(p.piece, s.V, s.d, &rule);
+        else rule = head_simt_rule(p.piece, s.V, s.d);
+        if (e != cudaSuccess) break;
+        rule.dx = want_dx;
+        rule.dw = want_dW;
+        rule.accumulate = dW.accumulate;
+        const int64_t items = up(rows, 64) * (up(p.Vp, kGradCols) / kGradCols);
+        e = launch_early(bf16 ? head_gradient_kernel<__nv_bfloat16> : head_gradient_kernel<float>,
+                         dim3((unsigned)((items + kGradWarps - 1) / kGradWarps)), 32 * kGradWarps, 0, 1, st, h, rule);
+        if (e != cudaSuccess) break;
+        e = bf16 ? launch_head_tc_grad(h, xc, c.W, dx, dW, part, rule, st)
+                 : launch_head_simt_grad(h, xc, c.W, dx, dW, part, rule, st);
     }
     if (e == cudaSuccess && want_dW && p.wide) {
         const int64_t n4 = (int64_t)s.V * s.d / 4;

@@ -21,60 +21,13 @@ constexpr float kHeadShift = 15.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The kernels' view of one call, and of the piece of its rows that is being
-// worked on.  Row r of a piece is row p0 + r of the live (not ignored) tokens, in
-// their order; token live[p0 + r].
-struct HeadDev {
-    int T, V, d, K;
-    int Vp;                  // row length of P (V rounded up to 64)
-    int nblk;                // blocks of kHeadBlock entries
-    int nstat;               // rows of stats: nblk, or for few rows two a CTA (fp32: blocks of 64)
-    int p0, rows;            // first live row of the piece, its most rows
-    int srows;               // row length of stats (rows, rounded up to kHeadRows)
-    const int* n_live;       // null: rows are tokens, all T of them
-    const int* live;
-    const int64_t* target;   // targets [T], or null:
-    const int* sidx;         // the teacher's indices, ascending [T][K] ...
-    const float* q;          // ... their weights, and the logarithms of these
-    const float* lq;
-    const int* ent;          // entries present [T]
-    const uint8_t* start;    // first entry of each block [T][nblk]
-    float* lz;               // logits of the targets / entries [T][K]
-    float2* stats;           // [nstat][srows]: largest exponent - kHeadShift, sum (0: no entries)
-    float4* row;             // [srows], with gradients: log2 of the sum of exponentials,
-                             // weight, and the target with its value of G (CE)
-    void* P;                 // [rows][Vp]: exponentials, then gradients by the logits
-    const float* weight;
-    float c;                 // log2(e) / temperature
-    float loss_scale;        // temperature^2
-    float grad_scale;        // scale * temperature
-    int mean;
-    float* loss;
-    float* lse;
-    int32_t* status;
-};
-
-__device__ __forceinline__ int head_live(const HeadDev& h) { return h.n_live ? *h.n_live : h.T; }
-__device__ __forceinline__ int head_rows(const HeadDev& h) {
-    const int n = head_live(h) - h.p0;
-    return n < 0 ? 0 : n < h.rows ? n : h.rows;
-}
-__device__ __forceinline__ int head_token(const HeadDev& h, int r) {
-    return h.live ? h.live[h.p0 + r] : h.p0 + r;
-}
-__device__ __forceinline__ float head_scale(const HeadDev& h) {
-    if (!h.mean) return h.grad_scale;
-    const int n = head_live(h);
-    return h.grad_scale / (float)(n > 0 ? n : 1);
-}
-
 // How the tiles of a reduction over kb blocks of 64 run on `units` CTAs (or pairs, or
 // blocks at once): tiles before `full` whole, the uneven last wave behind them (or
 // all, where there are few) in `parts` parts of kbp blocks, whose sums a second
 // launch joins in order.  Costs, in a block's time: a part's blocks and `each` more
 // (its start and end), and for cutting `once`, the joining launch, with a block for
-// `bytes` parts written and read.  Parts have at least `least` blocks.  The same
-// everywhere; called by whole warps.
+// `bytes` parts written and read.  Parts have at least `least` blocks.  Called by a
+// whole warp.
 struct Split { int tiles, full, parts, kbp; };
 constexpr int kMostParts = 64;
 __device__ __forceinline__ Split split_tiles(int tiles, int kb, int units, int cap, int least, int each,
@@ -100,6 +53,61 @@ __device__ __forceinline__ Split split_tiles(int tiles, int kb, int units, int c
     }
     return s;
 }
+// What the two products of a call need for that: tiles of tm x tn, reductions counted
+// in blocks of 64.
+struct SplitRule {
+    int tm, tn, units, capx, capw, least, each, once, bytes;
+    int dx, dw, accumulate;   // wanted; dW added to
+};
+
+// The kernels' view of one call, and of the piece of its rows that is being
+// worked on.  Row r of a piece is row p0 + r of the live (not ignored) tokens, in
+// their order; token live[p0 + r].
+struct HeadDev {
+    int T, V, d, K;
+    int Vp;                  // row length of P (V rounded up to 64)
+    int nblk;                // blocks of kHeadBlock entries
+    int nstat;               // rows of stats: nblk, or for few rows two a CTA (fp32: blocks of 64)
+    int p0, rows;            // first live row of the piece, its most rows
+    int srows;               // row length of stats (rows, rounded up to kHeadRows)
+    const int* n_live;       // null: rows are tokens, all T of them
+    const int* live;
+    const int64_t* target;   // targets [T], or null:
+    const int* sidx;         // the teacher's indices, ascending [T][K] ...
+    const float* q;          // ... their weights, and the logarithms of these
+    const float* lq;
+    const int* ent;          // entries present [T]
+    const uint8_t* start;    // first entry of each block [T][nblk]
+    float* lz;               // logits of the targets / entries [T][K]
+    float2* stats;           // [nstat][srows]: largest exponent - kHeadShift, sum (0: no entries)
+    float4* row;             // [srows], with gradients: log2 of the sum of exponentials,
+                             // weight, and the target with its value of G (CE)
+    Split* splits;           // DX's, DW's (head_gradient_kernel works them out)
+    void* P;                 // [rows][Vp]: exponentials, then gradients by the logits
+    const float* weight;
+    float c;                 // log2(e) / temperature
+    float loss_scale;        // temperature^2
+    float grad_scale;        // scale * temperature
+    int mean;
+    float* loss;
+    float* lse;
+    int32_t* status;
+};
+
+__device__ __forceinline__ int head_live(const HeadDev& h) { return h.n_live ? *h.n_live : h.T; }
+__device__ __forceinline__ int head_rows(const HeadDev& h) {
+    const int n = head_live(h) - h.p0;
+    return n < 0 ? 0 : n < h.rows ? n : h.rows;
+}
+__device__ __forceinline__ int head_token(const HeadDev& h, int r) {
+    return h.live ? h.live[h.p0 + r] : h.p0 + r;
+}
+__device__ __forceinline__ float head_scale(const HeadDev& h) {
+    if (!h.mean) return h.grad_scale;
+    const int n = head_live(h);
+    return h.grad_scale / (float)(n > 0 ? n : 1);
+}
+
 // The most parts that the workspace holds: four waves, and no more than split_tiles
 // can ask for.  No less for more tiles or blocks.
 inline size_t split_bound(int64_t tiles, int64_t kb, int units, int least) {
@@ -150,6 +158,20 @@ __device__ __forceinline__ int join_rows(const float* src, int64_t stride, int p
     return q * 4;
 }
 
+// (a whole warp)
+__device__ __forceinline__ void make_splits(const HeadDev& h, const SplitRule& p) {
+    const int n = head_rows(h), NT = (h.d + p.tn - 1) / p.tn;
+    const int kx = (h.V + 63) / 64, kw = (n + 63) / 64, tw = (h.V + p.tm - 1) / p.tm * NT;
+    Split x{0, 0, 1, kx}, w{0, 0, 1, kw};
+    if (p.dx) x = split_tiles((n + p.tm - 1) / p.tm * NT, kx, p.units, p.capx, p.least, p.each, p.once, p.bytes);
+    if (p.dw && n > 0) w = split_tiles(tw, kw, p.units, p.capw, p.least, p.each, p.once, p.bytes);
+    else if (p.dw && !p.accumulate) w = Split{tw, tw, 1, 0};   // no rows: zeros
+    if ((threadIdx.x & 31) == 0) {
+        h.splits[0] = x;
+        h.splits[1] = w;
+    }
+}
+
 // Kernels here begin while the one in front of them ends: nothing is touched before
 // wait_front(), and nothing is read through the non-coherent path.
 __device__ __forceinline__ void wait_front() {
@@ -188,12 +210,13 @@ struct HeadOut {
 };
 cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st);
 cudaError_t launch_head_simt_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
-                                  const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st);
+                                  const HeadOut& dW, float* part, const SplitRule& rule, cudaStream_t st);
+SplitRule head_simt_rule(int64_t rows, int V, int d);
 size_t head_simt_part_bytes(int64_t rows, int V, int d);
 int head_simt_few_rows();
 
 // The same on the tensor cores, bf16 (single: up to 128 rows; xc may be x itself,
-// where rows are tokens).  part_rows: those that head_part_bytes was asked for.
+// where rows are tokens).  rows of a rule: those that head_part_bytes was asked for.
 constexpr int kHeadFewRows = 128;
 int head_few_tile(int V);
 int head_few_stats(int V);   // rows of statistics of a few-row call
@@ -201,6 +224,7 @@ size_t head_part_bytes(int64_t rows, int V, int d);
 cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool keep, bool single,
                            cudaStream_t st);
 cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
-                                const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st);
+                                const HeadOut& dW, float* part, const SplitRule& rule, cudaStream_t st);
+cudaError_t head_tc_rule(int64_t rows, int V, int d, SplitRule* rule);
 
 }  // namespace moe

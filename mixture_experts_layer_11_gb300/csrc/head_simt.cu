@@ -19,7 +19,7 @@ namespace {
 constexpr int BM = 64, BN = 128, BK = 16, THREADS = 128;
 constexpr int STAGES = 3;
 constexpr int LDK = BK + 4;                 // a row of K values in shared memory
-constexpr int KB = 64;                      // K values the reduction is cut in multiples of
+constexpr int KB = 64;                      // K values the reduction is cut in multiples of (SplitRule)
 constexpr int kBlocksPerSm = 4;
 
 enum Mode { Z = 0, ZKEEP = 1, DX = 2, DW = 3 };
@@ -88,8 +88,7 @@ struct SimtParams {
     const float* xc;
     const float* W;
     float* part;             // [capx + capw][BM][BN] sums of cut tiles, DX's first
-    int capx, capw;
-    int units;               // blocks that run at once
+    int capx;
     int ux;                  // blocks of DX's (the first)
 };
 
@@ -212,11 +211,6 @@ template <int MODE> __device__ __forceinline__ Shape<MODE> shape_of(const HeadDe
     s.NT = (s.N + BN - 1) / BN;
     return s;
 }
-template <int MODE> __device__ __forceinline__ Split plan_tiles(const SimtParams& p, const Shape<MODE>& s) {
-    const int tiles = s.MT * s.NT, kb = (s.K + KB - 1) / KB;
-    if (MODE == DW && s.K == 0) return Split{p.dW.accumulate ? 0 : tiles, tiles, 1, 0};
-    return split_tiles(tiles, kb, p.units, MODE == DX ? p.capx : p.capw, 1, 1, 1, 1024);
-}
 // Tiles that share the larger operand follow each other: W's columns over the rows
 // (DX), G's columns over the width (DW).
 template <int MODE> __device__ __forceinline__ void tile_at(const Shape<MODE>& s, int i, int& mt, int& nt) {
@@ -245,7 +239,7 @@ template <int MODE> struct Loaders {
 };
 
 template <int MODE>
-__device__ __forceinline__ void product(const SimtParams& p, int u, float* smem_raw, Split& plan) {
+__device__ __forceinline__ void product(const SimtParams& p, int u, float* smem_raw) {
     using LA = typename Loaders<MODE>::A;
     using LB = typename Loaders<MODE>::B;
     float(*smem)[Loaders<MODE>::SIZE] = reinterpret_cast<float(*)[Loaders<MODE>::SIZE]>(smem_raw);
@@ -253,12 +247,8 @@ __device__ __forceinline__ void product(const SimtParams& p, int u, float* smem_
     const HeadOut& o = MODE == DX ? p.dx : p.dW;
     const Shape<MODE> sh = shape_of<MODE>(h);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    if (tid < 32) {
-        const Split s = plan_tiles<MODE>(p, sh);
-        if (tid == 0) plan = s;
-    }
-    __syncthreads();
-    const int rem = plan.tiles - min(plan.full, plan.tiles);
+    const Split plan = h.splits[MODE == DW];
+    const int rem = plan.tiles - plan.full;
     int tile = u, k0 = 0, k1 = sh.K, slot = -1;
     if (plan.parts > 1 && u >= plan.full) {
         const int v = u - plan.full, part = v / rem;
@@ -360,24 +350,18 @@ __device__ __forceinline__ void product(const SimtParams& p, int u, float* smem_
 __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_grad_kernel(const __grid_constant__ SimtParams p) {
     constexpr int SIZE = Loaders<DX>::SIZE > Loaders<DW>::SIZE ? Loaders<DX>::SIZE : Loaders<DW>::SIZE;
     __shared__ __align__(16) float smem[STAGES * SIZE];
-    __shared__ Split plan;
     wait_front();
-    if ((int)blockIdx.x < p.ux) product<DX>(p, blockIdx.x, smem, plan);
-    else product<DW>(p, blockIdx.x - p.ux, smem, plan);
+    if ((int)blockIdx.x < p.ux) product<DX>(p, blockIdx.x, smem);
+    else product<DW>(p, blockIdx.x - p.ux, smem);
 }
 
 // The parts of cut tiles, added in order.
 template <int MODE>
-__device__ __forceinline__ void join(const SimtParams& p, int i, Split& plan, float4 (*buf)[256]) {
+__device__ __forceinline__ void join(const SimtParams& p, int i, float4 (*buf)[256]) {
     const HeadDev& h = p.h;
     const HeadOut& o = MODE == DX ? p.dx : p.dW;
     const Shape<MODE> sh = shape_of<MODE>(h);
-    if (i >= sh.MT * sh.NT % p.units) return;
-    if (threadIdx.x < 32) {
-        const Split s = plan_tiles<MODE>(p, sh);
-        if (threadIdx.x == 0) plan = s;
-    }
-    __syncthreads();
+    const Split plan = h.splits[MODE == DW];
     if (plan.parts <= 1 || plan.full + i >= plan.tiles) return;
     int mt, nt;
     tile_at<MODE>(sh, plan.full + i, mt, nt);
@@ -396,11 +380,10 @@ __device__ __forceinline__ void join(const SimtParams& p, int i, Split& plan, fl
     }
 }
 __global__ void __launch_bounds__(256) head_simt_join_kernel(const __grid_constant__ SimtParams p, int nx) {
-    __shared__ Split plan;
     __shared__ float4 buf[kJoinRows][256];
     wait_front();
-    if ((int)blockIdx.x < nx) join<DX>(p, blockIdx.x, plan, buf);
-    else join<DW>(p, blockIdx.x - nx, plan, buf);
+    if ((int)blockIdx.x < nx) join<DX>(p, blockIdx.x, buf);
+    else join<DW>(p, blockIdx.x - nx, buf);
 }
 
 int simt_units() { return kBlocksPerSm * device_sm_count(); }
@@ -426,6 +409,10 @@ int head_simt_few_rows() { return 64; }
 
 size_t head_simt_part_bytes(int64_t rows, int V, int d) {
     return (size_t)(parts_dx(rows, V, d) + parts_dw(rows, V, d)) * BM * BN * 4;
+}
+
+SplitRule head_simt_rule(int64_t rows, int V, int d) {
+    return SplitRule{BM, BN, simt_units(), (int)parts_dx(rows, V, d), (int)parts_dw(rows, V, d), 1, 1, 1, 1024, 0, 0, 0};
 }
 
 cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bool keep, cudaStream_t st) {
@@ -454,7 +441,7 @@ cudaError_t launch_head_simt(const HeadDev& h, const void* xc, const void* W, bo
 }
 
 cudaError_t launch_head_simt_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
-                                  const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st) {
+                                  const HeadOut& dW, float* part, const SplitRule& rule, cudaStream_t st) {
     SimtParams p{};
     p.h = h;
     p.dx = dx;
@@ -462,19 +449,17 @@ cudaError_t launch_head_simt_grad(const HeadDev& h, const void* xc, const void* 
     p.xc = (const float*)xc;
     p.W = (const float*)W;
     p.part = part;
-    p.capx = (int)parts_dx(part_rows, h.V, h.d);
-    p.capw = (int)parts_dw(part_rows, h.V, h.d);
-    p.units = simt_units();
+    p.capx = rule.capx;
     // (fewer live rows leave fewer tiles, but perhaps more parts: at most what the
     // workspace holds)
     const int64_t rows = h.T - h.p0 < h.rows ? h.T - h.p0 : h.rows;
     const int64_t tx = dx.out ? tiles_of(rows, h.d) : 0, tw = dW.out ? tiles_of(h.V, h.d) : 0;
-    p.ux = (int)(tx ? tx + p.capx : 0);
-    const int64_t blocks = p.ux + (tw ? tw + p.capw : 0);
+    p.ux = (int)(tx ? tx + rule.capx : 0);
+    const int64_t blocks = p.ux + (tw ? tw + rule.capw : 0);
     if (blocks == 0) return cudaSuccess;
     cudaError_t e = launch_early(head_simt_grad_kernel, dim3((unsigned)blocks), THREADS, 0, 1, st, p);
     if (e != cudaSuccess) return e;
-    const int nx = p.capx ? (int)(tx < p.units ? tx : p.units) : 0, nw = p.capw ? (int)(tw % p.units) : 0;
+    const int nx = rule.capx ? (int)(tx < rule.units ? tx : rule.units) : 0, nw = rule.capw ? (int)(tw % rule.units) : 0;
     if (nx + nw == 0) return cudaSuccess;
     const int most = nw || rows > BM ? BM : (int)rows;
     return launch_early(head_simt_join_kernel, dim3((unsigned)(nx + nw), (unsigned)((most + kJoinRows - 1) / kJoinRows)),

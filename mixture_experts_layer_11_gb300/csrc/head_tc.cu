@@ -53,10 +53,29 @@ template <bool PAIR> struct Shape {
     static constexpr int STAGES = PAIR ? 6 : 4;
 };
 
+// Quotients by one divisor, without the hundreds of cycles of a division: they are
+// worked out by one thread or warp between two tiles.
+struct Quotient {
+    unsigned d, m;   // divisor, floor(2^32 / d) (2^32 - 1 for 1)
+    __device__ __forceinline__ void set(int by) {
+        d = (unsigned)(by > 0 ? by : 1);
+        m = d == 1 ? 0xffffffffu : (unsigned)(0x100000000ull / d);
+    }
+    __device__ __forceinline__ int of(int n, int& rest) const {
+        unsigned q = __umulhi((unsigned)n, m), r = (unsigned)n - q * d;
+        // at most two too small
+        if (r >= d) ++q, r -= d;
+        if (r >= d) ++q, r -= d;
+        rest = (int)r;
+        return (int)q;
+    }
+};
+
 // A product's tiles, their split, K blocks and units.
 struct Product {
     Split s;
     int MT, NT, kb;
+    Quotient group, rest;   // of tiles; of cut ones
     __device__ __forceinline__ int units() const { return s.full + (s.tiles - s.full) * s.parts; }
 };
 struct Plan { Product x, w; };   // Z's or DX's; DW's
@@ -82,13 +101,12 @@ struct TcParams {
     int few;                 // losses alone of up to 128 rows: running statistics a CTA
     HeadOut dx, dW;          // out null: not wanted
     float* part;             // [capx + capw][256][BN] sums of cut tiles, DX's first
-    int capx, capw;
-    int units;               // CTAs or pairs of the launch
+    int capx;
+    int units;               // pairs of GRAD's launches
     uint64_t limit_ns;
     int withhold_unit, withhold_kb;   // test hook: see launch_tc
 };
 
-// (called by whole warps)
 template <int MODE, bool PAIR> __device__ __forceinline__ Plan make_plan(const TcParams& p) {
     constexpr int TM = Shape<PAIR>::TILE_M;
     const HeadDev& h = p.h;
@@ -99,18 +117,20 @@ template <int MODE, bool PAIR> __device__ __forceinline__ Plan make_plan(const T
         q.x.NT = (h.V + p.tile_n - 1) / p.tile_n;
         q.x.kb = (h.d + BK - 1) / BK;
         q.x.s = Split{q.x.MT * q.x.NT, q.x.MT * q.x.NT, 1, q.x.kb};
+        q.x.group.set(GROUP_Z * q.x.NT);
         return q;
     }
     q.x.NT = q.w.NT = (h.d + BN - 1) / BN;
     q.x.kb = (h.V + BK - 1) / BK;
     q.w.MT = (h.V + TM - 1) / TM;
     q.w.kb = (n + BK - 1) / BK;
-    if (p.dx.out) q.x.s = split_tiles(q.x.MT * q.x.NT, q.x.kb, p.units, p.capx, 4, 4, 12, 8);
-    if (p.dW.out) {
-        const int tiles = q.w.MT * q.w.NT;
-        if (n > 0) q.w.s = split_tiles(tiles, q.w.kb, p.units, p.capw, 4, 4, 12, 8);
-        else if (!p.dW.accumulate) q.w.s = Split{tiles, tiles, 1, 0};   // zeros
-    }
+    q.x.s = q.w.s = Split{0, 0, 1, 0};
+    if (p.dx.out) q.x.s = h.splits[0];
+    if (p.dW.out) q.w.s = h.splits[1];
+    q.x.group.set(GROUP_DX * q.x.NT);
+    q.w.group.set(q.w.NT);
+    q.x.rest.set(q.x.s.tiles - q.x.s.full);
+    q.w.rest.set(q.w.s.tiles - q.w.s.full);
     return q;
 }
 
@@ -120,14 +140,19 @@ struct Tile { int mt, nt, kb0, nkb, slot; bool dw; };   // slot: of a part, else
 // columns follow each other (they share G's).
 template <int GROUP> __device__ __forceinline__ void place(const Product& a, int i, Tile& t) {
     if (GROUP == 0) {
-        t.mt = i / a.NT;
-        t.nt = i % a.NT;
+        t.mt = a.group.of(i, t.nt);
         return;
     }
     constexpr int G = GROUP > 0 ? GROUP : 1;
-    const int g = i / (G * a.NT), l = i - g * G * a.NT, gm = min(G, a.MT - g * G);
-    t.mt = g * G + l % gm;
-    t.nt = l / gm;
+    int l;
+    const int g = a.group.of(i, l), gm = min(G, a.MT - g * G);
+    if (gm == G) {
+        t.mt = g * G + l % G;
+        t.nt = l / G;
+    } else {
+        t.mt = g * G + l % gm;
+        t.nt = l / gm;
+    }
 }
 
 template <int GROUP> __device__ __forceinline__ Tile product_tile(const Product& a, int u, int slot0) {
@@ -138,11 +163,12 @@ template <int GROUP> __device__ __forceinline__ Tile product_tile(const Product&
     int i = u;
     if (u >= a.s.full && a.s.parts > 1) {
         // part after part: the parts of the same K range run at the same time
-        const int rem = a.s.tiles - a.s.full, v = u - a.s.full, part = v / rem;
-        i = a.s.full + v % rem;
+        int left;
+        const int part = a.rest.of(u - a.s.full, left);
+        i = a.s.full + left;
         t.kb0 = part * a.s.kbp;
         t.nkb = min(a.s.kbp, a.kb - t.kb0);
-        t.slot = slot0 + (i - a.s.full) * a.s.parts + part;
+        t.slot = slot0 + left * a.s.parts + part;
     }
     place<GROUP>(a, i, t);
     return t;
@@ -259,6 +285,27 @@ __device__ __forceinline__ void bulk_wait_read() {
 }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Loads 32 columns of the thread's TMEM lane; the values are there after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+// (the values go through, so that none is used before)
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[4][32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[i][j]));
+}
+
 // 16-byte chunk j of row r of a staged box (the TMA's 128-byte swizzle)
 __device__ __forceinline__ uint32_t box_at(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
@@ -309,10 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tma_prefetch_map(&mapB);
     }
     wait_front();
-    if (warp == 2) {
-        const Plan q = make_plan<MODE, PAIR>(p);
-        if (lane == 0) c.plan = q;
-    }
+    if (threadIdx.x == 64) c.plan = make_plan<MODE, PAIR>(p);
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync();
@@ -501,7 +545,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float v[4][32];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch)
-                    if (ch * 32 < left) tmem_ld32(trow + ch * 32, v[ch]);
+                    if (ch * 32 < left) tmem_ld32_start(trow + ch * 32, v[ch]);
+                tmem_ld_wait(v);
                 release();
                 if (left < 128) {
 #pragma unroll
@@ -682,21 +727,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 // first `nx` tiles are DX's.
 __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ TcParams p, int nx) {
     constexpr int TM = 2 * BM;
-    __shared__ Plan plan;
     __shared__ float4 buf[kJoinRows][256];
     wait_front();
     const HeadDev& h = p.h;
     const bool dw = (int)blockIdx.x >= nx;
     const int i = dw ? blockIdx.x - nx : blockIdx.x;   // tile behind the whole ones
-    const int M = dw ? h.V : head_rows(h);
-    if (i >= (M + TM - 1) / TM * ((h.d + BN - 1) / BN) % p.units) return;
-    if (threadIdx.x < 32) {
-        const Plan q = make_plan<GRAD, true>(p);
-        if (threadIdx.x == 0) plan = q;
-    }
-    __syncthreads();
-    const Product& a = dw ? plan.w : plan.x;
+    Product a;
+    a.s = h.splits[dw];
     if (a.s.parts <= 1 || a.s.full + i >= a.s.tiles) return;
+    const int M = dw ? h.V : head_rows(h);
+    a.MT = (M + TM - 1) / TM;
+    a.NT = (h.d + BN - 1) / BN;
+    a.group.set(dw ? a.NT : GROUP_DX * a.NT);
     Tile t;
     if (dw) place<0>(a, a.s.full + i, t);
     else place<GROUP_DX>(a, a.s.full + i, t);
@@ -812,11 +854,11 @@ void withhold_hook(int mode, TcParams& p) {
 template <int MODE, bool PAIR>
 cudaError_t launch_tc(const CUtensorMap (&m)[5], TcParams& p, int64_t tiles, cudaStream_t st) {
     int units = 0;
-    cudaError_t e = resident<MODE, PAIR>(&units);
+    const cudaError_t e = resident<MODE, PAIR>(&units);
     if (e != cudaSuccess) return e;
-    // (GRAD's tiles are cut for every unit)
     if (MODE <= ZKEEP && tiles < units) units = (int)(tiles > 0 ? tiles : 1);
-    p.units = units;
+    // (the tiles are cut for so many; all products' CTAs are alike, so that is all of them)
+    if (MODE >= GRAD && p.units < units) units = p.units;
     p.limit_ns = wait_limit_ns();
     withhold_hook(MODE <= ZKEEP ? Z : GRAD, p);
     return launch_early(head_tc_kernel<MODE, PAIR>, dim3((unsigned)(units * Shape<PAIR>::CTAS)), THREADS,
@@ -838,6 +880,11 @@ int64_t parts_dw(int64_t rows, int V, int d) {
 
 size_t head_part_bytes(int64_t rows, int V, int d) {
     return (size_t)(parts_dx(rows, V, d) + parts_dw(rows, V, d)) * kTileBytes;
+}
+
+cudaError_t head_tc_rule(int64_t rows, int V, int d, SplitRule* r) {
+    *r = SplitRule{2 * BM, BN, 0, (int)parts_dx(rows, V, d), (int)parts_dw(rows, V, d), 4, 4, 12, 8, 0, 0, 0};
+    return resident<GRAD, true>(&r->units);
 }
 
 // Columns of a tile where W's bytes bound: about equal tiles for whole waves of CTAs.
@@ -874,7 +921,7 @@ cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool
 }
 
 cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
-                                const HeadOut& dW, float* part, int64_t part_rows, cudaStream_t st) {
+                                const HeadOut& dW, float* part, const SplitRule& rule, cudaStream_t st) {
     TcParams p{};
     p.h = h;
     p.dx = dx;
@@ -882,8 +929,8 @@ cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W,
     p.tile_n = BN;
     p.a_rows = BM;
     p.part = part;
-    p.capx = (int)parts_dx(part_rows, h.V, h.d);
-    p.capw = (int)parts_dw(part_rows, h.V, h.d);
+    p.capx = rule.capx;
+    p.units = rule.units;
     // rows that are never made need not be read
     const int64_t made = ((h.T - h.p0 < h.rows ? h.T - h.p0 : h.rows) + 63) / 64 * 64;
     CUtensorMap m[5];
@@ -912,7 +959,7 @@ cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W,
         e = launch_tc<GRAD, true>(m, p, 0, st);
     }
     if (e != cudaSuccess) return e;
-    const int nx = p.capx ? (int)(tx < p.units ? tx : p.units) : 0, nw = p.capw ? (int)(tw % p.units) : 0;
+    const int nx = rule.capx ? (int)(tx < p.units ? tx : p.units) : 0, nw = rule.capw ? (int)(tw % p.units) : 0;
     if (nx + nw == 0) return cudaSuccess;
     const int64_t most = nw || made > 2 * BM ? 2 * BM : made;
     return launch_early(head_join_kernel, dim3((unsigned)(nx + nw), (unsigned)((most + kJoinRows - 1) / kJoinRows)),
