@@ -333,7 +333,15 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
     s = s == 0.f ? 0.f : s * exp2f(m - top);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float lse2 = top + log2f(s);
+    const float base = top + kHeadShift, sum = s * 0x1p-15f;
+    static_assert(kHeadShift == 15.f, "the sums' scale");
+    const float lse2 = base + log2f(sum);
+    // log2 of the sum over a target's exponential: small where the model is sure of it,
+    // and not the difference of two numbers of the logits' size
+    auto above = [&](float z) {
+        const float d = fmaf(z, h.c, -base);
+        return fabsf(d) <= 64.f ? log2f(sum * exp2f(-d)) : log2f(sum) - d;
+    };
     const int t = head_token(h, r);
     if (!h.n_live && !token_live(h, t)) {
         if (lane == 0) {
@@ -348,10 +356,9 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
     float loss = 0.f, g = 0.f;
     int k = -1;
     if (h.target) {
-        const float z = h.lz[at] * h.c;
-        loss = (lse2 - z) * kLn2;
+        loss = above(h.lz[at]) * kLn2;
         k = (int)h.target[t];
-        g = weight * (exp2f(z - lse2) - 1.f);
+        g = weight * expm1f(-loss);
     } else {
         const int e = h.ent[t];
         float gs[MOE_HEAD_MAX_ENTRIES / 32];
@@ -359,14 +366,14 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
         for (int i = 0; i < MOE_HEAD_MAX_ENTRIES / 32; ++i) {
             const int j = i * 32 + lane;
             if (j >= e) break;
-            const float z = h.lz[at + j] * h.c;
+            const float gap = above(h.lz[at + j]);
             float q = h.q[at + j];
-            loss += q * (h.lq[at + j] + (lse2 - z) * kLn2);
+            loss += q * (h.lq[at + j] + gap * kLn2);
             if (h.row) {   // an index that is there more than once has the sum of all
                 const int me = h.sidx[at + j];
                 for (int u = j - 1; u >= 0 && h.sidx[at + u] == me; --u) q += h.q[at + u];
                 for (int u = j + 1; u < e && h.sidx[at + u] == me; ++u) q += h.q[at + u];
-                gs[i] = weight * (exp2f(z - lse2) - q);
+                gs[i] = weight * (exp2f(-gap) - q);
             }
         }
         if (h.row) {   // the entries' values of G, in place of their logits

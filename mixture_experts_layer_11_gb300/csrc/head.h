@@ -18,6 +18,10 @@ constexpr int kHeadRows = 256;
 // block's largest: at most 2^15, so that fp16 holds 11 bits of each down to 2^-29
 // of the block's largest, and 2^-39 of it before it falls to 0.
 constexpr float kHeadShift = 15.f;
+// What a block's exponentials are relative to, m2 - kHeadShift: rounded to a 64th, so
+// that adding kHeadShift is exact, and what a target's logit is above or below it has
+// the bits of the difference and not of the logit.
+__device__ __forceinline__ float head_base(float largest) { return rintf(largest * 64.f) * 0.015625f - kHeadShift; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(TY * TX, BLOCKS)
             v[j] = a + b;
             if (n0 + tx + TX * j < h.V) m = fmaxf(m, v[j]);
         }
-        m = lanes_max<TX>(m) * h.c - kHeadShift;
+        m = head_base(lanes_max<TX>(m) * h.c);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             e[j] = n0 + tx + TX * j < h.V ? exp2f(fmaf(v[j], h.c, -m)) : 0.f;

@@ -39,6 +39,14 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int BOX = 32 * 128;                // an epilogue warp's staged box: 32 rows of 128 bytes
 constexpr int TMEM_COLS = 512;
+// Z of up to 128 rows: the sums leave TMEM every kChunk K blocks (256 products) and are
+// added in registers, rounded to nearest.  The tensor cores drop what is below the
+// accumulator's last bit, which over d = 4096 moves a logit by 4e-6 of itself towards
+// zero; the loss of a lone token that the model is sure of shows it (5e-6 of a loss of
+// 0.36 in place of 4e-5).  W's bytes bound
+// there (13 tokens of 131072 entries, d = 4096: 167 -> 171 us); calls of more rows, whose
+// errors average out, would take 5 to 10% longer, and leave it.
+constexpr int kChunk = 4;
 constexpr int GROUP_Z = 16, GROUP_DX = 8;    // row tiles that share a column tile's operand
 
 enum Mode { Z = 0, ZKEEP = 1, GRAD = 2, DX = 3, DW = 4 };   // GRAD: both of the others
@@ -326,6 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Z: A xc, B W, O P.  GRAD: A G, B W (DX); C G, D xc, O dW (DW).
     using S = Shape<PAIR>;
     constexpr int STAGES = S::STAGES;
+    constexpr bool CUT = MODE <= ZKEEP && !PAIR;   // sums drained every kChunk K blocks
     auto is_dw = [](const Tile& t) { return MODE == DW || (MODE == GRAD && t.dw); };
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base =
@@ -438,17 +447,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int u = unit0; u < units && ok; u += nunits) {
                     const Tile t = get_tile<MODE>(plan, p, u);
                     if (t.nkb == 0) continue;
-                    if (!mbar_wait_bounded(smem_u32(&c.tempty[acc]), acc_phase ^ 1, p.limit_ns, &c.abort_flag)) {
-                        raise_abort(c, p);
-                        break;
-                    }
-                    tc_fence_after();
+                    auto acquire = [&]() {
+                        if (!mbar_wait_bounded(smem_u32(&c.tempty[acc]), acc_phase ^ 1, p.limit_ns, &c.abort_flag)) {
+                            raise_abort(c, p);
+                            return false;
+                        }
+                        tc_fence_after();
+                        return true;
+                    };
+                    auto hand_over = [&]() {
+                        commit<PAIR>(smem_u32(&c.tfull[acc]));
+                        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                    };
+                    if (!acquire()) break;
                     // (a loop for each product: what is issued a stage is constant)
                     auto issue = [&](auto dw) {
                         constexpr bool a_n = decltype(dw)::value, b_n = MODE >= GRAD;
                         const uint32_t idesc = idesc_bf16_f32(S::TILE_M, 0, a_n, b_n) | width;
                         const uint64_t ad0 = a_n ? an : ak, bd0 = b_n ? bn : bk;
                         for (int k = 0; k < t.nkb; ++k) {
+                            if (CUT && k && k % kChunk == 0) {
+                                hand_over();
+                                if (!acquire()) return false;
+                            }
                             if (!mbar_wait_bounded(smem_u32(&c.full[stage]), phase, p.limit_ns, &c.abort_flag)) {
                                 raise_abort(c, p);
                                 return false;
@@ -458,7 +479,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int kk = 0; kk < BK / 16; ++kk)
                                 mma<PAIR>(tmem + acc * BN, ad0 + so + kk * (a_n ? STEP_N : STEP_K),
-                                          bd0 + so + kk * (b_n ? STEP_N : STEP_K), idesc, (k | kk) != 0);
+                                          bd0 + so + kk * (b_n ? STEP_N : STEP_K), idesc,
+                                          ((CUT ? k % kChunk : k) | kk) != 0);
                             commit<PAIR>(smem_u32(&c.empty[stage]));
                             if (++stage == STAGES) { stage = 0; phase ^= 1; }
                         }
@@ -466,8 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     };
                     ok = is_dw(t) ? issue(Flag<true>{}) : issue(Flag<false>{});
                     if (!ok) break;
-                    commit<PAIR>(smem_u32(&c.tfull[acc]));
-                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                    hand_over();
                 }
                 // every MMA issued has completed before TMEM is freed
                 commit_local<PAIR>(smem_u32(&c.drain));
@@ -540,6 +561,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int left = min(width, h.V - col0);   // the warp's columns (maybe none)
                 if (left <= 0) {
                     release();
+                    bool ok = true;
+                    for (int k = kChunk; CUT && k < t.nkb && ok; k += kChunk) {
+                        ok = mbar_wait_warp(smem_u32(&c.tfull[acc]), acc_phase, p.limit_ns, &c.abort_flag);
+                        if (ok) release();
+                    }
+                    if (!ok) {
+                        raise_abort(c, p);
+                        break;
+                    }
                     continue;
                 }
                 float v[4][32];
@@ -548,6 +578,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (ch * 32 < left) tmem_ld32_start(trow + ch * 32, v[ch]);
                 tmem_ld_wait(v);
                 release();
+                if (CUT) {
+                    bool ok = true;
+                    for (int k = kChunk; k < t.nkb && ok; k += kChunk) {
+                        ok = mbar_wait_warp(smem_u32(&c.tfull[acc]), acc_phase, p.limit_ns, &c.abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t more = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + half * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (i * 16 >= left) break;
+                            float w[16];
+                            tmem_ld16(more + i * 16, w);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[i >> 1][(i & 1) * 16 + j] += w[j];
+                        }
+                        release();
+                    }
+                    if (!ok) {
+                        raise_abort(c, p);
+                        break;
+                    }
+                }
                 if (left < 128) {
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch)
@@ -578,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[ch][j]);
-                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * h.c - kHeadShift;
+                const float m = head_base(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * h.c);
                 uint64_t sum[2] = {0, 0};
                 const uint64_t c2 = f2_pack(h.c, h.c), m2 = f2_pack(-m, -m);
 #pragma unroll
