@@ -85,6 +85,29 @@ def test_distill(T, d, V, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [1, 5, 128])
+@pytest.mark.parametrize("T,d,V", [(1, 64, 300), (8, 72, 33), (40, 64, 5000), (64, 264, 1001), (65, 64, 1001),
+                                   (128, 64, 40000), (129, 64, 700), (300, 72, 1025)])
+def test_distill_without_gradients(T, d, V, K, dtype):
+    # up to 64 (fp32) or 128 rows take tiles of other widths, in which rows are tokens
+    x, W, target = make(T, d, V, dtype, seed=K + T)
+    idx, logits = make_entries(T, K, V, target, seed=K, distinct=False)
+    if T > 3:
+        idx[1] = -1                                     # nothing left
+        x[1] = float("nan")
+        idx[2, 0] = -1
+        logits[3, K // 2:] = float("-inf")
+    head = HeadLoss(T, W, entries=K, backward=False)
+    for tau in (1.0, 3.0):
+        want, bound = reference(x, W, idx=idx, logits=logits, temperature=tau)
+        loss, lse, dx, dW = head.distill(x, idx, logits, temperature=tau)
+        assert dx is None and dW is None
+        near("loss", loss, want["loss"], bound["loss"])
+        near("lse", lse, want["lse"], bound["lse"])
+    head.check_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_entries_absent_and_repeated(dtype):
     T, d, V, K = 150, 64, 700, 24
     x, W, target = make(T, d, V, dtype)
@@ -343,6 +366,18 @@ def test_another_stream_and_a_graph():
         near("dW", got[3], w["dW"], e["dW"])
     a.check_status()
     b.check_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_certain_tokens(dtype):
+    # a vocabulary of one, and targets far above all others: losses of 0, not below
+    for V, boost in ((1, 1.0), (200, 400.0)):
+        x, W, target = make(150, 64, V, dtype, boost=0.0)
+        x = (x.float() + boost * W[target].float()).to(dtype)
+        loss, _, dx, dW = HeadLoss(150, W).cross_entropy(x, target)
+        assert (loss >= 0).all() and float(loss.max()) <= 1e-5
+        assert float(dx.float().abs().max()) <= 1e-5
+        assert (HeadLoss(60, W, backward=False).score(x[:60], target[:60])[0] >= 0).all()
 
 
 def test_weights_changed_in_place_take_effect():
