@@ -80,6 +80,8 @@
  *                           runs out, it writes MOE_ERR_TIMEOUT to *dev_status,
  *                           drains what it issued, frees its tensor memory and
  *                           exits.  The call's outputs are then incomplete.
+ *  MOE_DEBUG_HEAD_WITHHOLD  "m:u:kb", the same for the products of moe_head_*
+ *                           in bf16: m 0 the logits, 2 the gradients.
  */
 #ifndef MOE_H_
 #define MOE_H_

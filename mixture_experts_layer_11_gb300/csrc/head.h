@@ -15,7 +15,7 @@ constexpr int kHeadBlock = 128;
 // Rows of the compacted hidden states and of the probabilities are padded to this.
 constexpr int kHeadRows = 256;
 // Exponentials are kept as 2^(z2 - m2 + kHeadShift), z2 the logit in bits, m2 the
-// block's largest: at most 2^15, so that fp16 holds 11 bits of each down to 2^-29
+// block's largest (to a 128th): at most 2^15.01, so that fp16 holds 11 bits of each down to 2^-29
 // of the block's largest, and 2^-39 of it before it falls to 0.
 constexpr float kHeadShift = 15.f;
 // What a block's exponentials are relative to, m2 - kHeadShift: rounded to a 64th, so
@@ -71,7 +71,7 @@ struct HeadDev {
     int T, V, d, K;
     int Vp;                  // row length of P (V rounded up to 64)
     int nblk;                // blocks of kHeadBlock entries
-    int nstat;               // rows of stats: nblk, or for few rows two a CTA (fp32: blocks of 64)
+    int nstat;               // rows of stats: nblk, or for few rows two a CTA (fp32: tiles of 64)
     int p0, rows;            // first live row of the piece, its most rows
     int srows;               // row length of stats (rows, rounded up to kHeadRows)
     const int* n_live;       // null: rows are tokens, all T of them

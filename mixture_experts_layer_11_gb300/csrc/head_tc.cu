@@ -20,6 +20,14 @@
 // to the workspace in fp32 and are added in order by head_join_kernel.  The number
 // of live tokens, and with it tiles and parts, is read on the device.
 //
+// What bounds, and times: the tensor pipe in DX and DW (94 and 90 % busy; 5734 rows of
+// 50257 entries, d = 768: 241 and 251 us, 1800 TFLOP/s) and in Z with long rows (8191
+// rows, d = 2048, no exponentials kept: 1290 us, 1700 TFLOP/s; the power cap sets the
+// clock).  ZKEEP at d = 768 takes 290 us, 68 % busy: the exponentials' way out through
+// shared memory meets the MMAs' operands there (without it 248).  Up to 128 tokens W's
+// bytes bound: 13 tokens of 131072 entries, d = 4096, 164 us, 6.5 TB/s; one token of
+// 50257, d = 768, 17 us, half of it before the first and after the last load.
+//
 // Every wait is bounded; on expiry the CTA records MOE_ERR_TIMEOUT, waits for its
 // copies and MMAs in flight, frees TMEM and exits.
 #include <cudaTypedefs.h>
@@ -42,10 +50,10 @@ constexpr int TMEM_COLS = 512;
 // Z of up to 128 rows: the sums leave TMEM every kChunk K blocks (256 products) and are
 // added in registers, rounded to nearest.  The tensor cores drop what is below the
 // accumulator's last bit, which over d = 4096 moves a logit by 4e-6 of itself towards
-// zero; the loss of a lone token that the model is sure of shows it (5e-6 of a loss of
-// 0.36 in place of 4e-5).  W's bytes bound
-// there (13 tokens of 131072 entries, d = 4096: 167 -> 171 us); calls of more rows, whose
-// errors average out, would take 5 to 10% longer, and leave it.
+// zero; the loss of a lone token that the model is sure of shows it (1.2e-6 of a loss of
+// 0.36 in place of 4e-5).  W's bytes bound there (13 tokens of 131072 entries, d = 4096:
+// 167 -> 171 us); calls of more rows, whose errors average out, would take 5 to 10 %
+// longer, and leave it.
 constexpr int kChunk = 4;
 constexpr int GROUP_Z = 16, GROUP_DX = 8;    // row tiles that share a column tile's operand
 
