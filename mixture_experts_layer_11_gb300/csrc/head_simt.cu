@@ -14,7 +14,7 @@
 // sums are the more exact ones, too (dx over 8009 entries 8e-7 off in place of 2e-6).
 // 875 rows of 8009 entries, d = 768: Z 265 us (41 TFLOP/s, FMA pipe 61 % busy), DX and DW
 // together 371 (58 TFLOP/s, 77 %), joining 14.  33 rows of 32000: 57 us, FMA pipe 55 %.
-// 256 rows of 1000, d = 64: 8 and 8 us, latency.
+// 256 rows of 1000, d = 64: 8 and 14 us, latency.
 #include "head.h"
 
 namespace moe {
@@ -242,35 +242,18 @@ template <int MODE> struct Loaders {
     static constexpr int SIZE = A::SIZE + B::SIZE;
 };
 
+// The sums of a tile over K values k0 to k1: [row][pair of columns].
 template <int MODE>
-__device__ __forceinline__ void product(const SimtParams& p, int u, float* smem_raw) {
+__device__ __forceinline__ void tile_sums(const SimtParams& p, const Shape<MODE>& sh, int m0, int n0, int k0, int k1,
+                                          float* smem_raw, uint64_t (&acc)[8][4]) {
     using LA = typename Loaders<MODE>::A;
     using LB = typename Loaders<MODE>::B;
     float(*smem)[Loaders<MODE>::SIZE] = reinterpret_cast<float(*)[Loaders<MODE>::SIZE]>(smem_raw);
     const HeadDev& h = p.h;
-    const HeadOut& o = MODE == DX ? p.dx : p.dW;
-    const Shape<MODE> sh = shape_of<MODE>(h);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const Split plan = h.splits[MODE == DW];
-    const int rem = plan.tiles - plan.full;
-    int tile = u, k0 = 0, k1 = sh.K, slot = -1;
-    if (plan.parts > 1 && u >= plan.full) {
-        const int v = u - plan.full, part = v / rem;
-        if (part >= plan.parts) return;
-        tile = plan.full + v % rem;
-        k0 = part * plan.kbp * KB;
-        k1 = min(k1, k0 + plan.kbp * KB);
-        slot = (MODE == DX ? 0 : p.capx) + (tile - plan.full) * plan.parts + part;
-    } else if (u >= plan.tiles) {
-        return;
-    }
-    int mt, nt;
-    tile_at<MODE>(sh, tile, mt, nt);
-    const int m0 = mt * BM, n0 = nt * BN;
     const LA la((const float*)h.P, h.Vp, m0, sh.M, tid);
     const LB lb(MODE == DX ? p.W : p.xc, h.d, n0, sh.N, tid);
 
-    uint64_t acc[8][4];   // [row][pair of columns]
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -328,6 +311,32 @@ __device__ __forceinline__ void product(const SimtParams& p, int u, float* smem_
         }
         if (++cur == STAGES) cur = 0;
     }
+}
+
+template <int MODE>
+__device__ __forceinline__ void product(const SimtParams& p, int u, float* smem) {
+    const HeadDev& h = p.h;
+    const HeadOut& o = MODE == DX ? p.dx : p.dW;
+    const Shape<MODE> sh = shape_of<MODE>(h);
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const Split plan = h.splits[MODE == DW];
+    const int rem = plan.tiles - plan.full;
+    int tile = u, k0 = 0, k1 = sh.K, slot = -1;
+    if (plan.parts > 1 && u >= plan.full) {
+        const int v = u - plan.full, part = v / rem;
+        if (part >= plan.parts) return;
+        tile = plan.full + v % rem;
+        k0 = part * plan.kbp * KB;
+        k1 = min(k1, k0 + plan.kbp * KB);
+        slot = (MODE == DX ? 0 : p.capx) + (tile - plan.full) * plan.parts + part;
+    } else if (u >= plan.tiles) {
+        return;
+    }
+    int mt, nt;
+    tile_at<MODE>(sh, tile, mt, nt);
+    const int m0 = mt * BM, n0 = nt * BN;
+    uint64_t acc[8][4];
+    tile_sums<MODE>(p, sh, m0, n0, k0, k1, smem, acc);
 
     const float scale = head_scale(h);
 #pragma unroll
@@ -357,6 +366,91 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_grad_kernel(c
     wait_front();
     if ((int)blockIdx.x < p.ux) product<DX>(p, blockIdx.x, smem);
     else product<DW>(p, blockIdx.x - p.ux, smem);
+}
+
+// Small products: a cluster of eight blocks a tile, each an eighth of the reduction.  The
+// sums meet in shared memory, each block adds eight rows of them in order: no part goes
+// to the workspace, and no launch joins (256 rows of 1000 entries, d = 64: 14 us in place
+// of 16, the call 32 in place of 35).
+constexpr int kCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float4 load_from(uint32_t addr, int rank) {
+    uint32_t there;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(there)
+                 : "memory");
+    return v;
+}
+
+template <int MODE>
+__device__ __forceinline__ void cluster_product(const SimtParams& p, int tile, float* smem) {
+    const HeadDev& h = p.h;
+    const HeadOut& o = MODE == DX ? p.dx : p.dW;
+    const Shape<MODE> sh = shape_of<MODE>(h);
+    // (the same for all blocks of a cluster)
+    if (tile >= sh.MT * sh.NT || (MODE == DW && sh.K == 0 && o.accumulate)) return;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, rank = (int)cluster_rank();
+    int mt, nt;
+    tile_at<MODE>(sh, tile, mt, nt);
+    const int m0 = mt * BM, n0 = nt * BN;
+    const int share = ((sh.K + BK - 1) / BK + kCluster - 1) / kCluster * BK;
+    const int k0 = min(sh.K, rank * share), k1 = min(sh.K, k0 + share);
+    uint64_t acc[8][4];
+    tile_sums<MODE>(p, sh, m0, n0, k0, k1, smem, acc);
+    copies_wait<0>();
+    __syncthreads();   // the steps' memory is free
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float* row = smem + (MODE == DX ? ty + 8 * i : ty * 8 + i) * BN + tx * 4;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+            float4 v;
+            f2_unpack(acc[i][2 * jj], v.x, v.y);
+            f2_unpack(acc[i][2 * jj + 1], v.z, v.w);
+            *reinterpret_cast<float4*>(row + jj * 64) = v;
+        }
+    }
+    cluster_sync();
+    constexpr int ROWS = BM / kCluster;
+    const float scale = head_scale(h);
+#pragma unroll
+    for (int i = 0; i < ROWS * BN / 4 / THREADS; ++i) {
+        const int g = tid + i * THREADS, rl = rank * ROWS + g / (BN / 4), c = g % (BN / 4) * 4, r = m0 + rl;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < kCluster; ++q) {
+            const float4 v = load_from(smem_u32(smem + rl * BN + c), q);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        if (r < sh.M && n0 + c < sh.N)
+            write4<MODE>(o, (float*)o.out + (int64_t)(MODE == DX ? head_token(h, r) : r) * h.d + n0 + c,
+                         make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale));
+    }
+    cluster_sync();   // no block ends while others read its sums
+}
+
+__global__ void __launch_bounds__(THREADS) head_simt_cluster_kernel(const __grid_constant__ SimtParams p) {
+    constexpr int SIZE = Loaders<DX>::SIZE > Loaders<DW>::SIZE ? Loaders<DX>::SIZE : Loaders<DW>::SIZE;
+    static_assert(STAGES * SIZE >= BM * BN, "a tile's sums fit the steps' memory");
+    __shared__ __align__(16) float smem[STAGES * SIZE];
+    wait_front();
+    const int tile = blockIdx.x / kCluster;
+    if (tile < p.ux) cluster_product<DX>(p, tile, smem);
+    else cluster_product<DW>(p, tile - p.ux, smem);
 }
 
 // The parts of cut tiles, added in order.
@@ -458,6 +552,11 @@ cudaError_t launch_head_simt_grad(const HeadDev& h, const void* xc, const void* 
     // workspace holds)
     const int64_t rows = h.T - h.p0 < h.rows ? h.T - h.p0 : h.rows;
     const int64_t tx = dx.out ? tiles_of(rows, h.d) : 0, tw = dW.out ? tiles_of(h.V, h.d) : 0;
+    if ((tx + tw) * kCluster <= rule.units) {   // all clusters run at once
+        p.ux = (int)tx;
+        if (tx + tw == 0) return cudaSuccess;
+        return launch_early(head_simt_cluster_kernel, dim3((unsigned)((tx + tw) * kCluster)), THREADS, 0, kCluster, st, p);
+    }
     p.ux = (int)(tx ? tx + rule.capx : 0);
     const int64_t blocks = p.ux + (tw ? tw + rule.capw : 0);
     if (blocks == 0) return cudaSuccess;
