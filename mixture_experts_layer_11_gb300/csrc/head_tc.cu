@@ -55,7 +55,13 @@ constexpr int TMEM_COLS = 512;
 // 167 -> 171 us); calls of more rows, whose errors average out, would take 5 to 10 %
 // longer, and leave it.
 constexpr int kChunk = 4;
-constexpr int GROUP_Z = 16, GROUP_DX = 8;    // row tiles that share a column tile's operand
+// Row tiles that follow each other on one column tile's operand, as a power of two: DX's 8;
+// Z's as many as keep their rows of x, 512 d bytes a tile, within 32 MB of the second-level
+// cache.  Losses of 8191 rows of 65536 entries, d = 2048: 1234 us by 32, 1253 by 16; of
+// 16384 rows of 32768 entries, d = 4096: 2645 us by 32, 2523 by 16, 2657 by 8; of 16384
+// entries, d = 8192: 2834 us by 16, 2783 by 8.
+constexpr int DX_SHIFT = 3;
+__device__ __forceinline__ int z_shift(int d) { return d <= 2048 ? 5 : d <= 4096 ? 4 : 3; }
 
 enum Mode { Z = 0, ZKEEP = 1, GRAD = 2, DX = 3, DW = 4 };   // GRAD: both of the others
 
@@ -90,7 +96,7 @@ struct Quotient {
 // A product's tiles, their split, K blocks and units.
 struct Product {
     Split s;
-    int MT, NT, kb;
+    int MT, NT, kb, shift;
     Quotient group, rest;   // of tiles; of cut ones
     __device__ __forceinline__ int units() const { return s.full + (s.tiles - s.full) * s.parts; }
 };
@@ -133,7 +139,8 @@ template <int MODE, bool PAIR> __device__ __forceinline__ Plan make_plan(const T
         q.x.NT = (h.V + p.tile_n - 1) / p.tile_n;
         q.x.kb = (h.d + BK - 1) / BK;
         q.x.s = Split{q.x.MT * q.x.NT, q.x.MT * q.x.NT, 1, q.x.kb};
-        q.x.group.set(GROUP_Z * q.x.NT);
+        q.x.shift = z_shift(h.d);
+        q.x.group.set(q.x.NT << q.x.shift);
         return q;
     }
     q.x.NT = q.w.NT = (h.d + BN - 1) / BN;
@@ -143,7 +150,8 @@ template <int MODE, bool PAIR> __device__ __forceinline__ Plan make_plan(const T
     q.x.s = q.w.s = Split{0, 0, 1, 0};
     if (p.dx.out) q.x.s = h.splits[0];
     if (p.dW.out) q.w.s = h.splits[1];
-    q.x.group.set(GROUP_DX * q.x.NT);
+    q.x.shift = DX_SHIFT;
+    q.x.group.set(q.x.NT << DX_SHIFT);
     q.w.group.set(q.w.NT);
     q.x.rest.set(q.x.s.tiles - q.x.s.full);
     q.w.rest.set(q.w.s.tiles - q.w.s.full);
@@ -152,26 +160,25 @@ template <int MODE, bool PAIR> __device__ __forceinline__ Plan make_plan(const T
 
 struct Tile { int mt, nt, kb0, nkb, slot; bool dw; };   // slot: of a part, else -1
 
-// Where tile i of a product lies: GROUP row tiles share a column tile's operand; DW's
+// Where tile i of a product lies: 2^shift row tiles share a column tile's operand; DW's
 // columns follow each other (they share G's).
-template <int GROUP> __device__ __forceinline__ void place(const Product& a, int i, Tile& t) {
-    if (GROUP == 0) {
+template <bool DWS> __device__ __forceinline__ void place(const Product& a, int i, Tile& t) {
+    if (DWS) {
         t.mt = a.group.of(i, t.nt);
         return;
     }
-    constexpr int G = GROUP > 0 ? GROUP : 1;
     int l;
-    const int g = a.group.of(i, l), gm = min(G, a.MT - g * G);
-    if (gm == G) {
-        t.mt = g * G + l % G;
-        t.nt = l / G;
+    const int g = a.group.of(i, l), first = g << a.shift, gm = min(1 << a.shift, a.MT - first);
+    if (gm == 1 << a.shift) {
+        t.mt = first + (l & (gm - 1));
+        t.nt = l >> a.shift;
     } else {
-        t.mt = g * G + l % gm;
+        t.mt = first + l % gm;
         t.nt = l / gm;
     }
 }
 
-template <int GROUP> __device__ __forceinline__ Tile product_tile(const Product& a, int u, int slot0) {
+template <bool DWS> __device__ __forceinline__ Tile product_tile(const Product& a, int u, int slot0) {
     Tile t;
     t.kb0 = 0;
     t.nkb = a.kb;
@@ -186,20 +193,20 @@ template <int GROUP> __device__ __forceinline__ Tile product_tile(const Product&
         t.nkb = min(a.s.kbp, a.kb - t.kb0);
         t.slot = slot0 + left * a.s.parts + part;
     }
-    place<GROUP>(a, i, t);
+    place<DWS>(a, i, t);
     return t;
 }
 template <int MODE> __device__ __forceinline__ Tile get_tile(const Plan& q, const TcParams& p, int u) {
     Tile t;
     if (MODE <= ZKEEP) {
-        t = product_tile<GROUP_Z>(q.x, u, 0);
+        t = product_tile<false>(q.x, u, 0);
         t.dw = false;
         return t;
     }
     const int ux = MODE == DW ? 0 : q.x.units();
     t.dw = MODE == DW || (MODE == GRAD && u >= ux);
     const bool dw = t.dw;
-    t = dw ? product_tile<0>(q.w, u - ux, p.capx) : product_tile<GROUP_DX>(q.x, u, 0);
+    t = dw ? product_tile<true>(q.w, u - ux, p.capx) : product_tile<false>(q.x, u, 0);
     t.dw = dw;
     return t;
 }
@@ -798,10 +805,11 @@ __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ 
     const int M = dw ? h.V : head_rows(h);
     a.MT = (M + TM - 1) / TM;
     a.NT = (h.d + BN - 1) / BN;
-    a.group.set(dw ? a.NT : GROUP_DX * a.NT);
+    a.shift = DX_SHIFT;
+    a.group.set(dw ? a.NT : a.NT << DX_SHIFT);
     Tile t;
-    if (dw) place<0>(a, a.s.full + i, t);
-    else place<GROUP_DX>(a, a.s.full + i, t);
+    if (dw) place<true>(a, a.s.full + i, t);
+    else place<false>(a, a.s.full + i, t);
     const float scale = head_scale(h);
     const int rl = blockIdx.y * kJoinRows, r0 = t.mt * TM + rl, rows = M - r0;
     if (rows <= 0) return;
