@@ -25,10 +25,10 @@ from . import ops
 class HeadLoss:
     """Parameters: T the most tokens of one call; W [V,d] the head, bf16 or fp32,
     contiguous, d a multiple of 8, read at every call, so that weights updated in
-    place take effect; entries the most of a teacher's list a token (1 to
+    place, or given other memory, take effect; entries the most of a teacher's list a token (1 to
     ops.HEAD_MAX_ENTRIES); backward False for scores alone.  With backward: want_dx,
     want_dW which gradients; dW [V,d] the buffer for the head's (W's type or fp32),
-    None for one of W's type made here; piece the tokens whose probabilities are held
+    whose memory is bound here, None for one of W's type made here; piece the tokens whose probabilities are held
     at a time (0: as many as 2 GiB hold); more are worked on in rounds.
 
     The results, the workspace and the status word are this object's, on the head's
@@ -79,7 +79,7 @@ class HeadLoss:
         self._device = self.loss.device.index
         self._results = (self.loss, self.lse, self.dx, self.dW)
         self._size = (T, d)
-        self._W = W.data_ptr()
+        self._shape = W.shape
         self._losses = (self.loss.data_ptr(), self.lse.data_ptr())
         self._owned = (self.ws.data_ptr(), self.status.data_ptr())
 
@@ -134,8 +134,11 @@ class HeadLoss:
         if size != self._size and (len(size) != 2 or size[1] != d or size[0] > self.T):
             raise ValueError(f"x is {tuple(size)}, expected [t, {d}] with t <= {self.T}")
         t, lists = size[0], idx.shape
-        if lists[0] != t or (logits is None and len(lists) != 1):
+        if (lists != (t,)) if logits is None else (lists[0] != t):
             raise ValueError(f"targets are {tuple(lists)} for {t} tokens")
+        if self.W.shape != self._shape:
+            raise ValueError(f"W is {tuple(self.W.shape)} now, was {tuple(self._shape)}")
+        self._on_device("W", self.W)
         self._on_device("x", x)
         self._on_device("targets", idx)
         h = self.head
@@ -159,9 +162,9 @@ class HeadLoss:
     def _launch(self, x, idx, logits, temperature, grad):
         stream = ops.raw_stream(self._device)
         if logits is None:
-            ops.moe_head_ce(self.head, x, self._W, idx, *self._losses, grad, *self._owned, stream=stream)
+            ops.moe_head_ce(self.head, x, self.W, idx, *self._losses, grad, *self._owned, stream=stream)
         else:
-            ops.moe_head_distill(self.head, x, self._W, idx, logits, temperature, *self._losses, grad,
+            ops.moe_head_distill(self.head, x, self.W, idx, logits, temperature, *self._losses, grad,
                                  *self._owned, stream=stream)
 
     def check_status(self):

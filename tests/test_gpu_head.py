@@ -386,3 +386,14 @@ def test_weights_changed_in_place_take_effect():
     check(head, x, target)
     W.mul_(-1.5)
     check(head, x, target)
+
+
+def test_weights_given_other_memory_take_effect():
+    x, W, target = make(64, 64, 300, BF16)
+    head = HeadLoss(64, W)
+    check(head, x, target)
+    W.data = W.data * -1.5
+    check(head, x, target)
+    with pytest.raises(ops.MoEError, match="dtype"):
+        W.data = W.data.float()
+        head.score(x, target)

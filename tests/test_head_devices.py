@@ -67,6 +67,7 @@ def test_refuses_inputs_on_another_device(gpus, name):
     lambda h, a: h.score(Tensor(0, 32), a["target"]),
     lambda h, a: h.score(a["x"], Tensor(0, 3, dtype=I64)),
     lambda h, a: h.score(a["x"], Tensor(0, 4, 1, dtype=I64)),
+    lambda h, a: h.score(a["x"], Tensor(0, dtype=I64)),
     lambda h, a: h.cross_entropy(a["x"], a["target"], weight=Tensor(0, 3)),
     lambda h, a: h.distill(a["x"], a["idx"], Tensor(0, 4, 2)),
     lambda h, a: h.distill(a["x"], Tensor(0, 4, 4, dtype=I64), Tensor(0, 4, 4)),  # more entries
@@ -79,6 +80,18 @@ def test_refuses_what_does_not_fit(gpus, call):
     head = HeadLoss(4, Tensor(0, 20, 8, dtype=torch.bfloat16), entries=3)
     with pytest.raises(ValueError):
         call(head, tensors(0))
+    assert gpus.calls == []
+
+
+def test_a_head_given_another_shape_or_device_is_refused(gpus):
+    head = HeadLoss(4, Tensor(0, 20, 8), entries=3)
+    a = tensors(0)
+    head.W = Tensor(0, 10, 16)
+    with pytest.raises(ValueError, match="W is"):
+        head.score(a["x"], a["target"])
+    head.W = Tensor(1, 20, 8)
+    with pytest.raises(ops.MoEError, match="W on cuda:1"):
+        head.score(a["x"], a["target"])
     assert gpus.calls == []
 
 
