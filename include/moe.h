@@ -524,8 +524,8 @@ MOE_API size_t moe_head_workspace_size(const moe_head* h, const moe_head_grad* g
  * The launches may overlap the end of the kernel before them in the stream; they touch
  * memory only when that kernel has completed.
  * Precision: products are summed in fp32 (bf16: by the tensor cores, which drop
- * what is below the accumulator's last bit: 4e-6 of a logit at d = 4096 and 2e-6 of a
- * loss; with up to 128 tokens the sums of every 256 products are rounded to nearest),
+ * what is below the accumulator's last bit; a logit's sums of 256 products, with more
+ * than 128 tokens of up to 1536, are added rounded to nearest: losses to 1e-6 of their norm),
  * softmax statistics, losses and the entries' own logits are fp32.  bf16
  * gradients: weight[t] G is rounded to bf16 once, before the products with W and x;
  * scale and the mean are applied to their fp32 sums; dx and dW are rounded once.

@@ -22,8 +22,8 @@
 //
 // What bounds, and times: the tensor pipe in DX and DW (94 and 90 % busy; 5734 rows of
 // 50257 entries, d = 768: 241 and 251 us, 1800 TFLOP/s) and in Z with long rows (8191
-// rows, d = 2048, no exponentials kept: 1290 us, 1700 TFLOP/s; the power cap sets the
-// clock).  ZKEEP at d = 768 takes 290 us, 68 % busy: the exponentials' way out through
+// rows, d = 2048, no exponentials kept: 1225 us, 1800 TFLOP/s; the power cap sets the
+// clock).  ZKEEP at d = 768 takes 280 us, 73 % busy: the exponentials' way out through
 // shared memory meets the MMAs' operands there (without it 248).  Up to 128 tokens W's
 // bytes bound: 13 tokens of 131072 entries, d = 4096, 164 us, 6.5 TB/s; one token of
 // 50257, d = 768, 17 us, half of it before the first and after the last load.
@@ -47,14 +47,23 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int BOX = 32 * 128;                // an epilogue warp's staged box: 32 rows of 128 bytes
 constexpr int TMEM_COLS = 512;
-// Z of up to 128 rows: the sums leave TMEM every kChunk K blocks (256 products) and are
-// added in registers, rounded to nearest.  The tensor cores drop what is below the
-// accumulator's last bit, which over d = 4096 moves a logit by 4e-6 of itself towards
-// zero; the loss of a lone token that the model is sure of shows it (1.2e-6 of a loss of
-// 0.36 in place of 4e-5).  W's bytes bound there (13 tokens of 131072 entries, d = 4096:
-// 167 -> 171 us); calls of more rows, whose errors average out, would take 5 to 10 %
-// longer, and leave it.
-constexpr int kChunk = 4;
+// Z's sums leave TMEM in chunks of K blocks and are added in registers, rounded to
+// nearest.  The tensor cores drop what is below the accumulator's last bit, which in one
+// chain over d = 4096 moves a logit by 4e-6 of itself towards zero.
+//   up to 128 rows  every kChunk blocks (256 products): the loss of a lone token that the
+//             model is sure of shows it (1.2e-6 of a loss of 0.36 in place of 4e-5), and
+//             W's bytes bound (13 tokens of 131072 entries, d = 4096: 167 -> 171 us)
+//   more      rows longer than kWhole blocks in about equal chunks of 13 to 24: losses
+//             are off by 5e-7 of their norm in place of 2e-6 at d = 4096 and 1.1e-6 at
+//             2048 (8191 rows of 65536 entries, d = 2048: 1237 -> 1248 us; 16384 of
+//             32768, d = 4096: 2551 -> 2601).  Chunks of 8 blocks took 5 to 10 % longer:
+//             the MMAs of two have to cover an epilogue.  Shorter rows stay whole (8.5e-7
+//             at d = 1536).
+constexpr int kChunk = 4, kWhole = 24;
+__device__ __forceinline__ int z_chunk(int kb) {
+    const int n = kb <= kWhole ? 1 : (kb + 7) / 16;
+    return (kb + n - 1) / n;
+}
 // Row tiles that follow each other on one column tile's operand, as a power of two: DX's 8;
 // Z's as many as keep their rows of x, 512 d bytes a tile, within 32 MB of the second-level
 // cache.  Losses of 8191 rows of 65536 entries, d = 2048: 1234 us by 32, 1253 by 16; of
@@ -96,7 +105,7 @@ struct Quotient {
 // A product's tiles, their split, K blocks and units.
 struct Product {
     Split s;
-    int MT, NT, kb, shift;
+    int MT, NT, kb, shift, chunk;
     Quotient group, rest;   // of tiles; of cut ones
     __device__ __forceinline__ int units() const { return s.full + (s.tiles - s.full) * s.parts; }
 };
@@ -140,6 +149,7 @@ template <int MODE, bool PAIR> __device__ __forceinline__ Plan make_plan(const T
         q.x.kb = (h.d + BK - 1) / BK;
         q.x.s = Split{q.x.MT * q.x.NT, q.x.MT * q.x.NT, 1, q.x.kb};
         q.x.shift = z_shift(h.d);
+        q.x.chunk = PAIR ? z_chunk(q.x.kb) : kChunk;
         q.x.group.set(q.x.NT << q.x.shift);
         return q;
     }
@@ -341,7 +351,8 @@ __device__ __forceinline__ uint32_t bf2_bits(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int MODE, bool PAIR>
+// CUT (Z, ZKEEP): a tile's sums leave TMEM every plan.x.chunk K blocks
+template <int MODE, bool PAIR, bool CUT>
 __global__ void __launch_bounds__(THREADS, 1)
     head_tc_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                    const __grid_constant__ CUtensorMap mapC, const __grid_constant__ CUtensorMap mapD,
@@ -349,7 +360,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Z: A xc, B W, O P.  GRAD: A G, B W (DX); C G, D xc, O dW (DW).
     using S = Shape<PAIR>;
     constexpr int STAGES = S::STAGES;
-    constexpr bool CUT = MODE <= ZKEEP && !PAIR;   // sums drained every kChunk K blocks
     auto is_dw = [](const Tile& t) { return MODE == DW || (MODE == GRAD && t.dw); };
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base =
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = c.tmem_base;
     const Plan& plan = c.plan;
-    const int units = plan.x.units() + plan.w.units();
+    const int units = plan.x.units() + plan.w.units(), chunk = plan.x.chunk;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -474,17 +484,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         commit<PAIR>(smem_u32(&c.tfull[acc]));
                         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                     };
-                    if (!acquire()) break;
                     // (a loop for each product: what is issued a stage is constant)
-                    auto issue = [&](auto dw) {
+                    auto issue = [&](auto dw, int nkb) {
                         constexpr bool a_n = decltype(dw)::value, b_n = MODE >= GRAD;
                         const uint32_t idesc = idesc_bf16_f32(S::TILE_M, 0, a_n, b_n) | width;
                         const uint64_t ad0 = a_n ? an : ak, bd0 = b_n ? bn : bk;
-                        for (int k = 0; k < t.nkb; ++k) {
-                            if (CUT && k && k % kChunk == 0) {
-                                hand_over();
-                                if (!acquire()) return false;
-                            }
+                        for (int k = 0; k < nkb; ++k) {
                             if (!mbar_wait_bounded(smem_u32(&c.full[stage]), phase, p.limit_ns, &c.abort_flag)) {
                                 raise_abort(c, p);
                                 return false;
@@ -494,16 +499,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int kk = 0; kk < BK / 16; ++kk)
                                 mma<PAIR>(tmem + acc * BN, ad0 + so + kk * (a_n ? STEP_N : STEP_K),
-                                          bd0 + so + kk * (b_n ? STEP_N : STEP_K), idesc,
-                                          ((CUT ? k % kChunk : k) | kk) != 0);
+                                          bd0 + so + kk * (b_n ? STEP_N : STEP_K), idesc, (k | kk) != 0);
                             commit<PAIR>(smem_u32(&c.empty[stage]));
                             if (++stage == STAGES) { stage = 0; phase ^= 1; }
                         }
                         return true;
                     };
-                    ok = is_dw(t) ? issue(Flag<true>{}) : issue(Flag<false>{});
-                    if (!ok) break;
-                    hand_over();
+                    const int most = CUT ? chunk : t.nkb;
+                    for (int k = 0; k < t.nkb && ok; k += most) {
+                        const int nkb = min(most, t.nkb - k);
+                        ok = acquire() && (is_dw(t) ? issue(Flag<true>{}, nkb) : issue(Flag<false>{}, nkb));
+                        if (ok) hand_over();
+                    }
                 }
                 // every MMA issued has completed before TMEM is freed
                 commit_local<PAIR>(smem_u32(&c.drain));
@@ -577,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (left <= 0) {
                     release();
                     bool ok = true;
-                    for (int k = kChunk; CUT && k < t.nkb && ok; k += kChunk) {
+                    for (int k = chunk; CUT && k < t.nkb && ok; k += chunk) {
                         ok = mbar_wait_warp(smem_u32(&c.tfull[acc]), acc_phase, p.limit_ns, &c.abort_flag);
                         if (ok) release();
                     }
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 release();
                 if (CUT) {
                     bool ok = true;
-                    for (int k = kChunk; k < t.nkb && ok; k += kChunk) {
+                    for (int k = chunk; k < t.nkb && ok; k += chunk) {
                         ok = mbar_wait_warp(smem_u32(&c.tfull[acc]), acc_phase, p.limit_ns, &c.abort_flag);
                         if (!ok) break;
                         tc_fence_after();
@@ -872,7 +879,7 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
 // CTAs or pairs that run at once on the current device.
-template <int MODE, bool PAIR> cudaError_t resident(int* units) {
+template <int MODE, bool PAIR, bool CUT> cudaError_t resident(int* units) {
     static std::mutex mu;
     static int of[64] = {};
     int dev = 0;
@@ -881,7 +888,7 @@ template <int MODE, bool PAIR> cudaError_t resident(int* units) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (of[dev] == 0) {
-        auto kern = head_tc_kernel<MODE, PAIR>;
+        auto kern = head_tc_kernel<MODE, PAIR, CUT>;
         constexpr size_t SMEM = smem_bytes<PAIR>();
         static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
@@ -919,17 +926,17 @@ void withhold_hook(int mode, TcParams& p) {
     p.withhold_kb = k;
 }
 
-template <int MODE, bool PAIR>
+template <int MODE, bool PAIR, bool CUT>
 cudaError_t launch_tc(const CUtensorMap (&m)[5], TcParams& p, int64_t tiles, cudaStream_t st) {
     int units = 0;
-    const cudaError_t e = resident<MODE, PAIR>(&units);
+    const cudaError_t e = resident<MODE, PAIR, CUT>(&units);
     if (e != cudaSuccess) return e;
     if (MODE <= ZKEEP && tiles < units) units = (int)(tiles > 0 ? tiles : 1);
     // (the tiles are cut for so many; all products' CTAs are alike, so that is all of them)
     if (MODE >= GRAD && p.units < units) units = p.units;
     p.limit_ns = wait_limit_ns();
     withhold_hook(MODE <= ZKEEP ? Z : GRAD, p);
-    return launch_early(head_tc_kernel<MODE, PAIR>, dim3((unsigned)(units * Shape<PAIR>::CTAS)), THREADS,
+    return launch_early(head_tc_kernel<MODE, PAIR, CUT>, dim3((unsigned)(units * Shape<PAIR>::CTAS)), THREADS,
                         smem_bytes<PAIR>(), Shape<PAIR>::CTAS, st, m[0], m[1], m[2], m[3], m[4], p);
 }
 
@@ -952,7 +959,7 @@ size_t head_part_bytes(int64_t rows, int V, int d) {
 
 cudaError_t head_tc_rule(int64_t rows, int V, int d, SplitRule* r) {
     *r = SplitRule{2 * BM, BN, 0, (int)parts_dx(rows, V, d), (int)parts_dw(rows, V, d), 4, 4, 12, 8, 0, 0, 0};
-    return resident<GRAD, true>(&r->units);
+    return resident<GRAD, true, false>(&r->units);
 }
 
 // Columns of a tile where W's bytes bound: about equal tiles for whole waves of CTAs.
@@ -984,8 +991,10 @@ cudaError_t launch_head_tc(const HeadDev& h, const void* xc, const void* W, bool
     if (keep && !make_map(&m[4], h.P, h.Vp, h.srows, h.Vp, 32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
         return cudaErrorInvalidValue;
     const int64_t tiles = tiles_of(single ? BM : h.rows, single ? BM : 2 * BM, h.V, p.tile_n);
-    if (single) return keep ? launch_tc<ZKEEP, false>(m, p, tiles, st) : launch_tc<Z, false>(m, p, tiles, st);
-    return keep ? launch_tc<ZKEEP, true>(m, p, tiles, st) : launch_tc<Z, true>(m, p, tiles, st);
+    if (single) return keep ? launch_tc<ZKEEP, false, true>(m, p, tiles, st) : launch_tc<Z, false, true>(m, p, tiles, st);
+    if (h.d > kWhole * BK)
+        return keep ? launch_tc<ZKEEP, true, true>(m, p, tiles, st) : launch_tc<Z, true, true>(m, p, tiles, st);
+    return keep ? launch_tc<ZKEEP, true, false>(m, p, tiles, st) : launch_tc<Z, true, false>(m, p, tiles, st);
 }
 
 cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W, const HeadOut& dx,
@@ -1017,14 +1026,14 @@ cudaError_t launch_head_tc_grad(const HeadDev& h, const void* xc, const void* W,
     cudaError_t e;
     if (apart && tx && tw) {
         p.dW.out = nullptr;
-        e = launch_tc<DX, true>(m, p, 0, st);
+        e = launch_tc<DX, true, false>(m, p, 0, st);
         if (e != cudaSuccess) return e;
         p.dW = dW;
         p.dx.out = nullptr;
-        e = launch_tc<DW, true>(m, p, 0, st);
+        e = launch_tc<DW, true, false>(m, p, 0, st);
         p.dx = dx;
     } else {
-        e = launch_tc<GRAD, true>(m, p, 0, st);
+        e = launch_tc<GRAD, true, false>(m, p, 0, st);
     }
     if (e != cudaSuccess) return e;
     const int nx = rule.capx ? (int)(tx < p.units ? tx : p.units) : 0, nw = rule.capw ? (int)(tw % p.units) : 0;
