@@ -397,3 +397,19 @@ def test_weights_given_other_memory_take_effect():
     with pytest.raises(ops.MoEError, match="dtype"):
         W.data = W.data.float()
         head.score(x, target)
+
+
+@pytest.mark.parametrize("T,d,V", [(129, 1536, 640), (300, 1544, 300), (257, 1600, 1000), (400, 2560, 129),
+                                   (1000, 2568, 9000), (200, 4104, 20000)])
+def test_long_rows(T, d, V):
+    # around the lengths from which sums leave the tensor cores in chunks, of which the
+    # last may be short; column tiles of which half the warps have none
+    x, W, target = make(T, d, V, BF16, seed=d)
+    target[::5] = -1
+    check(HeadLoss(T, W), x, target, mean=True)
+    want, bound = reference(x, W, target)
+    head = HeadLoss(T, W, backward=False)
+    loss, lse = head.score(x, target)
+    near("loss", loss, want["loss"], bound["loss"])
+    near("lse", lse, want["lse"], bound["lse"])
+    head.check_status()

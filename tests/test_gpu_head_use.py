@@ -171,14 +171,14 @@ def test_tensors_the_library_cannot_check_are_refused():
     head.check_status()
 
 
-@pytest.mark.parametrize("T", [100, 600])
-@pytest.mark.parametrize("hook", ["0:0:1", "0:1:0", "2:0:1", "2:1:0"])
-def test_waits_that_run_out(T, hook, monkeypatch):
+@pytest.mark.parametrize("T,d,hook", [(T, 192, hook) for T in (100, 600) for hook in ("0:0:1", "0:1:0", "2:0:1", "2:1:0")]
+                         + [(300, 2048, "0:0:20"), (300, 2048, "0:1:3")])
+def test_waits_that_run_out(T, d, hook, monkeypatch):
     """With MOE_DEBUG_HEAD_WITHHOLD the producer of one unit issues nothing from a K
     block on (no copy is left in flight for it): the waits on that stage run out after
     1 s, the CTA waits for its copies, frees tensor memory and reports.  Afterwards the
     same call gives the same bits as before."""
-    x, W, target = make(T, 192, 1500, BF16)
+    x, W, target = make(T, d, 1500, BF16)
     head = HeadLoss(T, W)
     good = [v.clone() for v in head.cross_entropy(x, target)]
     head.check_status()
