@@ -508,9 +508,9 @@ typedef struct {
     int32_t accumulate;   /* 1: dW is added to (fp32 only), 0: overwritten */
 } moe_head_grad;
 
-/* Bytes of workspace for one call, and for any with fewer tokens; g as in the
- * call (its pointers say only what is wanted), NULL for the losses alone.  0 for
- * arguments that the calls refuse. */
+/* Bytes of workspace for one call, and for any with fewer tokens or entries, or
+ * without gradients; g as in the call (its pointers say only what is wanted), NULL
+ * for the losses alone.  0 for arguments that the calls refuse. */
 MOE_API size_t moe_head_workspace_size(const moe_head* h, const moe_head_grad* g);
 
 /*   x       [T,d] dtype       W  [V,d] dtype

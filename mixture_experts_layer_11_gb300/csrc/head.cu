@@ -505,8 +505,11 @@ __global__ void __launch_bounds__(256) head_round_kernel(const float4* in, uint2
 
 }  // namespace
 
+// What is made for a call with gradients is used by ones without them too (an object's
+// scores): these take other rounds, and gather up to kPieceRows rows whatever the piece.
 size_t head_workspace(const moe_head& h, const moe_head_grad* g) {
-    return make_plan(h, g, true).total;
+    const size_t with = make_plan(h, g, true).total, alone = make_plan(h, nullptr, true).total;
+    return with > alone ? with : alone;
 }
 
 cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {

@@ -29,7 +29,9 @@ class HeadLoss:
     ops.HEAD_MAX_ENTRIES); backward False for scores alone.  With backward: want_dx,
     want_dW which gradients; dW [V,d] the buffer for the head's (W's type or fp32),
     whose memory is bound here, None for one of W's type made here; piece the tokens whose probabilities are held
-    at a time (0: as many as 2 GiB hold); more are worked on in rounds.
+    at a time (0: as many as 2 GiB hold); more are worked on in rounds.  Scores hold
+    no probabilities, but up to 65536 rows of x: an object with a small piece has a
+    workspace for them too.
 
     The results, the workspace and the status word are this object's, on the head's
     device, whichever is current: calls of one object run in order on one stream
