@@ -1,10 +1,11 @@
 // head.cu -- losses over a vocabulary head: cross entropy and distillation from a
 // teacher's top logits, with the gradients of the hidden states and the head.
 //
-// With z the logits over the temperature in bits (times log2 e) and blocks b of
-// 128 vocabulary entries, the first product's epilogue leaves, a row,
-//   m_b = max z - 15,  s_b = sum 2^(z - m_b)   and   E = 2^(z - m_b)
-// so that  lse = m + log2(sum_b s_b 2^(m_b - m)),  p = E 2^(m_b - lse).  E has 16
+// With z the logits, c = log2(e) / temperature and blocks b of 128 vocabulary entries,
+// the first product's epilogue leaves, a row,
+//   m_b = max z,  s_b = sum E   and   E = 2^(c (z - m_b) + 15)
+// so that, with m = max m_b and S = sum_b s_b 2^(c (m_b - m)),
+//   lse = m / temperature + log(S / 2^15),  p = E 2^(c (m_b - m)) / S.  E has 16
 // bits (fp16: 11 of precision, 2^-12 at most off), a piece of rows at a time; the
 // logits are not kept.  head_gradient_kernel turns E into the gradients
 //   G = w (p - q)
@@ -316,10 +317,10 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
                 if (v[i].y == 0.f) continue;   // no entries
                 // (NaN: the comparison fails, and the sum takes it on)
                 if (v[i].x > m) {
-                    s = s * exp2f(m - v[i].x) + v[i].y;
+                    s = s * exp2f((m - v[i].x) * h.c) + v[i].y;
                     m = v[i].x;
                 } else {
-                    s += v[i].y * exp2f(v[i].x - m);
+                    s += v[i].y * exp2f((v[i].x - m) * h.c);
                 }
             }
         }
@@ -336,16 +337,16 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // (a share without blocks has m = -inf and s = 0)
-    s = s == 0.f ? 0.f : s * exp2f(m - top);
+    s = s == 0.f ? 0.f : s * exp2f((m - top) * h.c);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float base = top + kHeadShift, sum = s * 0x1p-15f;
+    const float sum = s * 0x1p-15f;
     static_assert(kHeadShift == 15.f, "the sums' scale");
-    const float lse2 = base + log2f(sum);
+    const float lse = fmaf(top, h.per, logf(sum));
     // log2 of the sum over a target's exponential: small where the model is sure of it,
     // and not the difference of two numbers of the logits' size
     auto above = [&](float z) {
-        const float d = fmaf(z, h.c, -base);
+        const float d = (z - top) * h.c;
         return fabsf(d) <= 64.f ? log2f(sum * exp2f(-d)) : log2f(sum) - d;
     };
     const int t = head_token(h, r);
@@ -393,10 +394,10 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
         loss *= h.loss_scale;
     }
     if (lane == 0) {
-        if (!isfinite(loss) || !isfinite(lse2)) report(h.status, MOE_ERR_NONFINITE);
+        if (!isfinite(loss) || !isfinite(lse)) report(h.status, MOE_ERR_NONFINITE);
         h.loss[t] = loss;
-        if (h.lse) h.lse[t] = lse2 * kLn2;
-        if (h.row) h.row[r] = make_float4(lse2, weight, __int_as_float(k), g);
+        if (h.lse) h.lse[t] = lse;
+        if (h.row) h.row[r] = make_float4(top, weight / s, __int_as_float(k), g);
     }
 }
 
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(32 * kGradWarps)
         for (int i = 0; i < LOADS; ++i)
             if (c + i * 32 * N < h.Vp)
                 *reinterpret_cast<uint4*>(row + c + i * 32 * N) =
-                    Pair<T>::scale(v[i], info.y * exp2f(m[i] - info.x), h.V - c - i * 32 * N);
+                    Pair<T>::scale(v[i], info.y * exp2f((m[i] - info.x) * h.c), h.V - c - i * 32 * N);
     }
     __syncwarp();
     // the targets' own values
@@ -554,6 +555,7 @@ cudaError_t launch_head(const HeadCall& c, cudaStream_t st) {
     h.P = ws + p.P;
     h.splits = (Split*)(ws + p.ctl + 64);
     h.c = kLog2e / c.temperature;
+    h.per = 1.f / c.temperature;
     h.loss_scale = c.temperature * c.temperature;
     if (g) {
         h.weight = g->weight;

@@ -14,14 +14,13 @@ namespace moe {
 constexpr int kHeadBlock = 128;
 // Rows of the compacted hidden states and of the probabilities are padded to this.
 constexpr int kHeadRows = 256;
-// Exponentials are kept as 2^(z2 - m2 + kHeadShift), z2 the logit in bits, m2 the
-// block's largest (to a 128th): at most 2^15.01, so that fp16 holds 11 bits of each down to 2^-29
-// of the block's largest, and 2^-39 of it before it falls to 0.
+// Exponentials are kept as 2^(c (z - m) + kHeadShift), z the logit, m the block's
+// largest, c = log2(e) / temperature: at most 2^15, so that fp16 holds 11 bits of each
+// down to 2^-29 of the block's largest, and 2^-39 of it before it falls to 0.  The
+// differences come first, of logits and not of logits times c: what is between two logits
+// of any size has the bits of the difference (from one fused c z - m, with lse as one
+// number, p is 3e-4 of itself off where the logits reach 1e4 bits, and infinite from 2^24).
 constexpr float kHeadShift = 15.f;
-// What a block's exponentials are relative to, m2 - kHeadShift: rounded to a 64th, so
-// that adding kHeadShift is exact, and what a target's logit is above or below it has
-// the bits of the difference and not of the logit.
-__device__ __forceinline__ float head_base(float largest) { return rintf(largest * 64.f) * 0.015625f - kHeadShift; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -83,13 +82,14 @@ struct HeadDev {
     const int* ent;          // entries present [T]
     const uint8_t* start;    // first entry of each block [T][nblk]
     float* lz;               // logits of the targets / entries [T][K]
-    float2* stats;           // [nstat][srows]: largest exponent - kHeadShift, sum (0: no entries)
-    float4* row;             // [srows], with gradients: log2 of the sum of exponentials,
-                             // weight, and the target with its value of G (CE)
+    float2* stats;           // [nstat][srows]: largest logit, sum of exponentials (0: no entries)
+    float4* row;             // [srows], with gradients: largest logit, weight over the sum of
+                             // exponentials, and the target with its value of G (CE)
     Split* splits;           // DX's, DW's (head_gradient_kernel works them out)
     void* P;                 // [rows][Vp]: exponentials, then gradients by the logits
     const float* weight;
     float c;                 // log2(e) / temperature
+    float per;               // 1 / temperature
     float loss_scale;        // temperature^2
     float grad_scale;        // scale * temperature
     int mean;

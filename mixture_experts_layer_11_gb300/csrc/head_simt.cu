@@ -169,10 +169,10 @@ __global__ void __launch_bounds__(TY * TX, BLOCKS)
             v[j] = a + b;
             if (n0 + tx + TX * j < h.V) m = fmaxf(m, v[j]);
         }
-        m = head_base(lanes_max<TX>(m) * h.c);
+        m = lanes_max<TX>(m);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            e[j] = n0 + tx + TX * j < h.V ? exp2f(fmaf(v[j], h.c, -m)) : 0.f;
+            e[j] = n0 + tx + TX * j < h.V ? exp2f(fmaf(v[j] - m, h.c, kHeadShift)) : 0.f;
             sum += e[j];
         }
         sum = lanes_sum<TX>(sum);

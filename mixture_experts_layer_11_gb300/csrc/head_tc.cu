@@ -652,15 +652,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[ch][j]);
-                const float m = head_base(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * h.c);
+                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 uint64_t sum[2] = {0, 0};
-                const uint64_t c2 = f2_pack(h.c, h.c), m2 = f2_pack(-m, -m);
+                const uint64_t c2 = f2_pack(h.c, h.c), m2 = f2_pack(-m, -m), s2 = f2_pack(kHeadShift, kHeadShift);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         float a, b;
-                        f2_unpack(f2_fma(f2_pack(v[ch][j], v[ch][j + 1]), c2, m2), a, b);
+                        f2_unpack(f2_fma(f2_add(f2_pack(v[ch][j], v[ch][j + 1]), m2), c2, s2), a, b);
                         a = ex2_approx(a);
                         b = ex2_approx(b);
                         sum[(j >> 1) & 1] = f2_add(sum[(j >> 1) & 1], f2_pack(a, b));
@@ -673,10 +673,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (p.few) {
                     // (NaN: the comparison fails, and the sum takes it on)
                     if (m > few_m) {
-                        few_s = few_s == 0.f ? sa : few_s * ex2_approx(few_m - m) + sa;
+                        few_s = few_s == 0.f ? sa : few_s * ex2_approx((few_m - m) * h.c) + sa;
                         few_m = m;
                     } else {
-                        few_s += sa * ex2_approx(m - few_m);
+                        few_s += sa * ex2_approx((m - few_m) * h.c);
                     }
                 } else if (r < n) {
                     h.stats[(int64_t)(col0 / kHeadBlock) * h.srows + r] = make_float2(m, sa);
