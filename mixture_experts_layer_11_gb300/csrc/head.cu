@@ -377,9 +377,8 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const HeadDev h) {
             const float gap = above(h.lz[at + j]);
             float q = h.q[at + j];
             loss += q * (h.lq[at + j] + gap * kLn2);
-            if (h.row) {   // an index that is there more than once has the sum of all
+            if (h.row) {   // an index that is there more than once: its first entry has the sum of all
                 const int me = h.sidx[at + j];
-                for (int u = j - 1; u >= 0 && h.sidx[at + u] == me; --u) q += h.q[at + u];
                 for (int u = j + 1; u < e && h.sidx[at + u] == me; ++u) q += h.q[at + u];
                 gs[i] = weight * (exp2f(-gap) - q);
             }
@@ -489,7 +488,8 @@ __global__ void __launch_bounds__(32 * kGradWarps)
     } else {
         for (int j = a + lane; j < b; j += 32) {
             const int k = h.sidx[at + j];
-            if (k >= c0 && k < c0 + kGradCols) row[k] = from_f32<T>(h.lz[at + j]);
+            const bool first = j == 0 || h.sidx[at + j - 1] != k;   // of the same index
+            if (first && k >= c0 && k < c0 + kGradCols) row[k] = from_f32<T>(h.lz[at + j]);
         }
     }
 }
