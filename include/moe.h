@@ -517,7 +517,8 @@ MOE_API size_t moe_head_workspace_size(const moe_head* h, const moe_head_grad* g
  *   target  [T] int64
  *   (outputs and ws overlap neither the inputs nor one another)
  *   loss    [T] fp32, out     lse  [T] fp32, out, or NULL
- *   g       gradients, or NULL: the losses alone (scores of given tokens)
+ *   g       gradients, or NULL: the losses alone (scores of given tokens; a g that
+ *           wants neither gives them too, at the cost of holding the probabilities)
  *   ws      workspace (contents need no initialisation, garbage after)
  *   dev_status  MOE_ERR_NONFINITE on a loss that is not finite, MOE_ERR_INVALID
  *           on an index of V or more, MOE_ERR_TIMEOUT

@@ -27,7 +27,7 @@ class HeadLoss:
     contiguous, d a multiple of 8, read at every call, so that weights updated in
     place, or given other memory, take effect; entries the most of a teacher's list a token (1 to
     ops.HEAD_MAX_ENTRIES); backward False for scores alone.  With backward: want_dx,
-    want_dW which gradients; dW [V,d] the buffer for the head's (W's type or fp32),
+    want_dW which gradients (neither: the calls are scores); dW [V,d] the buffer for the head's (W's type or fp32),
     whose memory is bound here, None for one of W's type made here; piece the tokens whose probabilities are held
     at a time (0: as many as 2 GiB hold); more are worked on in rounds.  Scores hold
     no probabilities, but up to 65536 rows of x: an object with a small piece has a
@@ -69,7 +69,9 @@ class HeadLoss:
                 self.dx = torch.empty(T, d, dtype=W.dtype, device=dev)
             if want_dW:
                 self.dW = torch.empty_like(W) if dW is None else dW
-            self.grad = ops.make_head_grad(self.dx, self.dW, W.dtype)
+            if want_dx or want_dW:
+                self.grad = ops.make_head_grad(self.dx, self.dW, W.dtype)
+        self._backward = bool(backward)
         with torch.cuda.device(dev):
             n = ops.moe_head_workspace_size(self.head, self.grad)
         if n == 0:
@@ -109,11 +111,11 @@ class HeadLoss:
             raise ValueError(f"idx is {tuple(idx.shape)}, logits {tuple(logits.shape)}")
         if not 1 <= idx.shape[1] <= self.entries:
             raise ValueError(f"{idx.shape[1]} entries, expected 1 to {self.entries}")
-        g = None if self.grad is None else self._grad(x, weight, scale, mean, accumulate)
+        g = self._grad(x, weight, scale, mean, accumulate) if self._backward else None
         return self._call(x, idx, logits, temperature, g)
 
     def _grad(self, x, weight, scale, mean, accumulate):
-        if self.grad is None:
+        if not self._backward:
             raise ValueError("gradients of an object made with backward=False")
         if weight is not None:
             if tuple(weight.shape) != (x.shape[0],):
@@ -122,7 +124,10 @@ class HeadLoss:
         g = self.grad
         if accumulate and self.dW is not None and self.dW.dtype != torch.float32:
             raise ValueError(f"accumulate takes a float32 dW, this one is {self.dW.dtype}")
-        g.weight = ops._ptr(weight, torch.float32)
+        address = ops._ptr(weight, torch.float32)
+        if g is None:
+            return None
+        g.weight = address
         g.scale, g.mean, g.accumulate = float(scale), int(bool(mean)), int(bool(accumulate))
         return g
 
