@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) head_simt_grad_kernel(c
 // Small products: a cluster of eight blocks a tile, each an eighth of the reduction.  The
 // sums meet in shared memory, each block adds eight rows of them in order: no part goes
 // to the workspace, and no launch joins (256 rows of 1000 entries, d = 64: 14 us in place
-// of 16, the call 32 in place of 35).
+// of 16 and the join's launch; the call takes 36).
 constexpr int kCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {

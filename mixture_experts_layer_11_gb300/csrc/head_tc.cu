@@ -22,9 +22,10 @@
 //
 // What bounds, and times: the tensor pipe in DX and DW (94 and 90 % busy; 5734 rows of
 // 50257 entries, d = 768: 241 and 251 us, 1800 TFLOP/s) and in Z with long rows (8191
-// rows, d = 2048, no exponentials kept: 1225 us, 1800 TFLOP/s; the power cap sets the
-// clock).  ZKEEP at d = 768 takes 280 us, 73 % busy: the exponentials' way out through
-// shared memory meets the MMAs' operands there (without it 248).  Up to 128 tokens W's
+// rows, d = 2048, no exponentials kept: 1230 us, 1790 TFLOP/s; the power cap sets the
+// clock).  ZKEEP at d = 768 takes 287 us, about 71 % busy: the exponentials' way out through
+// shared memory meets the MMAs' operands there (without it 248), and taking a block's
+// largest logit off before the temperature costs 6 of the 287.  Up to 128 tokens W's
 // bytes bound: 13 tokens of 131072 entries, d = 4096, 164 us, 6.5 TB/s; one token of
 // 50257, d = 768, 17 us, half of it before the first and after the last load.
 //
@@ -53,7 +54,7 @@ constexpr int TMEM_COLS = 512;
 //   up to 128 rows  every kChunk blocks (256 products): the loss of a lone token that the
 //             model is sure of shows it (1.2e-6 of a loss of 0.36 in place of 4e-5), and
 //             W's bytes bound (13 tokens of 131072 entries, d = 4096: 167 -> 171 us)
-//   more      rows longer than kWhole blocks in about equal chunks of 13 to 24: losses
+//   more      rows longer than kWhole blocks in about equal chunks of 13 to 20: losses
 //             are off by 5e-7 of their norm in place of 2e-6 at d = 4096 and 1.1e-6 at
 //             2048 (8191 rows of 65536 entries, d = 2048: 1237 -> 1248 us; 16384 of
 //             32768, d = 4096: 2551 -> 2601).  Chunks of 8 blocks took 5 to 10 % longer:
